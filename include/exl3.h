@@ -61,7 +61,7 @@ enum {
     EXL3_EUNSUPPORTED = -5   /* K or Hadamard block not supported */
 };
 
-enum { EXL3_F32 = 0, EXL3_BF16 = 1 };              /* weight storage type */
+enum { EXL3_F32 = 0, EXL3_BF16 = 1, EXL3_F16 = 2 };  /* storage types (weights: F32, BF16; activations: BF16, F16) */
 enum { EXL3_ROW_MAJOR = 0, EXL3_TILE_MAJOR = 1 };  /* layout of regularized output */
 
 typedef struct exl3_ctx exl3_ctx;
@@ -390,6 +390,108 @@ int exl3_quantize_matrix_ldlq(exl3_ctx *ctx, const void *w, int w_dtype, int row
                               uint16_t *packed, float *scale_out, double *mse_out, float *w_hat,
                               float *tile_err);
 
+/*
+ * ---- Products with coded weights ----
+ *
+ * A matrix held as the container exl3_quantize_matrix writes, for products with
+ * activations.  W = diag(su) H_l (scale * level[state]) H_r diag(sv), the
+ * dequantized matrix of exl3_decode_tiles and exl3_unregularize: `rows` are its
+ * output channels, `cols` its inputs.  `groups` matrices of one shape (experts)
+ * lie one after the other in every array; a single matrix has groups = 1.  The
+ * level table and the within-tile order are the context's at the call.
+ *   packed  uint16 [groups][rows/16][cols/16][16*K], 4-byte aligned
+ *   scale   float [groups]
+ *   su, sv  float [groups][rows], float [groups][cols]: any finite values (the
+ *           signs, or folded as by exl3_channel_normalize)
+ * K in 1..8 (5..8, a table set by exl3_set_codebook and a within-tile order
+ * other than the natural one take a slower general decoder); had_block 64 or
+ * 128; rows and cols positive multiples of had_block, at most 2^20; groups 1 ..
+ * 65535.  All pointers are device pointers, the struct itself is host memory.
+ */
+typedef struct {
+    const uint16_t *packed;
+    const float *scale;
+    const float *su;
+    const float *sv;
+    int groups, rows, cols, K, had_block;
+} exl3_weight;
+
+/*
+ * y = x W^T (transpose == 0), or y = x W (transpose != 0: the gradient with
+ * respect to x of the former, from the gradient with respect to y).
+ *   x      [n][in] 16-bit elements of `dtype` (EXL3_BF16 or EXL3_F16), rows ldx
+ *          elements apart; in = cols, or rows when transposed
+ *   y      [n][out] of the same type, rows ldy elements apart; out = the other
+ *          side.  x and y share no element.
+ * Products are summed in binary32 and rounded once to the type of y.  Few rows
+ * (not transposed) are multiplied by the levels themselves, with the
+ * transformed activations in binary16 under a power-of-two scale for each 256
+ * columns; many rows by W rounded to the type of x.  A row of x with a NaN or
+ * an infinity gives a row of y without finite values; other rows are not
+ * affected.  n may be 0; at most 2^24 rows.
+ * Asynchronous.  The context's workspace grows on demand: to capture the call
+ * in a graph, make a call with the same arguments on the same stream first
+ * (a growth during capture is refused with EXL3_ENOMEM).  Workspaces are kept
+ * until the context is destroyed, so a captured graph stays valid until then.
+ * Errors: EXL3_EINVAL, EXL3_EUNSUPPORTED, EXL3_ENOMEM (also when one dense
+ * matrix does not fit the context's scratch bound), EXL3_EHIP.
+ */
+int exl3_linear(exl3_ctx *ctx, const exl3_weight *w, int transpose, const void *x, int64_t ldx,
+                int64_t n, int dtype, void *y, int64_t ldy);
+
+/*
+ * The same with a matrix per group (expert): rows offsets[e] .. offsets[e+1]-1
+ * of x are multiplied by matrix e.
+ *   offsets  int32 [groups + 1], device: ascending, within 0..n.  Rows before
+ *            the first or from the last offset on belong to no group and give
+ *            rows of zeros.  Offsets that descend or leave 0..n give unspecified
+ *            rows, but the call stays memory-safe.
+ * The sizes of the groups stay on the device.  Errors: as exl3_linear.
+ */
+int exl3_grouped_linear(exl3_ctx *ctx, const exl3_weight *w, const int32_t *offsets, int transpose,
+                        const void *x, int64_t ldx, int64_t n, int dtype, void *y, int64_t ldy);
+
+/*
+ * Low-rank adapters beside a coded matrix: `count` adapters of one rank.
+ *   a      [count][rank][cols] in the activations' type
+ *   b      [count][rows][rank] in the activations' type
+ *   alpha  float [count]
+ * rank in 1..128 (adapters of smaller ranks: rows of zeros); count 1..65535.
+ */
+typedef struct {
+    const void *a;
+    const void *b;
+    const float *alpha;
+    int count, rank;
+} exl3_adapters;
+
+/*
+ * y_t = x_t W^T + alpha_a (x_t A_a^T) B_a^T with a = ids[t], for rows of many
+ * requests at once, each with its adapter.
+ *   ids    int32 [n], device: the row's adapter, or -1 for none (any value
+ *          outside 0..count-1 is none)
+ * W has groups = 1.  alpha (x A^T) is rounded to the activations' type; an
+ * adapter's values reach no row of another.  Otherwise as exl3_linear.
+ */
+int exl3_adapter_linear(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters *ad,
+                        const int32_t *ids, const void *x, int64_t ldx, int64_t n, int dtype,
+                        void *y, int64_t ldy);
+
+/*
+ * Gradients of exl3_adapter_linear for a given dy [n][rows] (W is frozen):
+ *   dx_t = dy_t W + alpha_a (dy_t B_a) A_a
+ *   da_a = sum over the rows t of adapter a of alpha_a (dy_t B_a)^T x_t
+ *   db_a = sum over the rows t of adapter a of dy_t^T (alpha_a x_t A_a^T)
+ *   dx   [n][cols], rows lddx apart, or null;  da, db  as a and b, or null
+ * Written whole (zero for adapters without rows), in the activations' type; the
+ * sums over rows are binary32, in an order that does not depend on scheduling.
+ * x is read for da and db only.  Errors: as exl3_linear.
+ */
+int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters *ad,
+                                 const int32_t *ids, const void *dy, int64_t lddy, const void *x,
+                                 int64_t ldx, int64_t n, int dtype, void *dx, int64_t lddx,
+                                 void *da, void *db);
+
 /* Kernel kinds for exl3_ctx_read_timing. */
 enum {
     EXL3_KERNEL_FWD1 = 0,        /* forward pass 1 (rotated input, free start) */
@@ -404,7 +506,10 @@ enum {
     EXL3_KERNEL_FWD_COST = 6,    /* pass 2's cost-only form (scale-search probes,
                                     on the context's stream) */
     EXL3_KERNEL_CHANNEL = 7,     /* out-channel normalization (tile count 0) */
-    EXL3_KERNEL_DECODE = 8       /* exl3_decode_tiles */
+    EXL3_KERNEL_DECODE = 8,      /* exl3_decode_tiles */
+    EXL3_KERNEL_PRODUCT = 9      /* products with coded weights (one record a
+                                    call, its launches together; tiles: the
+                                    weights' tiles) */
 };
 
 /*

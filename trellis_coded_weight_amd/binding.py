@@ -23,6 +23,7 @@ EXL3_EHIP = -4
 EXL3_EUNSUPPORTED = -5
 EXL3_F32 = 0
 EXL3_BF16 = 1
+EXL3_F16 = 2
 EXL3_ROW_MAJOR = 0
 EXL3_TILE_MAJOR = 1
 
@@ -35,10 +36,11 @@ EXPORTED = [
     "exl3_encode_tiles_f16", "exl3_decode_tiles", "exl3_quantize_matrix",
     "exl3_quantize_matrix_ldlq", "exl3_quantize_matrix_grid", "exl3_quantize_matrix_f16", "exl3_scratch_per_tile",
     "exl3_ctx_set_timing", "exl3_ctx_read_timing",
+    "exl3_linear", "exl3_grouped_linear", "exl3_adapter_linear", "exl3_adapter_linear_backward",
 ]
 CODEBOOK_KINDS = {"mul1": 0, "mcg": 1, "3inst": 2}
 KERNEL_KINDS = {"fwd1": 0, "fwd2": 1, "tb1": 2, "tb2": 3, "regularize": 4, "fwd_side": 5,
-                "fwd_cost": 6, "channel": 7, "decode": 8}
+                "fwd_cost": 6, "channel": 7, "decode": 8, "product": 9}
 
 
 class Exl3Error(RuntimeError):
@@ -57,6 +59,17 @@ class Grid(ctypes.Structure):
                 ("coarse_step", ctypes.c_double), ("stride", ctypes.c_int),
                 ("fine_radius", ctypes.c_double), ("fine_step", ctypes.c_double),
                 ("floor", ctypes.c_double)]
+
+
+class _Weight(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("su", ctypes.c_void_p),
+                ("sv", ctypes.c_void_p), ("groups", ctypes.c_int), ("rows", ctypes.c_int),
+                ("cols", ctypes.c_int), ("K", ctypes.c_int), ("had_block", ctypes.c_int)]
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("alpha", ctypes.c_void_p),
+                ("count", ctypes.c_int), ("rank", ctypes.c_int)]
 
 
 GRID_PAGES = (0.1, 1.9, 0.1, 2, 0.075, 0.025, 0.01)
@@ -136,6 +149,16 @@ def load_library():
     lib.exl3_ctx_read_timing.restype = i32
     lib.exl3_ctx_read_timing.argtypes = [vp, i32, ctypes.POINTER(f64), ctypes.POINTER(i64),
                                          ctypes.POINTER(i64)]
+    wp, ap = ctypes.POINTER(_Weight), ctypes.POINTER(_Adapters)
+    lib.exl3_linear.restype = i32
+    lib.exl3_linear.argtypes = [vp, wp, i32, vp, i64, i64, i32, vp, i64]
+    lib.exl3_grouped_linear.restype = i32
+    lib.exl3_grouped_linear.argtypes = [vp, wp, vp, i32, vp, i64, i64, i32, vp, i64]
+    lib.exl3_adapter_linear.restype = i32
+    lib.exl3_adapter_linear.argtypes = [vp, wp, ap, vp, vp, i64, i64, i32, vp, i64]
+    lib.exl3_adapter_linear_backward.restype = i32
+    lib.exl3_adapter_linear_backward.argtypes = [vp, wp, ap, vp, vp, i64, vp, i64, i64, i32, vp,
+                                                 i64, vp, vp]
     _lib = lib
     return lib
 
@@ -157,6 +180,93 @@ def _need(t: torch.Tensor, dtype, shape, name):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+
+
+class CodedWeight:
+    """A coded matrix, or one per group (expert), as the products take it: the container of
+    quantize_matrix, its scale and the vectors su [rows] and sv [cols] (signs, or folded).
+    W = diag(su) H (scale * levels) H diag(sv), rows the output channels.
+
+    packed  int16 [rows/16, cols/16, 16K], or [groups, ...]
+    scale   a number, or float32 [groups] on the device
+    su, sv  float32 [rows] and [cols], or [groups, ...]
+
+    The tensors are kept, not copied: in-place changes to them show in later products."""
+
+    def __init__(self, packed: torch.Tensor, K: int, scale, su: torch.Tensor, sv: torch.Tensor,
+                 had_block: int = 128):
+        if not isinstance(packed, torch.Tensor) or packed.dim() not in (3, 4):
+            raise ValueError("packed must be a tensor [rows/16, cols/16, 16K] or [groups, ...]")
+        self.grouped = packed.dim() == 4
+        lead = tuple(packed.shape[:-3])
+        groups = packed.shape[0] if self.grouped else 1
+        rows, cols = 16 * packed.shape[-3], 16 * packed.shape[-2]
+        _need(packed, torch.int16, lead + (rows // 16, cols // 16, 16 * int(K)), "packed")
+        if not isinstance(scale, torch.Tensor):
+            scale = torch.full((groups,), float(scale), dtype=torch.float32, device=packed.device)
+        scale = scale.reshape(-1)
+        if su.numel() == groups * rows:
+            su = su.reshape(lead + (rows,))
+        if sv.numel() == groups * cols:
+            sv = sv.reshape(lead + (cols,))
+        _need(scale, torch.float32, (groups,), "scale")
+        _need(su, torch.float32, lead + (rows,), "su")
+        _need(sv, torch.float32, lead + (cols,), "sv")
+        self.packed, self.scale, self.su, self.sv = packed, scale, su, sv
+        self.groups, self.rows, self.cols = groups, rows, cols
+        self.K, self.had_block, self.device = int(K), int(had_block), packed.device
+        self._c = _Weight(packed.data_ptr(), scale.data_ptr(), su.data_ptr(), sv.data_ptr(),
+                          groups, rows, cols, self.K, self.had_block)
+        self._ref = ctypes.byref(self._c)
+
+
+class Adapters:
+    """Low-rank adapters of one rank beside a coded matrix: A [count, rank, cols] and
+    B [count, rows, rank] in the activations' type, alpha float32 [count]."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, alpha: torch.Tensor):
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError("A must be [count, rank, cols] and B [count, rows, rank]")
+        count, rank, cols = A.shape
+        if A.dtype not in _ACT:
+            raise ValueError("A must be bfloat16 or float16, got %s" % A.dtype)
+        _need(A, A.dtype, (count, rank, cols), "A")
+        _need(B, A.dtype, (count, B.shape[1], rank), "B")
+        _need(alpha, torch.float32, (count,), "alpha")
+        self.A, self.B, self.alpha = A, B, alpha
+        self.count, self.rank, self.cols, self.rows = count, rank, cols, B.shape[1]
+        self.dtype, self.device = A.dtype, A.device
+        self._c = _Adapters(A.data_ptr(), B.data_ptr(), alpha.data_ptr(), count, rank)
+        self._ref = ctypes.byref(self._c)
+
+
+_ACT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
+
+
+def _act_rows(t: torch.Tensor, width: int, name: str):
+    """(tensor, row pitch) of activations [n, width]; a tensor whose rows are not of
+    consecutive elements is copied."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dtype not in _ACT:
+        raise ValueError("%s must be bfloat16 or float16, got %s" % (name, t.dtype))
+    if t.dim() != 2 or t.shape[1] != width:
+        raise ValueError("%s must have shape (n, %d), got %s" % (name, width, tuple(t.shape)))
+    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < width):
+        t = t.contiguous()
+    return t, t.stride(0) if t.shape[0] > 1 else width
+
+
+def _out_rows(out: Optional[torch.Tensor], n: int, width: int, like: torch.Tensor, name: str):
+    """(tensor, row pitch) of the output: `out` if given, else a new one."""
+    if out is None:
+        return torch.empty(n, width, dtype=like.dtype, device=like.device), width
+    if not isinstance(out, torch.Tensor) or out.device != like.device or out.dtype != like.dtype:
+        raise ValueError("%s must be a %s tensor on %s" % (name, like.dtype, like.device))
+    if tuple(out.shape) != (n, width) or out.stride(1) != 1 or (n > 1 and out.stride(0) < width):
+        raise ValueError("%s must have shape %s and rows of consecutive elements" %
+                         (name, (n, width)))
+    return out, out.stride(0) if n > 1 else width
 
 
 class Context:
@@ -359,6 +469,80 @@ class Context:
         self._check(self.lib.exl3_decode_tiles(self.handle, _ptr(packed), n, K, float(scale),
                                                _ptr(out)))
         return out
+
+    # -- products with coded weights --
+    def linear(self, x: torch.Tensor, weight: CodedWeight, transpose: bool = False,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """x [n, cols] -> x W^T [n, rows]; transpose: x [n, rows] -> x W [n, cols] (the input
+        gradient of the former).  bfloat16 or float16, rows of any pitch; out: a tensor to
+        write instead of a new one."""
+        if weight.grouped and weight.groups != 1:
+            raise ValueError("a weight of %d groups: use grouped_linear" % weight.groups)
+        wide, tall = (weight.rows, weight.cols) if transpose else (weight.cols, weight.rows)
+        x, ldx = _act_rows(x, wide, "x")
+        y, ldy = _out_rows(out, x.shape[0], tall, x, "out")
+        self._sync_stream()
+        self._check(self.lib.exl3_linear(self.handle, weight._ref, int(transpose), x.data_ptr(),
+                                         ldx, x.shape[0], _ACT[x.dtype], y.data_ptr(), ldy))
+        return y
+
+    def grouped_linear(self, x: torch.Tensor, weight: CodedWeight, offsets: torch.Tensor,
+                       transpose: bool = False,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """linear with a matrix per group (expert): rows offsets[e] .. offsets[e + 1] - 1 of x
+        are multiplied by matrix e; offsets int32 [groups + 1] on the device.  Rows of no group
+        give zeros."""
+        _need(offsets, torch.int32, (weight.groups + 1,), "offsets")
+        wide, tall = (weight.rows, weight.cols) if transpose else (weight.cols, weight.rows)
+        x, ldx = _act_rows(x, wide, "x")
+        y, ldy = _out_rows(out, x.shape[0], tall, x, "out")
+        self._sync_stream()
+        self._check(self.lib.exl3_grouped_linear(
+            self.handle, weight._ref, offsets.data_ptr(), int(transpose), x.data_ptr(), ldx,
+            x.shape[0], _ACT[x.dtype], y.data_ptr(), ldy))
+        return y
+
+    def _adapter_args(self, x, weight, adapters, ids):
+        if (adapters.rows, adapters.cols) != (weight.rows, weight.cols):
+            raise ValueError("adapters of a %d x %d matrix beside one of %d x %d" %
+                             (adapters.rows, adapters.cols, weight.rows, weight.cols))
+        if adapters.dtype != x.dtype:
+            raise ValueError("adapters must be %s, got %s" % (x.dtype, adapters.dtype))
+        _need(ids, torch.int32, (x.shape[0],), "ids")
+
+    def adapter_linear(self, x: torch.Tensor, weight: CodedWeight, adapters: Adapters,
+                       ids: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """x W^T + alpha_a (x A_a^T) B_a^T, a = ids[t] for row t (int32 [n] on the device, -1:
+        no adapter)."""
+        x, ldx = _act_rows(x, weight.cols, "x")
+        self._adapter_args(x, weight, adapters, ids)
+        y, ldy = _out_rows(out, x.shape[0], weight.rows, x, "out")
+        self._sync_stream()
+        self._check(self.lib.exl3_adapter_linear(
+            self.handle, weight._ref, adapters._ref, ids.data_ptr(), x.data_ptr(), ldx,
+            x.shape[0], _ACT[x.dtype], y.data_ptr(), ldy))
+        return y
+
+    def adapter_linear_backward(self, dy: torch.Tensor, x: torch.Tensor, weight: CodedWeight,
+                                adapters: Adapters, ids: torch.Tensor, want_dx: bool = True,
+                                want_adapters: bool = True):
+        """Gradients (dx, dA, dB) of adapter_linear at x for dy [n, rows]; None for what is
+        not wanted.  The coded matrix is frozen."""
+        dy, lddy = _act_rows(dy, weight.rows, "dy")
+        x, ldx = _act_rows(x, weight.cols, "x")
+        if x.shape[0] != dy.shape[0] or x.dtype != dy.dtype:
+            raise ValueError("x and dy differ in rows or type")
+        self._adapter_args(x, weight, adapters, ids)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
+        dA = torch.empty_like(adapters.A) if want_adapters else None
+        dB = torch.empty_like(adapters.B) if want_adapters else None
+        self._sync_stream()
+        self._check(self.lib.exl3_adapter_linear_backward(
+            self.handle, weight._ref, adapters._ref, ids.data_ptr(), dy.data_ptr(), lddy,
+            x.data_ptr(), ldx, x.shape[0], _ACT[x.dtype],
+            None if dx is None else dx.data_ptr(), weight.cols,
+            None if dA is None else dA.data_ptr(), None if dB is None else dB.data_ptr()))
+        return dx, dA, dB
 
     def quantize_matrix(self, w: torch.Tensor, K: int, su: torch.Tensor, sv: torch.Tensor,
                         had_block: int = 128,

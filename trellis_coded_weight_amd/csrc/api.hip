@@ -12,6 +12,7 @@
 // (ascending tile index), so the chosen scale does not depend on batching.
 #include "exl3.h"
 #include "exl3_internal.h"
+#include "coded.h"
 
 #include <algorithm>
 #include <cmath>
@@ -111,6 +112,14 @@ struct exl3_ctx {
     // order (the kernels then take null tables)
     uint8_t *d_order = nullptr;
     bool has_order = false;
+    // the procedural codebook the level table holds, or -1 for a caller's table
+    int cb_kind = EXL3_CB_MUL1;
+    // workspace of the products with coded weights; outgrown ones are kept, as
+    // a captured graph may hold their addresses
+    char *d_work = nullptr;
+    size_t work_cap = 0;
+    void *old_work[64] = {};
+    int n_old = 0;
     std::string err;
     // optional per-launch timing (HIP events on the context's stream)
     struct Timed {
@@ -665,6 +674,282 @@ int check_matrix_args(exl3_ctx *ctx, const void *w, int w_dtype, int rows, int c
     return EXL3_OK;
 }
 
+// ---- products with coded weights ----
+
+constexpr int64_t kMaxProductRows = (int64_t)1 << 24;
+constexpr int kMaxSide = 1 << 20, kMaxGroups = 65535, kMaxRank = 128;
+
+// Pieces of the workspace, each on a 256-byte boundary.
+struct Carve {
+    size_t used = 0;
+    size_t take(size_t bytes) {
+        const size_t at = used;
+        used += (bytes + 255) / 256 * 256;
+        return at;
+    }
+};
+
+int work_space(exl3_ctx *ctx, size_t bytes) {
+    if (bytes <= ctx->work_cap) return EXL3_OK;
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(ctx->stream, &st) != hipSuccess) (void)hipGetLastError();
+    if (st != hipStreamCaptureStatusNone)
+        return fail(ctx, EXL3_ENOMEM,
+                    "the workspace (%zu bytes) would have to grow to %zu during a capture: make "
+                    "the call once before it", ctx->work_cap, bytes);
+    if (ctx->n_old == 64) return fail(ctx, EXL3_ENOMEM, "the workspace has grown 64 times");
+    // twice the last where there is room, so that what is kept stays below what is used
+    size_t want = std::max(bytes, 2 * ctx->work_cap);
+    void *p = nullptr;
+    hipError_t e = hipMalloc(&p, want);
+    if (e != hipSuccess && want > bytes) {
+        (void)hipGetLastError();
+        want = bytes;
+        e = hipMalloc(&p, want);
+    }
+    if (e != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(ctx, EXL3_ENOMEM, "device allocation of %zu bytes failed: %s", bytes,
+                    hipGetErrorString(e));
+    }
+    if (ctx->d_work) ctx->old_work[ctx->n_old++] = ctx->d_work;
+    ctx->d_work = static_cast<char *>(p);
+    ctx->work_cap = want;
+    return EXL3_OK;
+}
+
+int check_weight(exl3_ctx *ctx, const exl3_weight *w, exl3::WeightArgs *out) {
+    if (!w) return fail(ctx, EXL3_EINVAL, "null weight");
+    if (!w->packed || !w->scale || !w->su || !w->sv)
+        return fail(ctx, EXL3_EINVAL, "null packed, scale, su or sv");
+    if (w->K < 1 || w->K > 8) return fail(ctx, EXL3_EUNSUPPORTED, "K = %d (supported: 1..8)", w->K);
+    if (w->had_block != 64 && w->had_block != 128)
+        return fail(ctx, EXL3_EUNSUPPORTED, "Hadamard block %d (supported: 64, 128)",
+                    w->had_block);
+    if (w->rows <= 0 || w->cols <= 0 || w->rows % w->had_block || w->cols % w->had_block ||
+        w->rows > kMaxSide || w->cols > kMaxSide)
+        return fail(ctx, EXL3_EINVAL, "shape %d x %d is not a positive multiple of %d up to %d",
+                    w->rows, w->cols, w->had_block, kMaxSide);
+    if (w->groups < 1 || w->groups > kMaxGroups)
+        return fail(ctx, EXL3_EINVAL, "groups = %d (1..%d)", w->groups, kMaxGroups);
+    if (reinterpret_cast<uintptr_t>(w->packed) % 4)
+        return fail(ctx, EXL3_EINVAL, "packed (%p) is not 4-byte aligned",
+                    static_cast<const void *>(w->packed));
+    const size_t g = (size_t)w->groups, r = (size_t)w->rows, c = (size_t)w->cols;
+    int rc;
+    if ((rc = check_span(ctx, w->packed, g * r * c / 256 * 32 * w->K, "packed")) != EXL3_OK ||
+        (rc = check_span(ctx, w->scale, g * sizeof(float), "scale")) != EXL3_OK ||
+        (rc = check_span(ctx, w->su, g * r * sizeof(float), "su")) != EXL3_OK ||
+        (rc = check_span(ctx, w->sv, g * c * sizeof(float), "sv")) != EXL3_OK)
+        return rc;
+    out->packed = reinterpret_cast<const uint32_t *>(w->packed);
+    out->scale = w->scale;
+    out->su = w->su;
+    out->sv = w->sv;
+    out->groups = w->groups;
+    out->rows = w->rows;
+    out->cols = w->cols;
+    out->K = w->K;
+    out->had = w->had_block;
+    out->lv = exl3::Levels{0, 0, ctx->d_levels, tile_order_inv(ctx), w->K};
+    out->lv_kind = exl3::kLevelsTable;
+    if (!ctx->has_order && w->K <= 4) {
+        if (ctx->cb_kind == EXL3_CB_MUL1) out->lv_kind = exl3::kLevelsMul1;
+        if (ctx->cb_kind == EXL3_CB_MCG || ctx->cb_kind == EXL3_CB_3INST) {
+            out->lv_kind = exl3::kLevelsHalves;
+            exl3::halves_codebook(ctx->cb_kind == EXL3_CB_MCG, &out->lv.a, &out->lv.b);
+        }
+    }
+    return EXL3_OK;
+}
+
+int check_adapters(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters *ad,
+                   const int32_t *ids, int64_t n, exl3::AdapterArgs *out) {
+    if (w->groups != 1) return fail(ctx, EXL3_EINVAL, "adapters with %d groups (1)", w->groups);
+    if (!ad || !ad->a || !ad->b || !ad->alpha) return fail(ctx, EXL3_EINVAL, "null adapters");
+    if (ad->rank < 1 || ad->rank > kMaxRank)
+        return fail(ctx, EXL3_EUNSUPPORTED, "rank %d (supported: 1..%d)", ad->rank, kMaxRank);
+    if (ad->count < 1 || ad->count > kMaxGroups)
+        return fail(ctx, EXL3_EINVAL, "count = %d (1..%d)", ad->count, kMaxGroups);
+    if (n > 0 && !ids) return fail(ctx, EXL3_EINVAL, "null ids");
+    const size_t m = (size_t)ad->count * ad->rank * 2;
+    int rc;
+    if ((rc = check_span(ctx, ad->a, m * w->cols, "a")) != EXL3_OK ||
+        (rc = check_span(ctx, ad->b, m * w->rows, "b")) != EXL3_OK ||
+        (rc = check_span(ctx, ad->alpha, (size_t)ad->count * sizeof(float), "alpha")) != EXL3_OK ||
+        (rc = check_span(ctx, ids, (size_t)n * sizeof(int32_t), "ids")) != EXL3_OK)
+        return rc;
+    *out = exl3::AdapterArgs{ad->a, ad->b, ad->alpha, ids, ad->count, ad->rank,
+                             (ad->rank + 31) / 32 * 32};
+    return EXL3_OK;
+}
+
+// A matrix of n rows of `width` 16-bit elements, ld apart.
+int check_rows(exl3_ctx *ctx, const void *p, int64_t ld, int64_t n, int width, const char *name) {
+    if (n == 0) return EXL3_OK;
+    if (!p) return fail(ctx, EXL3_EINVAL, "null %s", name);
+    if (ld < width || ld > ((int64_t)1 << 40))
+        return fail(ctx, EXL3_EINVAL, "%s: rows of %d elements %lld apart", name, width,
+                    (long long)ld);
+    if (reinterpret_cast<uintptr_t>(p) % 2)
+        return fail(ctx, EXL3_EINVAL, "%s (%p) is not 2-byte aligned", name, p);
+    return check_span(ctx, p, ((size_t)(n - 1) * (size_t)ld + (size_t)width) * 2, name);
+}
+
+// Whether two such matrices share an element (rows of one pitch may interleave).
+bool rows_overlap(const void *p, int64_t ldp, int wp, const void *q, int64_t ldq, int wq,
+                  int64_t n) {
+    const intptr_t a = reinterpret_cast<intptr_t>(p) / 2, b = reinterpret_cast<intptr_t>(q) / 2;
+    if (b >= a + (n - 1) * ldp + wp || a >= b + (n - 1) * ldq + wq) return false;
+    if (ldp != ldq) return true;
+    const int64_t at = ((b - a) % ldp + ldp) % ldp;      // where q's rows begin within p's
+    return at < wp || at + wq > ldp;
+}
+
+int check_product(exl3_ctx *ctx, int64_t n, int dtype) {
+    if (n < 0 || n > kMaxProductRows)
+        return fail(ctx, EXL3_EINVAL, "n = %lld (0..%lld)", (long long)n,
+                    (long long)kMaxProductRows);
+    if (dtype != EXL3_BF16 && dtype != EXL3_F16)
+        return fail(ctx, EXL3_EINVAL, "activation dtype %d is not EXL3_BF16 or EXL3_F16", dtype);
+    return EXL3_OK;
+}
+
+// Rows that start on 16 bytes, as the matrix product loads them.
+bool rows_aligned(const void *p, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
+}
+
+// Few rows: the codes are decoded once for each 64 rows of a group, in the
+// kernel that multiplies them.  Many: the dense weights are written first.
+bool few_rows(int64_t n, int groups) { return n <= (int64_t)64 * groups; }
+
+// y = x W^T or x W, with v b^T of the adapters when ad is given (ad_b: their
+// matrices on the output's side [count][out][rank], v from launch_shrink).
+// `done`: bytes of the workspace already taken.
+struct Product {
+    const exl3::WeightArgs *w;
+    const int32_t *offsets;
+    bool transpose;
+    const void *x;
+    int64_t ldx, n;
+    bool bf16;
+    void *y;
+    int64_t ldy;
+    const exl3::AdapterArgs *ad;
+    const void *ad_b;
+    size_t v_at;               // of v in the workspace
+    // set by plan_product
+    bool few;
+    int split, tiles, batch;
+    size_t xh_at, xs_at, part_at, dense_at, xpack_at;
+    bool pack;
+};
+
+int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
+    const exl3::WeightArgs &w = *p.w;
+    const size_t n = (size_t)p.n;
+    p.few = !p.transpose && few_rows(p.n, w.groups);
+    if (p.few) {
+        const int units = (w.cols + exl3::kUnit - 1) / exl3::kUnit;
+        // eight waves take a unit each before the columns are split further; a
+        // split more costs a pass over the sums, and is taken while the
+        // workgroups are fewer than two a compute unit
+        const int64_t groups = (int64_t)(w.rows / 16) * w.groups;
+        p.split = (int)std::min<int64_t>((units + 7) / 8,
+                                         std::max<int64_t>(1, 2 * ctx->n_cu / groups));
+        const int64_t per = (p.n + w.groups - 1) / w.groups;
+        p.tiles = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+        p.xh_at = c.take(n * w.cols * 2);
+        p.xs_at = c.take(n * units * sizeof(float));
+        p.part_at = c.take(n * w.rows * p.split * sizeof(float));
+        return EXL3_OK;
+    }
+    const size_t one = (size_t)w.rows * w.cols * 2;
+    if (one > ctx->scratch_limit)
+        return fail(ctx, EXL3_ENOMEM, "scratch limit %zu B is below one dense matrix's %zu B",
+                    ctx->scratch_limit, one);
+    p.batch = (int)std::min<size_t>((size_t)w.groups, ctx->scratch_limit / one);
+    p.dense_at = c.take(one * p.batch);
+    p.pack = !rows_aligned(p.x, p.ldx);
+    p.xpack_at = p.pack ? c.take(n * (p.transpose ? w.rows : w.cols) * 2) : 0;
+    return EXL3_OK;
+}
+
+int run_product(exl3_ctx *ctx, const Product &p) {
+    const exl3::WeightArgs &w = *p.w;
+    char *ws = ctx->d_work;
+    const uint16_t *v = p.ad ? reinterpret_cast<const uint16_t *>(ws + p.v_at) : nullptr;
+    if (p.few) {
+        uint16_t *xh = reinterpret_cast<uint16_t *>(ws + p.xh_at);
+        float *xs = reinterpret_cast<float *>(ws + p.xs_at);
+        float *part = reinterpret_cast<float *>(ws + p.part_at);
+        EXL3_HIP(ctx, exl3::launch_rotate(w, p.offsets, p.x, p.ldx, p.n, p.bf16, xh, xs,
+                                          ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_coded_rows(w, p.offsets, xh, xs, p.n, p.split, p.tiles, part,
+                                              ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_finish(w, p.offsets, part, p.split, p.n, p.bf16, p.ad, v, p.y,
+                                          p.ldy, ctx->stream));
+        return EXL3_OK;
+    }
+    const int m = p.transpose ? w.cols : w.rows, k = p.transpose ? w.rows : w.cols;
+    uint16_t *dense = reinterpret_cast<uint16_t *>(ws + p.dense_at);
+    const void *x = p.x;
+    int64_t ldx = p.ldx;
+    if (p.pack) {
+        uint16_t *xp = reinterpret_cast<uint16_t *>(ws + p.xpack_at);
+        EXL3_HIP(ctx, exl3::launch_pack_rows(x, ldx, p.n, k, xp, ctx->stream));
+        x = xp;
+        ldx = k;
+    }
+    if (p.offsets)
+        EXL3_HIP(ctx, exl3::launch_zero_rows(p.offsets, w.groups, p.n, m, p.y, p.ldy,
+                                             ctx->stream));
+    for (int g0 = 0; g0 < w.groups; g0 += p.batch) {
+        const int ng = std::min(p.batch, w.groups - g0);
+        EXL3_HIP(ctx, exl3::launch_dense(w, p.offsets, p.n, g0, ng, p.transpose, p.bf16, dense,
+                                         ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_gemm(x, ldx, dense, p.n, m, k, p.offsets, g0, ng, p.bf16, p.ad,
+                                        p.ad_b, v, p.y, p.ldy, ctx->n_cu, ctx->stream));
+    }
+    return EXL3_OK;
+}
+
+int linear_any(exl3_ctx *ctx, const exl3_weight *w, const int32_t *offsets, int transpose,
+               const void *x, int64_t ldx, int64_t n, int dtype, void *y, int64_t ldy) {
+    int rc;
+    exl3::WeightArgs wa;
+    if ((rc = check_weight(ctx, w, &wa)) != EXL3_OK) return rc;
+    if ((rc = check_product(ctx, n, dtype)) != EXL3_OK) return rc;
+    const int in = transpose ? w->rows : w->cols, out = transpose ? w->cols : w->rows;
+    if ((rc = check_rows(ctx, x, ldx, n, in, "x")) != EXL3_OK ||
+        (rc = check_rows(ctx, y, ldy, n, out, "y")) != EXL3_OK ||
+        (rc = check_span(ctx, offsets, ((size_t)w->groups + 1) * sizeof(int32_t), "offsets")) !=
+            EXL3_OK)
+        return rc;
+    if (n == 0) return EXL3_OK;
+    if (rows_overlap(x, ldx, in, y, ldy, out, n)) return fail(ctx, EXL3_EINVAL, "y overlaps x");
+    if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    Product p{};
+    p.w = &wa;
+    p.offsets = offsets;
+    p.transpose = transpose != 0;
+    p.x = x;
+    p.ldx = ldx;
+    p.n = n;
+    p.bf16 = dtype == EXL3_BF16;
+    p.y = y;
+    p.ldy = ldy;
+    Carve c;
+    if ((rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
+    if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
+    const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT,
+                              (int64_t)w->groups * (w->rows / 16) * (w->cols / 16));
+    rc = run_product(ctx, p);
+    close_timed(ctx, id);
+    return rc;
+}
+
 }  // namespace
 
 extern "C" {
@@ -724,9 +1009,10 @@ void exl3_ctx_destroy(exl3_ctx *ctx) {
                     ctx->d_sse,         ctx->d_flag,        ctx->d_err_tiles,   ctx->d_span_target,
                     ctx->d_span_what,   ctx->d_span_packed, ctx->d_gs,          ctx->d_x16,
                     ctx->d_pk,          ctx->d_order,       ctx->d_gss,         ctx->d_bidx,
-                    ctx->d_bscale};
+                    ctx->d_bscale,      ctx->d_work};
     for (void *p : bufs)
         if (p) (void)hipFree(p);
+    for (int i = 0; i < ctx->n_old; ++i) (void)hipFree(ctx->old_work[i]);
     delete ctx;
 }
 
@@ -799,6 +1085,7 @@ int exl3_set_codebook(exl3_ctx *ctx, const uint16_t *levels_fp16_host) {
     EXL3_HIP(ctx, hipMemcpyAsync(ctx->d_levels, lv.data(), 65536 * sizeof(uint16_t),
                                  hipMemcpyHostToDevice, ctx->stream));
     EXL3_HIP(ctx, hipStreamSynchronize(ctx->stream));
+    ctx->cb_kind = levels_fp16_host ? -1 : (int)EXL3_CB_MUL1;
     return EXL3_OK;
 }
 
@@ -816,6 +1103,7 @@ int exl3_set_codebook_kind(exl3_ctx *ctx, int kind) {
     EXL3_HIP(ctx, hipMemcpyAsync(ctx->d_levels, lv.data(), 65536 * sizeof(uint16_t),
                                  hipMemcpyHostToDevice, ctx->stream));
     EXL3_HIP(ctx, hipStreamSynchronize(ctx->stream));
+    ctx->cb_kind = kind;
     return EXL3_OK;
 }
 
@@ -1526,6 +1814,136 @@ int exl3_quantize_matrix_ldlq(exl3_ctx *ctx, const void *w, int w_dtype, int row
     }
     EXL3_HIP(ctx, hipStreamSynchronize(ctx->stream));
     *scale_out = scale;
+    return EXL3_OK;
+}
+
+int exl3_linear(exl3_ctx *ctx, const exl3_weight *w, int transpose, const void *x, int64_t ldx,
+                int64_t n, int dtype, void *y, int64_t ldy) {
+    if (!ctx) return EXL3_EINVAL;
+    if (w && w->groups != 1)
+        return fail(ctx, EXL3_EINVAL, "groups = %d; exl3_grouped_linear takes several", w->groups);
+    return linear_any(ctx, w, nullptr, transpose, x, ldx, n, dtype, y, ldy);
+}
+
+int exl3_grouped_linear(exl3_ctx *ctx, const exl3_weight *w, const int32_t *offsets, int transpose,
+                        const void *x, int64_t ldx, int64_t n, int dtype, void *y, int64_t ldy) {
+    if (!ctx) return EXL3_EINVAL;
+    if (!offsets) return fail(ctx, EXL3_EINVAL, "null offsets");
+    return linear_any(ctx, w, offsets, transpose, x, ldx, n, dtype, y, ldy);
+}
+
+int exl3_adapter_linear(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters *ad,
+                        const int32_t *ids, const void *x, int64_t ldx, int64_t n, int dtype,
+                        void *y, int64_t ldy) {
+    if (!ctx) return EXL3_EINVAL;
+    int rc;
+    exl3::WeightArgs wa;
+    exl3::AdapterArgs aa;
+    if ((rc = check_weight(ctx, w, &wa)) != EXL3_OK) return rc;
+    if ((rc = check_product(ctx, n, dtype)) != EXL3_OK) return rc;
+    if ((rc = check_adapters(ctx, w, ad, ids, n, &aa)) != EXL3_OK ||
+        (rc = check_rows(ctx, x, ldx, n, w->cols, "x")) != EXL3_OK ||
+        (rc = check_rows(ctx, y, ldy, n, w->rows, "y")) != EXL3_OK)
+        return rc;
+    if (n == 0) return EXL3_OK;
+    if (rows_overlap(x, ldx, w->cols, y, ldy, w->rows, n))
+        return fail(ctx, EXL3_EINVAL, "y overlaps x");
+    if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    Product p{};
+    p.w = &wa;
+    p.x = x;
+    p.ldx = ldx;
+    p.n = n;
+    p.bf16 = dtype == EXL3_BF16;
+    p.y = y;
+    p.ldy = ldy;
+    p.ad = &aa;
+    p.ad_b = aa.b;
+    Carve c;
+    p.v_at = c.take((size_t)n * aa.rank_pad * 2);
+    if ((rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
+    if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
+    const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
+    EXL3_HIP(ctx, exl3::launch_shrink(aa, aa.a, x, ldx, n, w->cols, p.bf16,
+                                      reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at),
+                                      ctx->stream));
+    rc = run_product(ctx, p);
+    close_timed(ctx, id);
+    return rc;
+}
+
+int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters *ad,
+                                 const int32_t *ids, const void *dy, int64_t lddy, const void *x,
+                                 int64_t ldx, int64_t n, int dtype, void *dx, int64_t lddx,
+                                 void *da, void *db) {
+    if (!ctx) return EXL3_EINVAL;
+    int rc;
+    exl3::WeightArgs wa;
+    exl3::AdapterArgs aa;
+    if ((rc = check_weight(ctx, w, &wa)) != EXL3_OK) return rc;
+    if ((rc = check_product(ctx, n, dtype)) != EXL3_OK) return rc;
+    if ((rc = check_adapters(ctx, w, ad, ids, n, &aa)) != EXL3_OK ||
+        (rc = check_rows(ctx, dy, lddy, n, w->rows, "dy")) != EXL3_OK)
+        return rc;
+    const size_t m = (size_t)aa.count * aa.rank;
+    if ((da || db) && (rc = check_rows(ctx, x, ldx, n, w->cols, "x")) != EXL3_OK) return rc;
+    if (dx && (rc = check_rows(ctx, dx, lddx, n, w->cols, "dx")) != EXL3_OK) return rc;
+    if ((rc = check_span(ctx, da, m * w->cols * 2, "da")) != EXL3_OK ||
+        (rc = check_span(ctx, db, m * w->rows * 2, "db")) != EXL3_OK)
+        return rc;
+    if (dx && n > 0 &&
+        (rows_overlap(dy, lddy, w->rows, dx, lddx, w->cols, n) ||
+         ((da || db) && rows_overlap(x, ldx, w->cols, dx, lddx, w->cols, n))))
+        return fail(ctx, EXL3_EINVAL, "dx overlaps dy or x");
+    if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    const bool bf16 = dtype == EXL3_BF16, wants_dx = dx && n > 0;
+    const bool needs_u = wants_dx || da;
+    Product p{};
+    p.w = &wa;
+    p.transpose = true;
+    p.x = dy;
+    p.ldx = lddy;
+    p.n = n;
+    p.bf16 = bf16;
+    p.y = dx;
+    p.ldy = lddx;
+    p.ad = &aa;
+    Carve c;
+    p.v_at = c.take((size_t)n * aa.rank_pad * 2);
+    const size_t v_at = c.take((size_t)n * aa.rank_pad * 2);
+    const size_t bt_at = c.take(m * w->rows * 2), at_at = c.take(m * w->cols * 2);
+    const int sa = exl3::adapter_grad_splits(n, w->cols, aa.count);
+    const int sb = exl3::adapter_grad_splits(n, w->rows, aa.count);
+    const size_t part_at = c.take(std::max(sa * m * w->cols, sb * m * w->rows) * sizeof(float));
+    if (wants_dx && (rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
+    if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
+    char *ws = ctx->d_work;
+    uint16_t *u = reinterpret_cast<uint16_t *>(ws + p.v_at);
+    uint16_t *v = reinterpret_cast<uint16_t *>(ws + v_at);
+    float *part = reinterpret_cast<float *>(ws + part_at);
+    const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
+    if (needs_u && n > 0) {
+        EXL3_HIP(ctx, exl3::launch_transpose16(aa.b, aa.count, w->rows, aa.rank, ws + bt_at,
+                                               ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_shrink(aa, ws + bt_at, dy, lddy, n, w->rows, bf16, u,
+                                          ctx->stream));
+    }
+    if (wants_dx) {
+        EXL3_HIP(ctx, exl3::launch_transpose16(aa.a, aa.count, aa.rank, w->cols, ws + at_at,
+                                               ctx->stream));
+        p.ad_b = ws + at_at;
+        if ((rc = run_product(ctx, p)) != EXL3_OK) return rc;
+    }
+    if (da)
+        EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, u, x, ldx, n, w->cols, bf16, false, sa, part,
+                                                da, ctx->stream));
+    if (db) {
+        if (n > 0)
+            EXL3_HIP(ctx, exl3::launch_shrink(aa, aa.a, x, ldx, n, w->cols, bf16, v, ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, v, dy, lddy, n, w->rows, bf16, true, sb, part,
+                                                db, ctx->stream));
+    }
+    close_timed(ctx, id);
     return EXL3_OK;
 }
 

@@ -105,4 +105,9 @@ void build_halves_sum(uint32_t a, uint32_t b, uint16_t *out) {
 void build_mcg_levels(uint16_t *out) { build_halves_sum(kMcgA, 0u, out); }
 void build_3inst_levels(uint16_t *out) { build_halves_sum(kInst3A, kInst3B, out); }
 
+void halves_codebook(bool mcg, uint32_t *a, uint32_t *b) {
+    *a = mcg ? kMcgA : kInst3A;
+    *b = mcg ? 0u : kInst3B;
+}
+
 }  // namespace exl3

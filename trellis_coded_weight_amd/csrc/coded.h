@@ -1,0 +1,287 @@
+// Device-side reading of coded weights in the register layout of the matrix
+// instructions (gfx950), shared by the products with coded weights.
+//
+// A matrix instruction contracts 32 values k per step: lane l holds row l & 15
+// of its operand and, with g = l >> 4, eight of the 32 k's.  Which k a lane's
+// eight are is free as long as both operands agree, so a lane takes one whole
+// row of one 16 x 16 tile: of 64 consecutive columns (four tiles), lane group
+// g owns tile g, and its row's 16 consecutive trellis positions are the
+// operands of two steps: columns 16 g + 0..7, then 16 g + 8..15.  Sixteen
+// consecutive positions are one run of 16 K stream bits, and their states are
+// windows of that run and the 16 bits before it: K / 2 + 1 words loaded (K
+// even; K = 2: two) for 16 weights, no shared memory and no exchange of lanes.
+//
+// The levels are computed, not looked up: the 128 KiB table would cost every
+// compute unit a fill as large as its share of many a matrix's codes, and 64
+// random LDS reads of a wave meet in few banks.
+//   mul1: h = A s mod 2^32 (two 24-bit products and a shift-add, each at full
+//     rate, where one 32-bit product runs at a quarter of it), beta = the sum of
+//     h's bytes (v_sad_u8), taken as the binary16 number 1024 + beta by placing
+//     it in that number's mantissa, two states in one register.  Then
+//     d = beta - 510 (exact) and level = fma(d, k_hi, fma(d, k_lo, e)) in
+//     binary16 with k_hi + k_lo = 1 / std and e = (510 - mean) / std: equal bit
+//     for bit to the table's binary16 rounding for every beta in 0..1020 that
+//     the table holds (the tests compare all 65,536 states).  6.5 operations a
+//     weight with the window.
+//   mcg, 3INST: w = a s + b mod 2^32 in the same way, masked, and the sum of
+//     its two binary16 halves for two states at once.
+// Any other table, any within-tile order and K = 5..8 take the general form:
+// every element's window by its position, and its level from the table.
+#pragma once
+
+#include "exl3_internal.h"
+
+namespace exl3 {
+
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
+using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+
+// How levels are found; the values are template arguments of the kernels.
+enum { kLevelsMul1 = 0, kLevelsHalves = 1, kLevelsTable = 2 };
+
+struct Levels {
+    uint32_t a, b;           // kLevelsHalves: w = a s + b
+    const uint16_t *table;   // kLevelsTable: 65,536 binary16 values
+    const uint8_t *inv;      // element -> position within a tile, or null (kLevelsTable only)
+    int K;                   // bits a weight (kLevelsTable only; otherwise a template argument)
+};
+
+__device__ __forceinline__ uint32_t mul_mod32(uint32_t s, uint32_t a, uint32_t b) {
+    return (__umul24(s, a & 0xFFFFFFu) + b) + (__umul24(s, a >> 24) << 24);
+}
+
+// The levels of two states as two binary16 values.
+template <int LV>
+__device__ __forceinline__ uint32_t level_pair(uint32_t s0, uint32_t s1, const Levels &lv) {
+    if (LV == kLevelsMul1) {
+        const uint32_t h0 = mul_mod32(s0, 0x9E3779B1u, 0u), h1 = mul_mod32(s1, 0x9E3779B1u, 0u);
+        uint32_t p = __builtin_amdgcn_sad_u8(h0, 0u, 0x64006400u);
+        p = __builtin_amdgcn_sad_hi_u8(h1, 0u, p);
+        const f16x2 base = __builtin_bit_cast(f16x2, 0xE5FEE5FEu);   // -1534
+        const f16x2 k_hi = __builtin_bit_cast(f16x2, 0x1EEC1EECu);
+        const f16x2 k_lo = __builtin_bit_cast(f16x2, 0x00110011u);
+        const f16x2 e = __builtin_bit_cast(f16x2, 0x0C580C58u);
+        const f16x2 d = __builtin_bit_cast(f16x2, p) + base;
+        const f16x2 c = __builtin_elementwise_fma(d, k_hi, __builtin_elementwise_fma(d, k_lo, e));
+        return __builtin_bit_cast(uint32_t, c);
+    } else if (LV == kLevelsHalves) {
+        const uint32_t w0 = (mul_mod32(s0, lv.a, lv.b) & 0x8FFF8FFFu) ^ 0x3B603B60u;
+        const uint32_t w1 = (mul_mod32(s1, lv.a, lv.b) & 0x8FFF8FFFu) ^ 0x3B603B60u;
+        const f16x2 lo = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(w1, w0, 0x05040100u));
+        const f16x2 hi = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(w1, w0, 0x07060302u));
+        return __builtin_bit_cast(uint32_t, lo + hi);
+    } else {
+        return (uint32_t)lv.table[s0] | ((uint32_t)lv.table[s1] << 16);
+    }
+}
+
+// Words a lane loads for one row of a tile (K = 0: the general form, which
+// loads its words when it decodes).
+template <int K>
+struct RowWords {
+    static constexpr int N = K == 0 ? 1 : (K % 2 == 0) ? K / 2 + 1 : (K + 3) / 2;
+};
+
+// The words that hold row r's 16 K bits and the 16 bits before them (the
+// stream is circular): from word ((K r + 1) >> 1) - 1 on.  For odd K and odd r
+// the bits start at that word's first bit and the last word loaded is not
+// used (it is held inside the tile); otherwise they start at its 17th bit.
+template <int K>
+__device__ __forceinline__ void load_row(const uint32_t *tile, int r,
+                                         uint32_t (&d)[RowWords<K>::N]) {
+    if constexpr (K > 0) {
+        const int first = ((K * r + 1) >> 1) - 1;
+        d[0] = tile[first < 0 ? 8 * K - 1 : first];
+#pragma unroll
+        for (int i = 1; i < RowWords<K>::N; ++i) {
+            int w = first + i;
+            if (K % 2 != 0 && i == RowWords<K>::N - 1) w = w < 8 * K ? w : 8 * K - 1;
+            d[i] = tile[w];
+        }
+    }
+}
+
+// The 16 levels of row r of a tile, as the operands of two steps.
+template <int LV, int K>
+__device__ __forceinline__ void decode_row(const uint32_t *tile, int r,
+                                           const uint32_t (&d)[RowWords<K>::N], const Levels &lv,
+                                           u32x4 (&out)[2]) {
+    if constexpr (K == 0) {
+        const int kk = lv.K, nbits = 256 * kk, nc = 8 * kk;
+#pragma unroll 2
+        for (int j = 0; j < 16; j += 2) {
+            uint32_t s[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int el = 16 * r + j + h;
+                const int t = lv.inv ? (int)lv.inv[el] : el;
+                int p = (t + 1) * kk - 16;
+                if (p < 0) p += nbits;
+                const int c = p >> 5;
+                const uint32_t hi = tile[c], lo = tile[c + 1 == nc ? 0 : c + 1];
+                s[h] = __funnelshift_l(lo, hi, (unsigned)(p & 31)) >> 16;
+            }
+            out[j >> 3][(j >> 1) & 3] = level_pair<kLevelsTable>(s[0], s[1], lv);
+        }
+    } else {
+        // e[q]: the 32 bits that start 16 q bits after the row's run starts
+        uint32_t e[K + 1];
+        if constexpr (K % 2 == 0) {
+#pragma unroll
+            for (int q = 0; q <= K; ++q)
+                e[q] = (q & 1) ? d[(q + 1) / 2]
+                     : q == K  ? d[K / 2] << 16
+                               : __builtin_amdgcn_alignbit(d[q / 2], d[q / 2 + 1], 16);
+        } else {
+            constexpr int NN = (K + 1) / 2;
+            uint32_t m[NN];
+#pragma unroll
+            for (int i = 0; i < NN; ++i)
+                m[i] = (r & 1) ? d[i] : __builtin_amdgcn_alignbit(d[i], d[i + 1], 16);
+#pragma unroll
+            for (int q = 0; q <= K; ++q)
+                e[q] = !(q & 1) ? m[q / 2]
+                     : q == K   ? m[(K - 1) / 2] << 16
+                                : __builtin_amdgcn_alignbit(m[(q - 1) / 2], m[(q + 1) / 2], 16);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const int b0 = (j + 1) * K, b1 = (j + 2) * K;
+            const uint32_t s0 = (e[b0 >> 4] >> (16 - (b0 & 15))) & 0xFFFFu;
+            const uint32_t s1 = (e[b1 >> 4] >> (16 - (b1 & 15))) & 0xFFFFu;
+            out[j >> 3][(j >> 1) & 3] = level_pair<LV>(s0, s1, lv);
+        }
+    }
+}
+
+// Binary16 and bfloat16 activations: conversions and the matrix instruction.
+template <bool BF>
+struct Act;
+template <>
+struct Act<false> {
+    static __device__ __forceinline__ float load(uint16_t v) {
+        return (float)__builtin_bit_cast(_Float16, v);
+    }
+    static __device__ __forceinline__ uint16_t store(float v) {
+        return __builtin_bit_cast(uint16_t, (_Float16)v);
+    }
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+};
+template <>
+struct Act<true> {
+    static __device__ __forceinline__ float load(uint16_t v) {
+        return __builtin_bit_cast(float, (uint32_t)v << 16);
+    }
+    static __device__ __forceinline__ uint16_t store(float v) {
+        return __builtin_bit_cast(uint16_t, (__bf16)v);
+    }
+    static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+};
+
+// The group (expert) of a row among `groups` ascending offsets[groups + 1]:
+// the number of groups that end at or before it (a row at or past the last
+// offset gives `groups`).  All 64 lanes of the wave take part.
+__device__ __forceinline__ int group_of_row(const int32_t *offsets, int groups, int64_t row) {
+    const int lane = threadIdx.x & 63;
+    int e = 0;
+    for (int j = 0; j < groups; j += 64) {
+        const bool past = j + lane < groups && (int64_t)offsets[1 + j + lane] <= row;
+        e += __popcll(__ballot(past));
+    }
+    return e;
+}
+
+// A group's rows [lo, hi), held inside [0, n) whatever the offsets say.
+__device__ __forceinline__ void group_rows(const int32_t *offsets, int e, int64_t n, int64_t &lo,
+                                           int64_t &hi) {
+    lo = 0;
+    hi = n;
+    if (offsets) {
+        lo = offsets[e];
+        hi = offsets[e + 1];
+        lo = lo < 0 ? 0 : lo;
+        hi = hi > n ? n : hi;
+    }
+}
+
+// ---- arguments and launchers of the products (linear.hip, dense.hip, adapters.hip) ----
+
+// Columns that share one power-of-two scale of the transformed activations.
+constexpr int kUnit = 256;
+
+struct WeightArgs {
+    const uint32_t *packed;   // [groups][rows / 16][cols / 16][8 K]
+    const float *scale, *su, *sv;
+    int groups, rows, cols, K, had;
+    int lv_kind;              // kLevels*
+    Levels lv;
+};
+
+struct AdapterArgs {
+    const void *a, *b;        // [count][rank][cols], [count][rows][rank]
+    const float *alpha;
+    const int32_t *ids;       // [n]
+    int count, rank, rank_pad;
+};
+
+// x' = H_r (sv x) as binary16 [n][cols] with a scale [n][units] (a power of two).
+hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void *x, int64_t ldx,
+                         int64_t n, bool bf16, uint16_t *xh, float *xs, hipStream_t stream);
+
+// part[split][n][rows]: sums over a split's columns of x' and the levels.
+hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
+                             const float *xs, int64_t n, int split, int tiles, float *part,
+                             hipStream_t stream);
+
+// y = su H_l (sum of the parts) scale / had, plus the adapters' products v B^T.
+hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const float *part, int split,
+                         int64_t n, bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
+                         int64_t ldy, hipStream_t stream);
+
+// The dense weights in the activations' type: [groups][rows][cols], or
+// [groups][cols][rows] when transposed; groups g0 .. g0 + ng - 1.
+hipError_t launch_dense(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
+                        bool transposed, bool bf16, uint16_t *dense, hipStream_t stream);
+
+// y[n][m] = x[n][k] dense[g][m][k]^T for the rows of groups g0 .. g0 + ng - 1,
+// plus the adapters' products v b^T (b: [count][m][rank]).
+hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_t n, int m, int k,
+                       const int32_t *offsets, int g0, int ng, bool bf16,
+                       const AdapterArgs *ad, const void *b, const uint16_t *v, void *y,
+                       int64_t ldy, int n_cu, hipStream_t stream);
+
+// Rows of x copied to [n][k] without gaps.
+hipError_t launch_pack_rows(const void *x, int64_t ldx, int64_t n, int k, uint16_t *out,
+                            hipStream_t stream);
+
+// Rows of y that no group holds, set to zero.
+hipError_t launch_zero_rows(const int32_t *offsets, int groups, int64_t n, int m, void *y,
+                            int64_t ldy, hipStream_t stream);
+
+// v[n][rank_pad] = alpha_a x a_a^T in the activations' type, zero past the rank
+// and for rows without an adapter; a: [count][rank][k].
+hipError_t launch_shrink(const AdapterArgs &ad, const void *a, const void *x, int64_t ldx,
+                         int64_t n, int k, bool bf16, uint16_t *v, hipStream_t stream);
+
+// [count][p][q] -> [count][q][p], 16-bit elements.
+hipError_t launch_transpose16(const void *src, int count, int p, int q, void *dst,
+                              hipStream_t stream);
+
+// out[a][i][j] = sum over the rows t of adapter a of u[t][i] q[t][j], i < rank;
+// written as [count][rank][k], or [count][k][rank] when transposed.  part:
+// float [splits][count][rank_pad][k].
+int adapter_grad_splits(int64_t n, int k, int count);
+hipError_t launch_adapter_grad(const AdapterArgs &ad, const uint16_t *u, const void *q,
+                               int64_t ldq, int64_t n, int k, bool bf16, bool transposed,
+                               int splits, float *part, void *out, hipStream_t stream);
+
+}  // namespace exl3

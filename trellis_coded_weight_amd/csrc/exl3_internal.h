@@ -212,5 +212,7 @@ hipError_t launch_gather_tiles(const float *src, const int32_t *idx, int64_t n, 
 void build_mul1_levels(uint16_t *out65536);
 void build_mcg_levels(uint16_t *out65536);
 void build_3inst_levels(uint16_t *out65536);
+// w = a s + b of mcg (or 3INST), for kernels that compute its levels.
+void halves_codebook(bool mcg, uint32_t *a, uint32_t *b);
 
 }  // namespace exl3
