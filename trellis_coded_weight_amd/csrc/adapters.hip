@@ -22,19 +22,19 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *p, bool wide) {
 // ---- v = alpha A x ----
 // A workgroup per 16 rows of x, and in grid.y the share of the rows' distinct
 // adapters it takes in turn (many requests: one each, so that they run beside
-// each other; long prompts: one share).  Eight waves split the contraction
-// and their sums meet in shared memory.  The matrix instruction multiplies
-// all 16 rows by each adapter and keeps those that have it: its rate is far
-// from the bound, which is reading A once per 16 rows.
+// each other; long prompts: one share).  Eight waves split the contraction,
+// four steps of 32 loaded ahead of their use, and their sums meet in shared
+// memory.  The matrix instruction multiplies all 16 rows by each adapter and
+// keeps those that have it: its rate is far from the bound, which is reading A
+// once per 16 rows from the caches.  grid.z: up to two such products.
 template <bool BF, int RT>
 __global__ void __launch_bounds__(512)
-shrink_kernel(AdapterArgs ad, const uint16_t *__restrict__ a, const uint16_t *__restrict__ x,
-              int64_t ldx, int64_t n, int k, bool wide_a, bool wide_x,
-              uint16_t *__restrict__ v) {
+shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
     __shared__ f32x4 sums[8][RT][64];
     __shared__ int ids[16];
+    const ShrinkArgs p = blockIdx.z ? p1 : p0;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
+    const int r = lane & 15, g = lane >> 4, k = p.k;
     const int64_t t0 = (int64_t)blockIdx.x * 16;
     if (threadIdx.x < 16) {
         const int64_t tok = t0 + threadIdx.x;
@@ -43,13 +43,15 @@ shrink_kernel(AdapterArgs ad, const uint16_t *__restrict__ a, const uint16_t *__
     }
     __syncthreads();
     if (blockIdx.y == 0) {
+        // rows without an adapter, and the padding that no tile of ranks covers
         for (int i = threadIdx.x; i < 16 * ad.rank_pad; i += 512) {
-            const int t = i / ad.rank_pad;
-            if (t0 + t < n && ids[t] < 0) v[(t0 + t) * ad.rank_pad + i % ad.rank_pad] = 0;
+            const int t = i / ad.rank_pad, c = i % ad.rank_pad;
+            if (t0 + t < n && (ids[t] < 0 || c >= 16 * RT))
+                p.v[(t0 + t) * ad.rank_pad + c] = 0;
         }
     }
     const int64_t tok = t0 + r < n ? t0 + r : n - 1;
-    const uint16_t *xr = x + tok * ldx + 8 * g;
+    const uint16_t *xr = p.x + tok * p.ldx + 8 * g;
     int turn = 0;
     for (int s = 0; s < 16; ++s) {
         const int id = ids[s];
@@ -57,18 +59,29 @@ shrink_kernel(AdapterArgs ad, const uint16_t *__restrict__ a, const uint16_t *__
         for (int q = 0; q < s; ++q) seen |= ids[q] == id;
         if (seen) continue;
         if (turn++ % (int)gridDim.y != (int)blockIdx.y) continue;
-        const uint16_t *ar = a + (size_t)id * ad.rank * k + 8 * g;
+        const uint16_t *ar = p.a + (size_t)id * ad.rank * k + 8 * g;
         f32x4 acc[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int c = wv * 32; c < k; c += 256) {
-            const u32x4 xv = load8(xr + c, wide_x);
+        constexpr int U = RT <= 4 ? 4 : 2;
+        for (int c0 = wv * 32; c0 < k; c0 += 256 * U) {
+            u32x4 xv[U], av[U][RT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                u32x4 av = {0u, 0u, 0u, 0u};
-                if (16 * t + r < ad.rank) av = load8(ar + (size_t)(16 * t + r) * k + c, wide_a);
-                acc[t] = Act<BF>::mfma(av, xv, acc[t]);
+            for (int j = 0; j < U; ++j) {
+                const int c = c0 + 256 * j;
+                xv[j] = u32x4{0u, 0u, 0u, 0u};
+                if (c < k) xv[j] = load8(xr + c, p.wide_x);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    av[j][t] = u32x4{0u, 0u, 0u, 0u};
+                    if (c < k && 16 * t + r < ad.rank)
+                        av[j][t] = load8(ar + (size_t)(16 * t + r) * k + c, p.wide_a);
+                }
             }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) acc[t] = Act<BF>::mfma(av[j][t], xv[j], acc[t]);
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) sums[wv][t][lane] = acc[t];
@@ -81,126 +94,210 @@ shrink_kernel(AdapterArgs ad, const uint16_t *__restrict__ a, const uint16_t *__
             const int c = 16 * t + 4 * (l >> 4);
             if (ids[l & 15] == id && c < ad.rank_pad) {
                 const float al = ad.alpha[id];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[(t0 + (l & 15)) * ad.rank_pad + c + j] = Act<BF>::store(al * z[j]);
+                const int64_t to = t0 + (l & 15);
+                const uint32_t lo = Act<BF>::store2(al * z[0], al * z[1]);
+                const uint32_t hi = Act<BF>::store2(al * z[2], al * z[3]);
+                *reinterpret_cast<uint2 *>(p.v + to * ad.rank_pad + c) = uint2{lo, hi};
+                if (p.vt) {
+                    uint16_t *o = p.vt + (size_t)c * p.ldvt + to;
+                    o[0] = (uint16_t)lo;
+                    o[p.ldvt] = (uint16_t)(lo >> 16);
+                    o[2 * p.ldvt] = (uint16_t)hi;
+                    o[3 * p.ldvt] = (uint16_t)(hi >> 16);
+                }
             }
         }
         __syncthreads();
     }
 }
 
+// [count][p][q] -> [count][q][p] for up to two arrays (grid.z: count of each).
 __global__ void __launch_bounds__(256)
-transpose16_kernel(const uint16_t *__restrict__ src, int p, int q, uint16_t *__restrict__ dst) {
+transpose16_kernel(TransposeArgs t0, TransposeArgs t1, int count) {
     __shared__ uint16_t tile[32][33];
+    const TransposeArgs t = (int)blockIdx.y < count ? t0 : t1;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const size_t at = (size_t)blockIdx.z * p * q;
-    const int q0 = blockIdx.x * 32, p0 = blockIdx.y * 32;
+    const int across = (t.q + 31) / 32, down = (t.p + 31) / 32;
+    if ((int)blockIdx.x >= across * down) return;
+    const size_t at = (size_t)(blockIdx.y % count) * t.p * t.q;
+    const int q0 = blockIdx.x % across * 32, p0 = blockIdx.x / across * 32;
     for (int i = ty; i < 32; i += 8)
-        if (p0 + i < p && q0 + tx < q) tile[i][tx] = src[at + (size_t)(p0 + i) * q + q0 + tx];
+        if (p0 + i < t.p && q0 + tx < t.q)
+            tile[i][tx] = t.src[at + (size_t)(p0 + i) * t.q + q0 + tx];
     __syncthreads();
     for (int i = ty; i < 32; i += 8)
-        if (q0 + i < q && p0 + tx < p) dst[at + (size_t)(q0 + i) * p + p0 + tx] = tile[tx][i];
+        if (q0 + i < t.q && p0 + tx < t.p)
+            t.dst[at + (size_t)(q0 + i) * t.p + p0 + tx] = tile[tx][i];
 }
 
 // ---- gradients of the adapters' matrices ----
-// sum over the rows t of adapter a of u[t][i] q[t][j], 32 rows a step.  Rows of
-// other adapters enter as zeros on both sides, chosen and not multiplied, so
-// that whatever they hold stays out.  The rows are split in `splits` parts,
+// sum over the rows t of adapter a of u[t][i] q[t][j]: the contraction runs over
+// rows, 32 a step.  u comes transposed, so its operand is one load; of q a lane
+// loads four neighbouring columns of its eight rows and pairs the rows up in
+// registers, which gives the operands of four tiles of 16 columns (columns
+// 4 r + c of tile c).  Rows of other adapters enter as zeros on both sides,
+// chosen and not multiplied, so that whatever they hold stays out; blocks of
+// 32 rows without the adapter are passed over.  The rows are split in parts,
 // summed in order afterwards: the result does not depend on scheduling.
+// grid: blocks of 256 columns of the first product, then of the second;
+// adapters; parts.
+constexpr int kGradBlocks = 16;            // blocks of 32 rows whose adapters are read at once
+
 template <bool BF, int RT>
 __global__ void __launch_bounds__(256)
-adapter_grad_kernel(AdapterArgs ad, const uint16_t *__restrict__ u,
-                    const uint16_t *__restrict__ q, int64_t ldq, int64_t n, int k,
-                    int64_t per_split, float *__restrict__ part) {
+adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t per_split) {
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
-    const int id = blockIdx.y, j = blockIdx.x * 64 + wv * 16 + r;
+    const int r = lane & 15, g = lane >> 4, id = blockIdx.y;
+    const int first = (g0.k + 255) / 256;
+    const bool second = (int)blockIdx.x >= first;
+    const GradArgs p = second ? g1 : g0;
+    const int j0 = ((int)blockIdx.x - (second ? first : 0)) * 256 + wv * 64;
+    if (j0 >= p.k) return;
     const int64_t t_lo = blockIdx.z * per_split;
     const int64_t t_hi = t_lo + per_split < n ? t_lo + per_split : n;
-    f32x4 acc[RT];
+    f32x4 acc[RT][4];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t t0 = t_lo; t0 < t_hi; t0 += 32) {
-        const int64_t mine = t0 + (lane & 31);
-        const uint32_t has = (uint32_t)__ballot(mine < t_hi && ad.ids[mine] == id);
-        if (!has) continue;
-        u32x4 b;
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint16_t *qc = p.q + j0 + 4 * r;
+
+    struct Step {
+        uint2 x[8];
+        u32x4 u[RT];
+        uint32_t has;
+    };
+    auto fetch = [&](Step &s, int64_t b, uint32_t has) {
+        s.has = has;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            s.x[t] = uint2{0u, 0u};
+            if ((has >> (8 * g + t)) & 1u) {
+                const uint16_t *at = qc + (b + 8 * g + t) * p.ldq;
+                if (p.wide_q)
+                    s.x[t] = *reinterpret_cast<const uint2 *>(at);
+                else
+                    s.x[t] = uint2{at[0] | ((uint32_t)at[1] << 16),
+                                   at[2] | ((uint32_t)at[3] << 16)};
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            s.u[t] = u32x4{0u, 0u, 0u, 0u};
+            if (16 * t + r < ad.rank)
+                s.u[t] = *reinterpret_cast<const u32x4 *>(p.ut + (size_t)(16 * t + r) * p.ldut + b +
+                                                          8 * g);
+        }
+    };
+    auto use = [&](Step &s) {
+        u32x4 keep;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            uint32_t w = 0;
+            const uint32_t two = (s.has >> (8 * g + 2 * c)) & 3u;
+            keep[c] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+        }
+        u32x4 b[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = 8 * g + 2 * c + h;
-                if ((has >> t) & 1u) w |= (uint32_t)q[(t0 + t) * ldq + j] << (16 * h);
-            }
-            b[c] = w;
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t ax = s.x[2 * c].x, bx = s.x[2 * c + 1].x;
+            const uint32_t ay = s.x[2 * c].y, by = s.x[2 * c + 1].y;
+            b[0][c] = __builtin_amdgcn_perm(bx, ax, 0x05040100u);
+            b[1][c] = __builtin_amdgcn_perm(bx, ax, 0x07060302u);
+            b[2][c] = __builtin_amdgcn_perm(by, ay, 0x05040100u);
+            b[3][c] = __builtin_amdgcn_perm(by, ay, 0x07060302u);
         }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            u32x4 a;
+        for (int t = 0; t < RT; ++t) {
+            const u32x4 u = s.u[t] & keep;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t w = 0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int t = 8 * g + 2 * c + h;
-                    if (((has >> t) & 1u) && 16 * rt + r < ad.rank)
-                        w |= (uint32_t)u[(t0 + t) * ad.rank_pad + 16 * rt + r] << (16 * h);
-                }
-                a[c] = w;
-            }
-            acc[rt] = Act<BF>::mfma(a, b, acc[rt]);
+            for (int c = 0; c < 4; ++c) acc[t][c] = Act<BF>::mfma(u, b[c], acc[t][c]);
         }
+    };
+    for (int64_t c0 = t_lo; c0 < t_hi; c0 += 32 * kGradBlocks) {
+        // which rows of each block have the adapter: bits of 16 words, one a lane
+        uint32_t mine = 0;
+#pragma unroll
+        for (int b = 0; b < kGradBlocks; b += 2) {
+            const int64_t t = c0 + 32 * b + lane;
+            const uint64_t has = __ballot(t < t_hi && ad.ids[t] == id);
+            if (lane == b) mine = (uint32_t)has;
+            if (lane == b + 1) mine = (uint32_t)(has >> 32);
+        }
+        uint64_t left = __ballot(mine != 0);
+        if (!left) continue;
+        Step s[2];
+        int b = __ffsll((unsigned long long)left) - 1;
+        left &= left - 1;
+        fetch(s[0], c0 + 32 * b, __builtin_amdgcn_readlane(mine, b));
+        while (left) {
+            b = __ffsll((unsigned long long)left) - 1;
+            left &= left - 1;
+            fetch(s[1], c0 + 32 * b, __builtin_amdgcn_readlane(mine, b));
+            use(s[0]);
+            s[0] = s[1];
+        }
+        use(s[0]);
     }
-    float *o = part + ((size_t)blockIdx.z * ad.count + id) * ad.rank * k;
+    // column j0 + 4 r + c, ranks 16 t + 4 g ..
+    float *o = p.part + ((size_t)blockIdx.z * ad.count + id) * ad.rank * p.k;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int i = 16 * rt + 4 * g + c;
-            if (i < ad.rank) o[(size_t)i * k + j] = acc[rt][c];
+        for (int i = 0; i < 4; ++i) {
+            const int rank = 16 * t + 4 * g + i;
+            if (rank >= ad.rank) continue;
+            if (p.transposed) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    o[(size_t)(j0 + 4 * r + c) * ad.rank + rank] = acc[t][c][i];
+            } else {
+                *reinterpret_cast<f32x4 *>(o + (size_t)rank * p.k + j0 + 4 * r) =
+                    f32x4{acc[t][0][i], acc[t][1][i], acc[t][2][i], acc[t][3][i]};
+            }
         }
 }
 
+// The parts' sums of both products (grid.y), four elements a thread.
 template <bool BF>
 __global__ void __launch_bounds__(256)
-adapter_sum_kernel(const float *__restrict__ part, int splits, int count, int rank, int k,
-                   bool transposed, uint16_t *__restrict__ out) {
-    const size_t all = (size_t)count * rank * k, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+adapter_sum_kernel(GradArgs g0, GradArgs g1, int splits, int count, int rank) {
+    const GradArgs p = blockIdx.y ? g1 : g0;
+    const size_t all = (size_t)count * rank * p.k;
+    const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= all) return;
-    size_t from = i;
-    if (transposed) {                    // out is [count][k][rank]
-        const size_t a = i / ((size_t)rank * k), rest = i - a * rank * k;
-        from = (a * rank + rest % rank) * k + rest / rank;
+    f32x4 s = *reinterpret_cast<const f32x4 *>(p.part + i);
+    for (int q = 1; q < splits; ++q) s += *reinterpret_cast<const f32x4 *>(p.part + q * all + i);
+    const uint32_t lo = Act<BF>::store2(s[0], s[1]), hi = Act<BF>::store2(s[2], s[3]);
+    uint16_t *o = p.out + i;
+    if (p.wide_out) {
+        *reinterpret_cast<uint2 *>(o) = uint2{lo, hi};
+    } else {
+        o[0] = (uint16_t)lo;
+        o[1] = (uint16_t)(lo >> 16);
+        o[2] = (uint16_t)hi;
+        o[3] = (uint16_t)(hi >> 16);
     }
-    float s = 0.0f;
-    for (int p = 0; p < splits; ++p) s += part[(size_t)p * all + from];
-    out[i] = Act<BF>::store(s);
 }
 
 }  // namespace
 
-hipError_t launch_shrink(const AdapterArgs &ad, const void *a, const void *x, int64_t ldx,
-                         int64_t n, int k, bool bf16, uint16_t *v, hipStream_t stream) {
+hipError_t launch_shrink(const AdapterArgs &ad, const ShrinkArgs *p, int products, int64_t n,
+                         bool bf16, hipStream_t stream) {
+    ShrinkArgs q[2];
+    for (int i = 0; i < 2; ++i) {
+        q[i] = p[i < products ? i : 0];
+        q[i].wide_a = reinterpret_cast<uintptr_t>(q[i].a) % 16 == 0;
+        q[i].wide_x = reinterpret_cast<uintptr_t>(q[i].x) % 16 == 0 && q[i].ldx % 8 == 0;
+    }
     const unsigned tiles = (unsigned)((n + 15) / 16);
     // up to 16 distinct adapters a tile: a workgroup each while there are few tiles
-    const dim3 grid(tiles, tiles <= 32 ? 16u : tiles <= 128 ? 4u : 1u);
-    const bool wide_a = reinterpret_cast<uintptr_t>(a) % 16 == 0;
-    const bool wide_x = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % 8 == 0;
-    const uint16_t *aa = static_cast<const uint16_t *>(a), *xx = static_cast<const uint16_t *>(x);
-#define EXL3_SHRINK(RT)                                                                      \
-    do {                                                                                     \
-        if (bf16)                                                                            \
-            hipLaunchKernelGGL((shrink_kernel<true, RT>), grid, dim3(512), 0, stream, ad, aa, \
-                               xx, ldx, n, k, wide_a, wide_x, v);                            \
-        else                                                                                 \
-            hipLaunchKernelGGL((shrink_kernel<false, RT>), grid, dim3(512), 0, stream, ad, aa, \
-                               xx, ldx, n, k, wide_a, wide_x, v);                            \
-    } while (0)
-    if (ad.rank_pad <= 32)
+    const dim3 grid(tiles, tiles <= 32 ? 16u : tiles <= 128 ? 4u : 1u, (unsigned)products);
+#define EXL3_SHRINK(RT)                                                                             do {                                                                                                if (bf16)                                                                                           hipLaunchKernelGGL((shrink_kernel<true, RT>), grid, dim3(512), 0, stream, ad, q[0],                                q[1], n);                                                                else                                                                                                hipLaunchKernelGGL((shrink_kernel<false, RT>), grid, dim3(512), 0, stream, ad,                                     q[0], q[1], n);                                                      } while (0)
+    if (ad.rank <= 16)
+        EXL3_SHRINK(1);
+    else if (ad.rank <= 32)
         EXL3_SHRINK(2);
-    else if (ad.rank_pad <= 64)
+    else if (ad.rank <= 64)
         EXL3_SHRINK(4);
     else
         EXL3_SHRINK(8);
@@ -208,37 +305,34 @@ hipError_t launch_shrink(const AdapterArgs &ad, const void *a, const void *x, in
     return hipGetLastError();
 }
 
-hipError_t launch_transpose16(const void *src, int count, int p, int q, void *dst,
-                              hipStream_t stream) {
-    const dim3 grid((unsigned)((q + 31) / 32), (unsigned)((p + 31) / 32), (unsigned)count);
-    hipLaunchKernelGGL(transpose16_kernel, grid, dim3(256), 0, stream,
-                       static_cast<const uint16_t *>(src), p, q, static_cast<uint16_t *>(dst));
+hipError_t launch_transpose16(const TransposeArgs *t, int arrays, int count, hipStream_t stream) {
+    const TransposeArgs &a = t[0], &b = t[arrays - 1];
+    const unsigned ta = (unsigned)((a.p + 31) / 32) * (unsigned)((a.q + 31) / 32);
+    const unsigned tb = (unsigned)((b.p + 31) / 32) * (unsigned)((b.q + 31) / 32);
+    hipLaunchKernelGGL(transpose16_kernel, dim3(ta > tb ? ta : tb, (unsigned)(count * arrays)),
+                       dim3(256), 0, stream, a, b, count);
     return hipGetLastError();
 }
 
-int adapter_grad_splits(int64_t n, int k, int count) {
-    // about two workgroups a compute unit, of 128 rows at least
-    const int64_t groups = (int64_t)(k / 64) * count;
-    int64_t s = 512 / groups;
-    if (s > (n + 127) / 128) s = (n + 127) / 128;
-    return s < 1 ? 1 : (int)s;
+int adapter_grad_splits(int64_t n, int count) {
+    // parts of 512 rows, one round of reading their adapters, up to 16 parts;
+    // many adapters fill the chip without
+    const int64_t s = (n + 32 * kGradBlocks - 1) / (32 * kGradBlocks), most = 64 / count;
+    return (int)(s < 1 || most < 1 ? 1 : s < most ? (s < 16 ? s : 16) : most < 16 ? most : 16);
 }
 
-hipError_t launch_adapter_grad(const AdapterArgs &ad, const uint16_t *u, const void *q,
-                               int64_t ldq, int64_t n, int k, bool bf16, bool transposed,
-                               int splits, float *part, void *out, hipStream_t stream) {
+hipError_t launch_adapter_grad(const AdapterArgs &ad, const GradArgs *p, int products, int64_t n,
+                               bool bf16, int splits, hipStream_t stream) {
+    GradArgs q[2];
+    for (int i = 0; i < 2; ++i) {
+        q[i] = p[i < products ? i : 0];
+        q[i].wide_q = reinterpret_cast<uintptr_t>(q[i].q) % 8 == 0 && q[i].ldq % 4 == 0;
+        q[i].wide_out = reinterpret_cast<uintptr_t>(q[i].out) % 8 == 0;
+    }
     const int64_t per = ((n + splits - 1) / splits + 31) / 32 * 32;
-    const dim3 grid((unsigned)(k / 64), (unsigned)ad.count, (unsigned)splits);
-    const uint16_t *qq = static_cast<const uint16_t *>(q);
-#define EXL3_GRAD(RT)                                                                          \
-    do {                                                                                       \
-        if (bf16)                                                                              \
-            hipLaunchKernelGGL((adapter_grad_kernel<true, RT>), grid, dim3(256), 0, stream, ad, \
-                               u, qq, ldq, n, k, per, part);                                   \
-        else                                                                                   \
-            hipLaunchKernelGGL((adapter_grad_kernel<false, RT>), grid, dim3(256), 0, stream,   \
-                               ad, u, qq, ldq, n, k, per, part);                               \
-    } while (0)
+    const int blocks = (q[0].k + 255) / 256 + (products > 1 ? (q[1].k + 255) / 256 : 0);
+    const dim3 grid((unsigned)blocks, (unsigned)ad.count, (unsigned)splits);
+#define EXL3_GRAD(RT)                                                                                do {                                                                                                 if (bf16)                                                                                            hipLaunchKernelGGL((adapter_grad_kernel<true, RT>), grid, dim3(256), 0, stream, ad,                                 q[0], q[1], n, per);                                                      else                                                                                                 hipLaunchKernelGGL((adapter_grad_kernel<false, RT>), grid, dim3(256), 0, stream, ad,                                q[0], q[1], n, per);                                                  } while (0)
     if (ad.rank <= 16)
         EXL3_GRAD(1);
     else if (ad.rank <= 32)
@@ -250,15 +344,14 @@ hipError_t launch_adapter_grad(const AdapterArgs &ad, const uint16_t *u, const v
 #undef EXL3_GRAD
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    const size_t all = (size_t)ad.count * ad.rank * k;
-    const unsigned blocks = (unsigned)((all + 255) / 256);
-    uint16_t *o = static_cast<uint16_t *>(out);
+    const int k = q[0].k > q[1].k ? q[0].k : q[1].k;
+    const unsigned groups = (unsigned)(((size_t)ad.count * ad.rank * k / 4 + 255) / 256);
     if (bf16)
-        hipLaunchKernelGGL((adapter_sum_kernel<true>), dim3(blocks), dim3(256), 0, stream, part,
-                           splits, ad.count, ad.rank, k, transposed, o);
+        hipLaunchKernelGGL((adapter_sum_kernel<true>), dim3(groups, (unsigned)products), dim3(256),
+                           0, stream, q[0], q[1], splits, ad.count, ad.rank);
     else
-        hipLaunchKernelGGL((adapter_sum_kernel<false>), dim3(blocks), dim3(256), 0, stream, part,
-                           splits, ad.count, ad.rank, k, transposed, o);
+        hipLaunchKernelGGL((adapter_sum_kernel<false>), dim3(groups, (unsigned)products),
+                           dim3(256), 0, stream, q[0], q[1], splits, ad.count, ad.rank);
     return hipGetLastError();
 }
 

@@ -815,9 +815,10 @@ int check_product(exl3_ctx *ctx, int64_t n, int dtype) {
     return EXL3_OK;
 }
 
-// Rows that start on 16 bytes, as the matrix product loads them.
+// Rows that start on 16 bytes, as the matrix product loads them (and near enough
+// for its 32-bit offsets of 256 rows).
 bool rows_aligned(const void *p, int64_t ld) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && ld < (1 << 22);
 }
 
 // Few rows: the codes are decoded once for each 64 rows of a group, in the
@@ -902,13 +903,10 @@ int run_product(exl3_ctx *ctx, const Product &p) {
         x = xp;
         ldx = k;
     }
-    if (p.offsets)
-        EXL3_HIP(ctx, exl3::launch_zero_rows(p.offsets, w.groups, p.n, m, p.y, p.ldy,
-                                             ctx->stream));
     for (int g0 = 0; g0 < w.groups; g0 += p.batch) {
         const int ng = std::min(p.batch, w.groups - g0);
         EXL3_HIP(ctx, exl3::launch_dense(w, p.offsets, p.n, g0, ng, p.transpose, p.bf16, dense,
-                                         ctx->stream));
+                                         p.y, p.ldy, ctx->stream));
         EXL3_HIP(ctx, exl3::launch_gemm(x, ldx, dense, p.n, m, k, p.offsets, g0, ng, p.bf16, p.ad,
                                         p.ad_b, v, p.y, p.ldy, ctx->n_cu, ctx->stream));
     }
@@ -1864,9 +1862,11 @@ int exl3_adapter_linear(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters
     if ((rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
     const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
-    EXL3_HIP(ctx, exl3::launch_shrink(aa, aa.a, x, ldx, n, w->cols, p.bf16,
-                                      reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at),
-                                      ctx->stream));
+    const exl3::ShrinkArgs sh{static_cast<const uint16_t *>(aa.a),
+                              static_cast<const uint16_t *>(x), ldx, w->cols,
+                              reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at), nullptr, 0,
+                              false, false};
+    EXL3_HIP(ctx, exl3::launch_shrink(aa, &sh, 1, n, p.bf16, ctx->stream));
     rc = run_product(ctx, p);
     close_timed(ctx, id);
     return rc;
@@ -1910,39 +1910,54 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
     p.ad = &aa;
     Carve c;
     p.v_at = c.take((size_t)n * aa.rank_pad * 2);
-    const size_t v_at = c.take((size_t)n * aa.rank_pad * 2);
+    const size_t pitch = ((size_t)n + 31) / 32 * 32, ranks = (size_t)aa.rank_pad;
+    const size_t v_at = c.take((size_t)n * ranks * 2);
+    const size_t ut_at = c.take(pitch * ranks * 2), vt_at = c.take(pitch * ranks * 2);
     const size_t bt_at = c.take(m * w->rows * 2), at_at = c.take(m * w->cols * 2);
-    const int sa = exl3::adapter_grad_splits(n, w->cols, aa.count);
-    const int sb = exl3::adapter_grad_splits(n, w->rows, aa.count);
-    const size_t part_at = c.take(std::max(sa * m * w->cols, sb * m * w->rows) * sizeof(float));
+    const int splits = exl3::adapter_grad_splits(n, aa.count);
+    const size_t pa_at = c.take(splits * m * w->cols * sizeof(float));
+    const size_t pb_at = c.take(splits * m * w->rows * sizeof(float));
     if (wants_dx && (rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
     char *ws = ctx->d_work;
-    uint16_t *u = reinterpret_cast<uint16_t *>(ws + p.v_at);
-    uint16_t *v = reinterpret_cast<uint16_t *>(ws + v_at);
-    float *part = reinterpret_cast<float *>(ws + part_at);
+    auto at16 = [ws](size_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
     const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
-    if (needs_u && n > 0) {
-        EXL3_HIP(ctx, exl3::launch_transpose16(aa.b, aa.count, w->rows, aa.rank, ws + bt_at,
-                                               ctx->stream));
-        EXL3_HIP(ctx, exl3::launch_shrink(aa, ws + bt_at, dy, lddy, n, w->rows, bf16, u,
-                                          ctx->stream));
+    const uint16_t *a16 = static_cast<const uint16_t *>(aa.a);
+    const uint16_t *b16 = static_cast<const uint16_t *>(aa.b);
+    const uint16_t *x16 = static_cast<const uint16_t *>(x);
+    const uint16_t *dy16 = static_cast<const uint16_t *>(dy);
+    if (n > 0) {
+        // u = alpha dy B (its matrix transposed), v = alpha x A^T
+        exl3::TransposeArgs tr[2];
+        exl3::ShrinkArgs sh[2];
+        int nt = 0, ns = 0;
+        if (needs_u) {
+            tr[nt++] = exl3::TransposeArgs{b16, at16(bt_at), w->rows, aa.rank};
+            sh[ns++] = exl3::ShrinkArgs{at16(bt_at), dy16, lddy, w->rows, at16(p.v_at),
+                                        da ? at16(ut_at) : nullptr, (int64_t)pitch, false, false};
+        }
+        if (wants_dx) tr[nt++] = exl3::TransposeArgs{a16, at16(at_at), aa.rank, w->cols};
+        if (db)
+            sh[ns++] = exl3::ShrinkArgs{a16, x16, ldx, w->cols, at16(v_at), at16(vt_at),
+                                        (int64_t)pitch, false, false};
+        if (nt) EXL3_HIP(ctx, exl3::launch_transpose16(tr, nt, aa.count, ctx->stream));
+        if (ns) EXL3_HIP(ctx, exl3::launch_shrink(aa, sh, ns, n, bf16, ctx->stream));
     }
     if (wants_dx) {
-        EXL3_HIP(ctx, exl3::launch_transpose16(aa.a, aa.count, aa.rank, w->cols, ws + at_at,
-                                               ctx->stream));
         p.ad_b = ws + at_at;
         if ((rc = run_product(ctx, p)) != EXL3_OK) return rc;
     }
+    exl3::GradArgs gr[2];
+    int ng = 0;
     if (da)
-        EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, u, x, ldx, n, w->cols, bf16, false, sa, part,
-                                                da, ctx->stream));
-    if (db) {
-        if (n > 0)
-            EXL3_HIP(ctx, exl3::launch_shrink(aa, aa.a, x, ldx, n, w->cols, bf16, v, ctx->stream));
-        EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, v, dy, lddy, n, w->rows, bf16, true, sb, part,
-                                                db, ctx->stream));
-    }
+        gr[ng++] = exl3::GradArgs{at16(ut_at), x16, (int64_t)pitch, ldx, w->cols, false,
+                                  reinterpret_cast<float *>(ws + pa_at),
+                                  static_cast<uint16_t *>(da), false, false};
+    if (db)
+        gr[ng++] = exl3::GradArgs{at16(vt_at), dy16, (int64_t)pitch, lddy, w->rows, true,
+                                  reinterpret_cast<float *>(ws + pb_at),
+                                  static_cast<uint16_t *>(db), false, false};
+    if (ng) EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, gr, ng, n, bf16, splits, ctx->stream));
     close_timed(ctx, id);
     return EXL3_OK;
 }

@@ -14,15 +14,14 @@
 // The levels are computed, not looked up: the 128 KiB table would cost every
 // compute unit a fill as large as its share of many a matrix's codes, and 64
 // random LDS reads of a wave meet in few banks.
-//   mul1: h = A s mod 2^32 (two 24-bit products and a shift-add, each at full
-//     rate, where one 32-bit product runs at a quarter of it), beta = the sum of
-//     h's bytes (v_sad_u8), taken as the binary16 number 1024 + beta by placing
+//   mul1: h = A s mod 2^32 (one 32-bit product; two 24-bit ones and a shift-add
+//     measured 0-7 % slower), beta = the sum of h's bytes (v_sad_u8), taken as the binary16 number 1024 + beta by placing
 //     it in that number's mantissa, two states in one register.  Then
 //     d = beta - 510 (exact) and level = fma(d, k_hi, fma(d, k_lo, e)) in
 //     binary16 with k_hi + k_lo = 1 / std and e = (510 - mean) / std: equal bit
 //     for bit to the table's binary16 rounding for every beta in 0..1020 that
-//     the table holds (the tests compare all 65,536 states).  6.5 operations a
-//     weight with the window.
+//     the table holds (the tests compare all 65,536 states).  5.5 instructions
+//     a weight with the window.
 //   mcg, 3INST: w = a s + b mod 2^32 in the same way, masked, and the sum of
 //     its two binary16 halves for two states at once.
 // Any other table, any within-tile order and K = 5..8 take the general form:
@@ -35,6 +34,7 @@ namespace exl3 {
 
 using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
 using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
+using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
@@ -49,15 +49,11 @@ struct Levels {
     int K;                   // bits a weight (kLevelsTable only; otherwise a template argument)
 };
 
-__device__ __forceinline__ uint32_t mul_mod32(uint32_t s, uint32_t a, uint32_t b) {
-    return (__umul24(s, a & 0xFFFFFFu) + b) + (__umul24(s, a >> 24) << 24);
-}
-
 // The levels of two states as two binary16 values.
 template <int LV>
 __device__ __forceinline__ uint32_t level_pair(uint32_t s0, uint32_t s1, const Levels &lv) {
     if (LV == kLevelsMul1) {
-        const uint32_t h0 = mul_mod32(s0, 0x9E3779B1u, 0u), h1 = mul_mod32(s1, 0x9E3779B1u, 0u);
+        const uint32_t h0 = s0 * 0x9E3779B1u, h1 = s1 * 0x9E3779B1u;
         uint32_t p = __builtin_amdgcn_sad_u8(h0, 0u, 0x64006400u);
         p = __builtin_amdgcn_sad_hi_u8(h1, 0u, p);
         const f16x2 base = __builtin_bit_cast(f16x2, 0xE5FEE5FEu);   // -1534
@@ -68,8 +64,8 @@ __device__ __forceinline__ uint32_t level_pair(uint32_t s0, uint32_t s1, const L
         const f16x2 c = __builtin_elementwise_fma(d, k_hi, __builtin_elementwise_fma(d, k_lo, e));
         return __builtin_bit_cast(uint32_t, c);
     } else if (LV == kLevelsHalves) {
-        const uint32_t w0 = (mul_mod32(s0, lv.a, lv.b) & 0x8FFF8FFFu) ^ 0x3B603B60u;
-        const uint32_t w1 = (mul_mod32(s1, lv.a, lv.b) & 0x8FFF8FFFu) ^ 0x3B603B60u;
+        const uint32_t w0 = ((s0 * lv.a + lv.b) & 0x8FFF8FFFu) ^ 0x3B603B60u;
+        const uint32_t w1 = ((s1 * lv.a + lv.b) & 0x8FFF8FFFu) ^ 0x3B603B60u;
         const f16x2 lo = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(w1, w0, 0x05040100u));
         const f16x2 hi = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(w1, w0, 0x07060302u));
         return __builtin_bit_cast(uint32_t, lo + hi);
@@ -168,6 +164,12 @@ struct Act<false> {
     static __device__ __forceinline__ uint16_t store(float v) {
         return __builtin_bit_cast(uint16_t, (_Float16)v);
     }
+    static __device__ __forceinline__ uint32_t store2(float a, float b) {
+        f16x2 v;
+        v[0] = (_Float16)a;
+        v[1] = (_Float16)b;
+        return __builtin_bit_cast(uint32_t, v);
+    }
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                       __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -180,6 +182,12 @@ struct Act<true> {
     }
     static __device__ __forceinline__ uint16_t store(float v) {
         return __builtin_bit_cast(uint16_t, (__bf16)v);
+    }
+    static __device__ __forceinline__ uint32_t store2(float a, float b) {
+        bf16x2 v;
+        v[0] = (__bf16)a;
+        v[1] = (__bf16)b;
+        return __builtin_bit_cast(uint32_t, v);
     }
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -248,9 +256,11 @@ hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const floa
                          int64_t ldy, hipStream_t stream);
 
 // The dense weights in the activations' type: [groups][rows][cols], or
-// [groups][cols][rows] when transposed; groups g0 .. g0 + ng - 1.
+// [groups][cols][rows] when transposed; groups g0 .. g0 + ng - 1.  With offsets
+// and g0 = 0 also sets the rows of y that no group holds to zero.
 hipError_t launch_dense(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
-                        bool transposed, bool bf16, uint16_t *dense, hipStream_t stream);
+                        bool transposed, bool bf16, uint16_t *dense, void *y, int64_t ldy,
+                        hipStream_t stream);
 
 // y[n][m] = x[n][k] dense[g][m][k]^T for the rows of groups g0 .. g0 + ng - 1,
 // plus the adapters' products v b^T (b: [count][m][rank]).
@@ -263,25 +273,44 @@ hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_
 hipError_t launch_pack_rows(const void *x, int64_t ldx, int64_t n, int k, uint16_t *out,
                             hipStream_t stream);
 
-// Rows of y that no group holds, set to zero.
-hipError_t launch_zero_rows(const int32_t *offsets, int groups, int64_t n, int m, void *y,
-                            int64_t ldy, hipStream_t stream);
-
 // v[n][rank_pad] = alpha_a x a_a^T in the activations' type, zero past the rank
-// and for rows without an adapter; a: [count][rank][k].
-hipError_t launch_shrink(const AdapterArgs &ad, const void *a, const void *x, int64_t ldx,
-                         int64_t n, int k, bool bf16, uint16_t *v, hipStream_t stream);
+// and for rows without an adapter; a: [count][rank][k].  vt, if not null, also
+// gets v transposed, [rank_pad][ldvt] (rows with an adapter only).  One launch
+// takes up to two such products.
+struct ShrinkArgs {
+    const uint16_t *a, *x;
+    int64_t ldx;
+    int k;
+    uint16_t *v, *vt;
+    int64_t ldvt;
+    bool wide_a, wide_x;      // set by the launcher
+};
+hipError_t launch_shrink(const AdapterArgs &ad, const ShrinkArgs *p, int products, int64_t n,
+                         bool bf16, hipStream_t stream);
 
-// [count][p][q] -> [count][q][p], 16-bit elements.
-hipError_t launch_transpose16(const void *src, int count, int p, int q, void *dst,
-                              hipStream_t stream);
+// [count][p][q] -> [count][q][p], 16-bit elements, up to two arrays.
+struct TransposeArgs {
+    const uint16_t *src;
+    uint16_t *dst;
+    int p, q;
+};
+hipError_t launch_transpose16(const TransposeArgs *t, int arrays, int count, hipStream_t stream);
 
 // out[a][i][j] = sum over the rows t of adapter a of u[t][i] q[t][j], i < rank;
-// written as [count][rank][k], or [count][k][rank] when transposed.  part:
-// float [splits][count][rank_pad][k].
-int adapter_grad_splits(int64_t n, int k, int count);
-hipError_t launch_adapter_grad(const AdapterArgs &ad, const uint16_t *u, const void *q,
-                               int64_t ldq, int64_t n, int k, bool bf16, bool transposed,
-                               int splits, float *part, void *out, hipStream_t stream);
+// written as [count][rank][k], or [count][k][rank] when transposed.  ut: u
+// transposed, rows 16-byte aligned and ldut >= n rounded up to 32 apart.  part:
+// float [splits][count][rank][k].  Up to two products of equal n and splits.
+struct GradArgs {
+    const uint16_t *ut, *q;
+    int64_t ldut, ldq;
+    int k;
+    bool transposed;
+    float *part;
+    uint16_t *out;
+    bool wide_q, wide_out;    // set by the launcher
+};
+int adapter_grad_splits(int64_t n, int count);
+hipError_t launch_adapter_grad(const AdapterArgs &ad, const GradArgs *p, int products, int64_t n,
+                               bool bf16, int splits, hipStream_t stream);
 
 }  // namespace exl3

@@ -11,143 +11,234 @@ namespace {
 __device__ __forceinline__ uint32_t parity16(uint32_t v) { return __popc(v) & 1u; }
 
 // ---- dense weights ----
-// A workgroup per HB x HB block of W (HB: the Hadamard block), a wave per 16
-// rows and then per 16 columns.  Both transforms run on the matrix units: the
-// levels are exact in binary16 and the transform's entries are +-1.
+// A workgroup takes an HB x HB block of W (HB: the Hadamard block), a wave per
+// 16 rows and then per 16 columns.  Both transforms run
+// on the matrix units: the levels are exact in binary16 and the transform's
+// entries are +-1, held as operands made once.
 //   1. The wave decodes 16 x 64 levels into operands (coded.h) and multiplies
-//      by H_64 over their columns, an operand made of signs: entry (c, n) is
-//      (-1)^popcount(c & n); for HB = 128 the halves' sum and difference
-//      follow.
-//   2. The result, sums of HB levels, is rounded to binary16 (2^-12 of each,
-//      below the final rounding to binary16 or bfloat16) and passes through
-//      shared memory column by column.
-//   3. The wave multiplies 16 columns by H_HB over the rows, then the scale,
-//      su and sv in binary32, and rounds once to the activations' type.
-// Row-major and transposed output differ in the order of step 3's operands:
-// either way a lane holds four consecutive elements of the output.
+//      them by H_64 over their columns: entry (c, n) is (-1)^popcount(c & n).
+//      For HB = 128 the halves' sum and difference follow.
+//   2. The result, sums of HB levels, passes through shared memory column by
+//      column as binary16: for bfloat16 weights rounded to it (2^-12 of each,
+//      an eighth of what the final rounding takes), for binary16 weights in two
+//      parts, the rounded value and the rest, so that the weights are rounded
+//      once.
+//   3. The wave transforms 16 columns over the rows.  Of a row's index in H_HB
+//      the lowest five bits meet the matrix instruction's 32 k's; the sums over
+//      the remaining index are butterflies of the results.
+// Then the scale, su and sv in binary32 and one rounding to the activations'
+// type.  Row-major and transposed output differ in the order of step 3's
+// operands: either way a lane holds four consecutive elements of the output.
+// The write of the weights bounds it.
+using f32x4u = float __attribute__((ext_vector_type(4), aligned(4)));
+
 template <int LV, int K, int HB, bool BF, bool TR>
-__global__ void __launch_bounds__(HB * 4)
+__global__ void __launch_bounds__(HB * 4, 4)
 dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols, int Kr,
              const float *__restrict__ scale, const float *__restrict__ su,
              const float *__restrict__ sv, const int32_t *__restrict__ offsets, int64_t n, int g0,
-             uint16_t *__restrict__ dense) {
+             uint16_t *__restrict__ dense, uint16_t *__restrict__ y, int64_t ldy,
+             int groups) {
     constexpr int kPitch = HB * 2 + 16;          // bytes a column of the block takes in LDS
-    __shared__ __align__(16) char mid[HB * kPitch];
+    constexpr int kParts = BF ? 1 : 2, NT = HB / 16, NP = HB / 32;
+    __shared__ __align__(16) char mid[kParts][HB * kPitch];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4;
     const int e = g0 + blockIdx.y, blocks = cols / HB;
     const int br = blockIdx.x / blocks, bc = blockIdx.x % blocks;
     int64_t lo, hi;
+    if (offsets && g0 == 0) {
+        // rows of y before the first group and after the last, by all workgroups
+        const int64_t from = offsets[0], to = offsets[groups];
+        const int64_t all = (int64_t)gridDim.x * gridDim.y;
+        const int64_t me = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+        const int m = TR ? cols : rows;
+        for (int64_t t = me; t < n && t < from; t += all)
+            for (int c = threadIdx.x; c < m; c += HB * 4) y[t * ldy + c] = 0;
+        for (int64_t t = (to > 0 ? to : 0) + me; t < n; t += all)
+            for (int c = threadIdx.x; c < m; c += HB * 4) y[t * ldy + c] = 0;
+    }
     group_rows(offsets, e, n, lo, hi);
     if (lo >= hi) return;                        // no row uses this group
     const int kk = K ? K : Kr;
-    const int rt = br * (HB / 16) + wv;
-    const uint32_t *tiles = packed + (((size_t)e * (rows / 16) + rt) * (cols / 16) +
-                                      (size_t)bc * (HB / 16) + g) * (8 * kk);
-    f32x4 sum[HB / 16];
+    const uint32_t *tiles = packed + (((size_t)e * (rows / 16) + br * NT + wv) * (cols / 16) + g) *
+                                         (8 * kk);
+    // the words come first, the operands of signs are made meanwhile
     uint32_t d[HB / 64][RowWords<K>::N];
 #pragma unroll
-    for (int q = 0; q < HB / 64; ++q) load_row<K>(tiles + (size_t)(4 * q) * (8 * kk), r, d[q]);
+    for (int q = 0; q < HB / 64; ++q)
+        load_row<K>(tiles + (size_t)(bc * NT + 4 * q) * (8 * kk), r, d[q]);
+    // operands of signs: column (or row) r against k's low four bits 8 s + j
+    u32x4 low[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            low[s][j] = 0x3C003C00u | (parity16((8 * s + 2 * j) & r) << 15) |
+                        (parity16((8 * s + 2 * j + 1) & r) << 31);
+    u32x4 h64[4][2];                             // H_64 at k = 16 g + 8 s + j, column 16 t + r
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const uint32_t flip = parity16(g & t) ? 0x80008000u : 0u;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) h64[t][s] = low[s] ^ flip;
+    }
+    // H_32 at row 16 o + r, k = 8 g + j
+    u32x4 h32[2];
+    h32[0] = (g & 1) ? low[1] : low[0];
+    h32[1] = h32[0] ^ ((g >> 1) ? 0x80008000u : 0u);
+    const float f = scale[e] / (float)HB;
+    const float *su_b = su + (size_t)e * rows + (size_t)br * HB;
+    float su_t[TR ? 1 : NT];
+    if (!TR)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) su_t[t] = f * su_b[16 * t + r];
+    uint16_t *out = dense + (size_t)blockIdx.y * rows * cols;
+
+    f32x4 sum[NT];
 #pragma unroll
     for (int q = 0; q < HB / 64; ++q) {
         u32x4 w[2];
-        decode_row<LV, K>(tiles + (size_t)(4 * q) * (8 * kk), r, d[q], lv, w);
+        decode_row<LV, K>(tiles + (size_t)(bc * NT + 4 * q) * (8 * kk), r, d[q], lv, w);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                // signs of H_64 at rows 16 g + 8 s + j, column 16 t + r
-                const uint32_t flip = parity16(g & t);
-                u32x4 h;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t a = parity16((8 * s + 2 * j) & r) ^ flip;
-                    const uint32_t b = parity16((8 * s + 2 * j + 1) & r) ^ flip;
-                    h[j] = 0x3C003C00u | (a << 15) | (b << 31);
-                }
-                p = Act<false>::mfma(w[s], h, p);
-            }
+            p = Act<false>::mfma(w[0], h64[t][0], p);
+            p = Act<false>::mfma(w[1], h64[t][1], p);
             if (q == 0) {
                 sum[t] = p;
             } else {
-                sum[(4 + t) % (HB / 16)] = sum[t] - p;
+                sum[(4 + t) % NT] = sum[t] - p;
                 sum[t] = sum[t] + p;
             }
         }
     }
     // column 16 t + r, rows 16 wv + 4 g .. + 3
 #pragma unroll
-    for (int t = 0; t < HB / 16; ++t) {
+    for (int t = 0; t < NT; ++t) {
         f16x2 a, b;
         a[0] = (_Float16)sum[t][0];
         a[1] = (_Float16)sum[t][1];
         b[0] = (_Float16)sum[t][2];
         b[1] = (_Float16)sum[t][3];
-        uint2 o;
-        o.x = __builtin_bit_cast(uint32_t, a);
-        o.y = __builtin_bit_cast(uint32_t, b);
-        *reinterpret_cast<uint2 *>(mid + (16 * t + r) * kPitch + (16 * wv + 4 * g) * 2) = o;
+        const int at = (16 * t + r) * kPitch + (16 * wv + 4 * g) * 2;
+        *reinterpret_cast<uint2 *>(mid[0] + at) =
+            uint2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+        if (!BF) {
+            f16x2 c, dd;
+            c[0] = (_Float16)(sum[t][0] - (float)a[0]);
+            c[1] = (_Float16)(sum[t][1] - (float)a[1]);
+            dd[0] = (_Float16)(sum[t][2] - (float)b[0]);
+            dd[1] = (_Float16)(sum[t][3] - (float)b[1]);
+            *reinterpret_cast<uint2 *>(mid[kParts - 1] + at) =
+                uint2{__builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, dd)};
+        }
     }
     __syncthreads();
-    u32x4 m[HB / 32];
+    // sums over 32 rows p for the two values of the row index's fifth bit,
+    // then over the p's
+    f32x4 z[NT];
 #pragma unroll
-    for (int p = 0; p < HB / 32; ++p)
-        m[p] = *reinterpret_cast<const u32x4 *>(mid + (16 * wv + r) * kPitch + (32 * p + 8 * g) * 2);
-    const float f = scale[e] / (float)HB;
-    const float *su_b = su + (size_t)e * rows + (size_t)br * HB;
-    const float *sv_b = sv + (size_t)e * cols + (size_t)bc * HB;
-    uint16_t *out = dense + (size_t)blockIdx.y * rows * cols;
+    for (int p = 0; p < NP; ++p) {
+        const int at = (16 * wv + r) * kPitch + (32 * p + 8 * g) * 2;
 #pragma unroll
-    for (int t = 0; t < HB / 16; ++t) {
-        f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int o = 0; o < 2; ++o) {
+            f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int p = 0; p < HB / 32; ++p) {
-            // signs of H_HB at row 16 t + r, rows 32 p + 8 g + j
-            const uint32_t flip = parity16(t & (2 * p + (g >> 1)));
-            u32x4 h;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t a = parity16(r & (8 * (g & 1) + 2 * j)) ^ flip;
-                const uint32_t b = parity16(r & (8 * (g & 1) + 2 * j + 1)) ^ flip;
-                h[j] = 0x3C003C00u | (a << 15) | (b << 31);
+            for (int q = 0; q < kParts; ++q) {
+                const u32x4 m = *reinterpret_cast<const u32x4 *>(mid[q] + at);
+                a = TR ? Act<false>::mfma(h32[o], m, a) : Act<false>::mfma(m, h32[o], a);
             }
-            z = TR ? Act<false>::mfma(h, m[p], z) : Act<false>::mfma(m[p], h, z);
+            z[2 * p + o] = a;
         }
-        // transposed: column 16 wv + r, rows 16 t + 4 g ..; else row 16 t + r,
-        // columns 16 wv + 4 g ..
-        const int row = TR ? 16 * t + 4 * g : 16 * t + r, col = TR ? 16 * wv + r : 16 * wv + 4 * g;
-        uint2 o;
-        uint16_t q[4];
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            q[i] = Act<BF>::store(z[i] * (f * su_b[TR ? row + i : row] * sv_b[TR ? col : col + i]));
-        o.x = q[0] | ((uint32_t)q[1] << 16);
-        o.y = q[2] | ((uint32_t)q[3] << 16);
-        const size_t at = TR ? ((size_t)bc * HB + col) * rows + (size_t)br * HB + row
-                             : ((size_t)br * HB + row) * cols + (size_t)bc * HB + col;
-        *reinterpret_cast<uint2 *>(out + at) = o;
+    for (int s = 2; s < NT; s <<= 1)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (!(t & s)) {
+                const f32x4 a = z[t], b = z[t + s];
+                z[t] = a + b;
+                z[t + s] = a - b;
+            }
+    // transposed: column 16 wv + r, rows 16 t + 4 g ..; else row 16 t + r,
+    // columns 16 wv + 4 g ..
+    const float *sv_b = sv + (size_t)e * cols + (size_t)bc * HB + 16 * wv;
+    float sv_r = 0.0f;
+    f32x4 sv_4 = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (TR)
+        sv_r = f * sv_b[r];
+    else
+        sv_4 = *reinterpret_cast<const f32x4u *>(sv_b + 4 * g);
+    __syncthreads();                         // the halves have been read
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        f32x4 v = z[t];
+        if (TR) {
+            const f32x4 s4 = *reinterpret_cast<const f32x4u *>(su_b + 16 * t + 4 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] *= sv_r * s4[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] *= su_t[t] * sv_4[i];
+        }
+        char *at = TR ? mid[0] + (16 * wv + r) * kPitch + (16 * t + 4 * g) * 2
+                      : mid[0] + (16 * t + r) * kPitch + (16 * wv + 4 * g) * 2;
+        *reinterpret_cast<uint2 *>(at) =
+            uint2{Act<BF>::store2(v[0], v[1]), Act<BF>::store2(v[2], v[3])};
+    }
+    __syncthreads();
+    // whole rows of the block to memory
+    const size_t pitch = TR ? rows : cols;
+    uint16_t *o0 = out + (TR ? (size_t)bc : (size_t)br) * HB * pitch +
+                   (TR ? (size_t)br : (size_t)bc) * HB;
+#pragma unroll
+    for (int i = 0; i < HB / 32; ++i) {
+        const int piece = i * HB * 4 + threadIdx.x, row = piece / (HB / 8);
+        const int c = piece % (HB / 8);
+        *reinterpret_cast<u32x4 *>(o0 + row * pitch + c * 8) =
+            *reinterpret_cast<const u32x4 *>(mid[0] + row * kPitch + c * 16);
     }
 }
 
 // ---- matrix product ----
 // y[n][m] = x[n][k] w[m][k]^T: the weights are the instruction's first operand
 // and the rows of x its second, so a lane's four results are consecutive
-// elements of one row of y.  A workgroup computes BM columns of y by BN rows;
-// 64 of k at a time pass through two buffers in shared memory, the next ones
-// loaded straight into it while these are used.  A load writes a wave's 64
-// pieces of 16 bytes in lane order, so the swizzle that spreads a column of
-// pieces over the banks is in which piece each lane fetches: piece s of row r
-// holds k piece s ^ (r & 7).
-template <int BM, int BN, int WM, int WN, bool BF>
-__global__ void __launch_bounds__(64 * WM * WN)
+// elements of one row of y.  A workgroup computes BM columns of y by BN rows.
+// Slices of 64 k (whole cache lines) pass through two places in shared memory,
+// loaded straight into them.  While the matrix units work on one half slice the
+// next one's operands are read into registers: those of x beside the present
+// ones, those of the weights over them, row by row as they are used up.  The one
+// barrier a slice stands where its second half has just been read: the slice's
+// place is free for the slice after the next, whose loads get the time of a whole
+// slice to land.  A load writes a wave's 64 pieces of 16 bytes in lane order, so
+// the swizzle that spreads rows over the banks is in which piece each lane
+// fetches: piece s of row r holds k piece s ^ spread(r), so that 16 rows of one
+// piece, 8 of two and 4 of four each meet no bank twice.
+__device__ __forceinline__ int spread(int row) {
+    return ((row << 1) & 4) | ((row >> 1) & 2) | ((row >> 3) & 1);
+}
+
+// Waits until at most `loads` of the wave's vector loads are under way and its
+// shared-memory reads are done (the counts' places in the instruction).
+template <int kLoads>
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((kLoads & 15) | (7 << 4) | ((kLoads >> 4) << 14));
+}
+
+template <int BM, int BN, int WM, int WN, bool BF, bool AD>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
 gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w, int64_t n,
             int m, int k, const int32_t *__restrict__ offsets, int g0, int ng, int m_tiles,
-            int total, AdapterArgs ad, const uint16_t *__restrict__ ad_b,
-            const uint16_t *__restrict__ v, uint16_t *__restrict__ y, int64_t ldy) {
-    constexpr int kThreads = 64 * WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
-    constexpr int kPieces = (BM + BN) * 8 / kThreads;     // 16-byte pieces a thread loads
-    __shared__ __align__(16) uint16_t buf[2][(BM + BN) * 64];
+            int total, AdapterArgs ad, const uint16_t *__restrict__ ad_b, bool wide_b,
+            const uint16_t *__restrict__ v, uint16_t *__restrict__ y, int64_t ldy, bool wide_y) {
+    constexpr int kThreads = 64 * WM * WN, SM = BM / WM, SN = BN / WN, TM = SM / 16, TN = SN / 16;
+    constexpr int kPiecesW = BM * 8 / kThreads, kPiecesX = BN * 8 / kThreads;
+    constexpr int kPieces = kPiecesW + kPiecesX;          // 16-byte pieces a thread loads a slice
+    constexpr int kSlice = (BM + BN) * 64, kRing = 2;
+    constexpr int kPitch = SM * 2 + 16;                   // bytes a row of y takes in the epilogue
+    static_assert(WM * WN * 16 * kPitch <= kRing * kSlice * 2, "the epilogue fits the ring");
+    __shared__ __align__(16) uint16_t ring[kRing * kSlice];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4, wm = wv % WM, wn = wv / WM;
     // consecutive workgroups go to different dies: give each die a run of tiles
@@ -156,8 +247,14 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
         const int per = total / 8, rest = total % 8, die = id % 8;
         id = die * per + (die < rest ? die : rest) + id / 8;
     }
-    const int mt = id % m_tiles;
-    int nt = id / m_tiles, e = 0;
+    // and order a run's tiles in panels eight tiles wide, so that the 32 tiles a
+    // die works on at a time share their operands in its cache in both
+    // directions (one row of 32 tiles fetches 2.75 times what 8 x 4 do)
+    const int n_tiles = total / m_tiles, panel = id / (8 * n_tiles);
+    const int wide = m_tiles - 8 * panel < 8 ? m_tiles - 8 * panel : 8;
+    id -= 8 * panel * n_tiles;
+    const int mt = 8 * panel + id % wide;
+    int nt = id / wide, e = 0;
     int64_t lo = 0, hi = n;
     if (offsets) {
         // the group that holds the nt-th tile of rows, groups in order
@@ -186,64 +283,106 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
         group_rows(offsets, g0 + e, n, lo, hi);
     }
     const int64_t row0 = lo + (int64_t)nt * BN;
-    const uint16_t *wg = w + (size_t)e * m * k;
-
-    const uint16_t *src[kPieces];
+    // the tile's operands from uniform bases that move along k, and 32-bit
+    // offsets of the thread's pieces
+    const char *w_at = reinterpret_cast<const char *>(w + ((size_t)e * m + (size_t)mt * BM) * k);
+    const char *x_at = reinterpret_cast<const char *>(x + row0 * ldx);
+    uint32_t piece_at[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        const int piece = i * kThreads + threadIdx.x, row = piece >> 3;
-        const int kp = (piece & 7) ^ (row & 7);
-        if (row < BM) {
-            int mr = mt * BM + row;
-            mr = mr < m ? mr : m - 1;        // past the edge: repeats, not stored
-            src[i] = wg + (size_t)mr * k + kp * 8;
+        const int q = (i < kPiecesW ? i : i - kPiecesW) * kThreads + threadIdx.x, row = q >> 3;
+        const int kp = ((q & 7) ^ spread(row)) * 16;
+        if (i < kPiecesW) {
+            const int left = m - mt * BM - 1;    // past the edge: repeats, not stored
+            piece_at[i] = (uint32_t)(row < left ? row : left) * (uint32_t)(k * 2) + kp;
         } else {
-            int64_t xr = row0 + row - BM;
-            xr = xr < hi ? xr : hi - 1;
-            src[i] = x + xr * ldx + kp * 8;
+            const int64_t left = hi - row0 - 1;
+            piece_at[i] = (uint32_t)(row < left ? row : left) * (uint32_t)(ldx * 2) + kp;
         }
     }
-    auto load = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void *)src[i],
-                (__attribute__((address_space(3))) void *)(&buf[b][(i * kThreads + wv * 64) * 8]),
-                16, 0, 0);
-            src[i] += 64;
-        }
+    const int steps = k / 64;
+    auto load_piece = [&](int i, int place) {
+        const int q = i < kPiecesW ? i : BM * 8 / kThreads + i - kPiecesW;
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void *)((i < kPiecesW ? w_at : x_at) +
+                                                             piece_at[i]),
+            (__attribute__((address_space(3))) void *)(ring + place * kSlice +
+                                                       (q * kThreads + wv * 64) * 8),
+            16, 0, 0);
+    };
+    // to the next slice; the last is repeated into the place that nobody reads
+    auto advance = [&](int loaded) {
+        const int by = loaded < steps ? 128 : 0;
+        w_at += by;
+        x_at += by;
+    };
+    u32x4 a[TM], b[2][TN];
+    const int at[2] = {(g ^ spread(r)) * 8, ((4 + g) ^ spread(r)) * 8};
+    const uint16_t *ra = ring + (wm * SM + r) * 64, *rb = ring + (BM + wn * SN + r) * 64;
+    auto read_a = [&](int i, int place, int half) {
+        a[i] = *reinterpret_cast<const u32x4 *>(ra + place * kSlice + 16 * i * 64 + at[half]);
+    };
+    auto read_b = [&](int j, int place, int half) {
+        b[half][j] = *reinterpret_cast<const u32x4 *>(rb + place * kSlice + 16 * j * 64 + at[half]);
     };
     f32x4 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = k / 64;
-    load(0);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) load_piece(i, 0);
+    advance(1);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) load_piece(i, 1);
+    advance(2);
+    wait_loads<kPieces>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < TN; ++j) read_b(j, 0, 0);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) read_a(i, 0, 0);
+    auto products = [&](int i, int half) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = Act<BF>::mfma(a[i], b[half][j], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     for (int s = 0; s < steps; ++s) {
-        __syncthreads();                     // this step's loads have landed, the other buffer is free
-        if (s + 1 < steps) load((s + 1) & 1);
-        const uint16_t *ba = buf[s & 1] + (size_t)(wm * (BM / WM)) * 64;
-        const uint16_t *bb = buf[s & 1] + (size_t)(BM + wn * (BN / WN)) * 64;
+        const int place = s & 1;
+        // the first half; the second is read
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int at = (((4 * h + g) ^ (r & 7)) * 8);
-            u32x4 a[TM], b[TN];
+        for (int i = 0; i < TM; ++i) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-                a[i] = *reinterpret_cast<const u32x4 *>(ba + (16 * i + r) * 64 + at);
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                b[j] = *reinterpret_cast<const u32x4 *>(bb + (16 * j + r) * 64 + at);
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = Act<BF>::mfma(a[i], b[j], acc[i][j]);
+            for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j) read_b(j, place, 1);
+            products(i, 0);
+            read_a(i, place, 1);
         }
+        // the second half; the next slice's first is read, the one after loaded
+        products(0, 1);
+        wait_loads<0>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        read_a(0, place ^ 1, 0);
+#pragma unroll
+        for (int i = 1; i < TM; ++i) {
+#pragma unroll
+            for (int j = (i - 1) * TN / (TM - 1); j < i * TN / (TM - 1); ++j)
+                read_b(j, place ^ 1, 0);
+#pragma unroll
+            for (int q = (i - 1) * kPieces / (TM - 1); q < i * kPieces / (TM - 1); ++q)
+                load_piece(q, place);
+            products(i, 1);
+            read_a(i, place ^ 1, 0);
+        }
+        advance(s + 3);
     }
-    const int m0 = mt * BM + wm * (BM / WM);
-    const int64_t t0 = row0 + wn * (BN / WN);
-    if (v) {
+    const int m0 = mt * BM + wm * SM;
+    const int64_t t0 = row0 + wn * SN;
+    if (AD) {
         // v b^T of each adapter that some row of the wave has, in ascending
         // order; its result is added where the row's adapter is this one, so
         // nothing of another adapter's values reaches a row
@@ -267,6 +406,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
             if (next == 0x7FFFFFFF) break;
             last = next;
             const uint16_t *ab = ad_b + (size_t)next * m * ad.rank;
+#pragma unroll
             for (int i = 0; i < TM; ++i) {
                 int mr = m0 + 16 * i + r;
                 mr = mr < m ? mr : m - 1;
@@ -274,14 +414,16 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
 #pragma unroll
                 for (int j = 0; j < TN; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 for (int kk = 0; kk < ad.rank_pad; kk += 32) {
-                    uint16_t q[8];
+                    const uint16_t *ap = ab + (size_t)mr * ad.rank + kk + 8 * g;
+                    u32x4 a = {0u, 0u, 0u, 0u};
+                    if (wide_b) {
+                        if (kk + 8 * g < ad.rank) a = *reinterpret_cast<const u32x4 *>(ap);
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        q[c] = kk + 8 * g + c < ad.rank
-                                   ? ab[(size_t)mr * ad.rank + kk + 8 * g + c] : (uint16_t)0;
-                    u32x4 a;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) a[c] = q[2 * c] | ((uint32_t)q[2 * c + 1] << 16);
+                        for (int c = 0; c < 8; ++c)
+                            if (kk + 8 * g + c < ad.rank)
+                                a[c >> 1] |= (uint32_t)ap[c] << (16 * (c & 1));
+                    }
 #pragma unroll
                     for (int j = 0; j < TN; ++j) {
                         int64_t tok = t0 + 16 * j + r;
@@ -291,27 +433,38 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
                     }
                 }
 #pragma unroll
-                for (int ii = 0; ii < TM; ++ii)
-                    if (ii == i)
+                for (int j = 0; j < TN; ++j)
 #pragma unroll
-                        for (int j = 0; j < TN; ++j)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                acc[ii][j][c] += idj[j] == next ? p[j][c] : 0.0f;
+                    for (int c = 0; c < 4; ++c) acc[i][j][c] += idj[j] == next ? p[j][c] : 0.0f;
             }
         }
     }
+    // 16 rows of y at a time through the wave's part of the ring, so that whole
+    // lines are written
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    char *out = reinterpret_cast<char *>(ring) + wv * 16 * kPitch;
+    constexpr int kPer = SM / 8;             // 16-byte pieces a row
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-        const int64_t tok = t0 + 16 * j + r;
-        if (tok >= hi) continue;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int col = m0 + 16 * i + 4 * g;
-            if (col >= m) continue;
-            uint16_t *o = y + tok * ldy + col;
+        for (int i = 0; i < TM; ++i)
+            *reinterpret_cast<uint2 *>(out + r * kPitch + (16 * i + 4 * g) * 2) =
+                uint2{Act<BF>::store2(acc[i][j][0], acc[i][j][1]),
+                      Act<BF>::store2(acc[i][j][2], acc[i][j][3])};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = Act<BF>::store(acc[i][j][c]);
+        for (int q = 0; q < 16 * kPer / 64; ++q) {
+            const int piece = q * 64 + lane, row = piece / kPer, c = piece % kPer * 8;
+            const u32x4 o = *reinterpret_cast<const u32x4 *>(out + row * kPitch + c * 2);
+            const int64_t tok = t0 + 16 * j + row;
+            if (tok >= hi || m0 + c >= m) continue;
+            uint16_t *yo = y + tok * ldy + m0 + c;
+            if (wide_y) {
+                *reinterpret_cast<u32x4 *>(yo) = o;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) yo[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+            }
         }
     }
 }
@@ -327,22 +480,15 @@ pack_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int k,
     for (int j = 0; j < 8; ++j) out[row * k + c + j] = x[row * ldx + c + j];
 }
 
-__global__ void __launch_bounds__(256)
-zero_rows_kernel(const int32_t *__restrict__ offsets, int groups, int64_t n, int m,
-                 uint16_t *__restrict__ y, int64_t ldy) {
-    const int64_t row = blockIdx.x;
-    if (row >= offsets[0] && row < offsets[groups]) return;
-    for (int c = threadIdx.x; c < m; c += 256) y[row * ldy + c] = 0;
-}
-
 template <int LV, int K, int HB>
 hipError_t dense_t(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
-                   bool transposed, bool bf16, uint16_t *dense, hipStream_t stream) {
+                   bool transposed, bool bf16, uint16_t *dense, uint16_t *y, int64_t ldy,
+                   hipStream_t stream) {
     const dim3 grid((unsigned)(w.rows / HB * (w.cols / HB)), (unsigned)ng);
 #define EXL3_DENSE(BF, TR)                                                                     \
     hipLaunchKernelGGL((dense_kernel<LV, K, HB, BF, TR>), grid, dim3(HB * 4), 0, stream,       \
                        w.packed, w.lv, w.rows, w.cols, w.K, w.scale, w.su, w.sv, offsets, n, g0, \
-                       dense)
+                       dense, y, ldy, w.groups)
     if (bf16 && transposed)
         EXL3_DENSE(true, true);
     else if (bf16)
@@ -357,18 +503,21 @@ hipError_t dense_t(const WeightArgs &w, const int32_t *offsets, int64_t n, int g
 
 template <int LV, int K>
 hipError_t dense_h(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
-                   bool transposed, bool bf16, uint16_t *dense, hipStream_t stream) {
+                   bool transposed, bool bf16, uint16_t *dense, uint16_t *y, int64_t ldy,
+                   hipStream_t stream) {
     return w.had == 128
-               ? dense_t<LV, K, 128>(w, offsets, n, g0, ng, transposed, bf16, dense, stream)
-               : dense_t<LV, K, 64>(w, offsets, n, g0, ng, transposed, bf16, dense, stream);
+               ? dense_t<LV, K, 128>(w, offsets, n, g0, ng, transposed, bf16, dense, y, ldy, stream)
+               : dense_t<LV, K, 64>(w, offsets, n, g0, ng, transposed, bf16, dense, y, ldy, stream);
 }
 
 }  // namespace
 
 hipError_t launch_dense(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
-                        bool transposed, bool bf16, uint16_t *dense, hipStream_t stream) {
+                        bool transposed, bool bf16, uint16_t *dense, void *yv, int64_t ldy,
+                        hipStream_t stream) {
+    uint16_t *y = static_cast<uint16_t *>(yv);
 #define EXL3_DENSE_K(LV, KK) \
-    case KK: return dense_h<LV, KK>(w, offsets, n, g0, ng, transposed, bf16, dense, stream)
+    case KK: return dense_h<LV, KK>(w, offsets, n, g0, ng, transposed, bf16, dense, y, ldy, stream)
     if (w.lv_kind == kLevelsMul1)
         switch (w.K) {
             EXL3_DENSE_K(kLevelsMul1, 1);
@@ -384,7 +533,7 @@ hipError_t launch_dense(const WeightArgs &w, const int32_t *offsets, int64_t n, 
             EXL3_DENSE_K(kLevelsHalves, 4);
         }
 #undef EXL3_DENSE_K
-    return dense_h<kLevelsTable, 0>(w, offsets, n, g0, ng, transposed, bf16, dense, stream);
+    return dense_h<kLevelsTable, 0>(w, offsets, n, g0, ng, transposed, bf16, dense, y, ldy, stream);
 }
 
 hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_t n, int m, int k,
@@ -394,28 +543,33 @@ hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_
     const AdapterArgs args = ad ? *ad : AdapterArgs{};
     const uint16_t *xx = static_cast<const uint16_t *>(x), *bb = static_cast<const uint16_t *>(b);
     uint16_t *yy = static_cast<uint16_t *>(y);
-#define EXL3_GEMM(BM, BN, WM, WN, BF)                                                            \
+    const bool wide_b = reinterpret_cast<uintptr_t>(b) % 16 == 0 && args.rank % 8 == 0;
+    const bool wide_y = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0;
+#define EXL3_GEMM_T(BM, BN, WM, WN, BF, AD)                                                      \
+    hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, BF, AD>), dim3((unsigned)total),             \
+                       dim3(64 * WM * WN), 0, stream, xx, ldx, dense, n, m, k, offsets, g0, ng,  \
+                       m_tiles, total, args, bb, wide_b, v, yy, ldy, wide_y)
+#define EXL3_GEMM(BM, BN, WM, WN)                                                                \
     do {                                                                                         \
         const int m_tiles = (m + BM - 1) / BM;                                                   \
         const int64_t n_tiles = offsets ? n / BN + ng : (n + BN - 1) / BN;                       \
         const int total = (int)(m_tiles * n_tiles);                                              \
-        hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, BF>), dim3((unsigned)total),             \
-                           dim3(64 * WM * WN), 0, stream, xx, ldx, dense, n, m, k, offsets, g0,  \
-                           ng, m_tiles, total, args, bb, v, yy, ldy);                            \
+        if (bf16 && ad)                                                                          \
+            EXL3_GEMM_T(BM, BN, WM, WN, true, true);                                             \
+        else if (bf16)                                                                           \
+            EXL3_GEMM_T(BM, BN, WM, WN, true, false);                                            \
+        else if (ad)                                                                             \
+            EXL3_GEMM_T(BM, BN, WM, WN, false, true);                                            \
+        else                                                                                     \
+            EXL3_GEMM_T(BM, BN, WM, WN, false, false);                                           \
     } while (0)
     // the large tile needs a workgroup for most compute units to be worth it
     const int64_t large = (int64_t)((m + 255) / 256) * ((n + 255) / 256);
-    if (!offsets && large >= n_cu / 2) {
-        if (bf16)
-            EXL3_GEMM(256, 256, 2, 4, true);
-        else
-            EXL3_GEMM(256, 256, 2, 4, false);
-    } else {
-        if (bf16)
-            EXL3_GEMM(128, 128, 2, 2, true);
-        else
-            EXL3_GEMM(128, 128, 2, 2, false);
-    }
+    if (!offsets && large >= 3 * n_cu / 4)
+        EXL3_GEMM(256, 256, 2, 4);
+    else
+        EXL3_GEMM(128, 128, 2, 2);
+#undef EXL3_GEMM_T
 #undef EXL3_GEMM
     return hipGetLastError();
 }
@@ -425,13 +579,6 @@ hipError_t launch_pack_rows(const void *x, int64_t ldx, int64_t n, int k, uint16
     const unsigned grid = (unsigned)((n * (k / 8) + 255) / 256);
     hipLaunchKernelGGL(pack_rows_kernel, dim3(grid), dim3(256), 0, stream,
                        static_cast<const uint16_t *>(x), ldx, n, k, out);
-    return hipGetLastError();
-}
-
-hipError_t launch_zero_rows(const int32_t *offsets, int groups, int64_t n, int m, void *y,
-                            int64_t ldy, hipStream_t stream) {
-    hipLaunchKernelGGL(zero_rows_kernel, dim3((unsigned)n), dim3(256), 0, stream, offsets, groups,
-                       n, m, static_cast<uint16_t *>(y), ldy);
     return hipGetLastError();
 }
 
