@@ -627,9 +627,9 @@ def test_refusals_leave_the_output(T, ctx):
     torch.cuda.synchronize()
     assert (y == 3.0).all()
     with T.Context(0, scratch_bytes=1000) as tiny:
-        wide = torch.zeros(100, 256, dtype=BF, device=DEV)
+        wide = torch.zeros(100, 128, dtype=BF, device=DEV)
         with pytest.raises(T.Exl3Error) as e:
-            tiny.linear(wide, w)
+            tiny.linear(wide, w, transpose=True)     # the direction that takes dense weights
         assert e.value.code == T.EXL3_ENOMEM
 
 

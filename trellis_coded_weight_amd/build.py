@@ -19,6 +19,10 @@ OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.hip", "viterbi_fwd.hip", "viterbi_fwd_f16.hip", "traceback.hip", "regularize.hip",
            "channel.hip", "ldlq.hip", "linear.hip", "dense.hip", "adapters.hip", "codebook.cpp"]
+# Matrix instructions on vector registers throughout: where a kernel has more than
+# 256 registers a lane, the compiler otherwise moves accumulators to and from the
+# accumulation registers in the product's inner loop.
+EXTRA = {"dense.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = [
@@ -42,7 +46,7 @@ def build(verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(OBJ_DIR, src + ".o")
-        cmd = [HIPCC, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [HIPCC, *COMMON, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
         if src.endswith(".cpp"):
             cmd[1:1] = ["-x", "hip"]
         _run(cmd, verbose)

@@ -821,9 +821,21 @@ bool rows_aligned(const void *p, int64_t ld) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && ld < (1 << 22);
 }
 
-// Few rows: the codes are decoded once for each 64 rows of a group, in the
-// kernel that multiplies them.  Many: the dense weights are written first.
-bool few_rows(int64_t n, int groups) { return n <= (int64_t)64 * groups; }
+// The three forms of a product.  Few rows a group: a workgroup per 16 rows of W
+// streams the codes once.  Some: tiles of 128 rows of x, the codes decoded once
+// a tile.  Many: the dense weights are written first, which pays when a group's
+// rows pass a few tiles; also the form of the other direction and of decoding by
+// table.
+enum Form { kFewRows, kTiles, kDense };
+
+Form form_of(const exl3::WeightArgs &w, bool transpose, int64_t n) {
+    if (transpose) return kDense;
+    if (n <= (int64_t)32 * w.groups) return kFewRows;
+    const bool tiles = w.lv_kind != exl3::kLevelsTable &&
+                       reinterpret_cast<uintptr_t>(w.packed) % 16 == 0;
+    if (tiles && n <= (int64_t)512 * w.groups) return kTiles;
+    return n <= (int64_t)64 * w.groups ? kFewRows : kDense;
+}
 
 // y = x W^T or x W, with v b^T of the adapters when ad is given (ad_b: their
 // matrices on the output's side [count][out][rank], v from launch_shrink).
@@ -841,7 +853,7 @@ struct Product {
     const void *ad_b;
     size_t v_at;               // of v in the workspace
     // set by plan_product
-    bool few;
+    Form form;
     int split, tiles, batch;
     size_t xh_at, xs_at, part_at, dense_at, xpack_at;
     bool pack;
@@ -850,19 +862,26 @@ struct Product {
 int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
     const exl3::WeightArgs &w = *p.w;
     const size_t n = (size_t)p.n;
-    p.few = !p.transpose && few_rows(p.n, w.groups);
-    if (p.few) {
-        const int units = (w.cols + exl3::kUnit - 1) / exl3::kUnit;
-        // eight waves take a unit each before the columns are split further; a
-        // split more costs a pass over the sums, and is taken while the
-        // workgroups are fewer than two a compute unit
-        const int64_t groups = (int64_t)(w.rows / 16) * w.groups;
-        p.split = (int)std::min<int64_t>((units + 7) / 8,
-                                         std::max<int64_t>(1, 2 * ctx->n_cu / groups));
-        const int64_t per = (p.n + w.groups - 1) / w.groups;
-        p.tiles = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+    p.form = form_of(w, p.transpose, p.n);
+    if (p.form != kDense) {
+        if (p.form == kFewRows) {
+            // eight waves take 256 columns each before the columns are split further;
+            // a split more costs a pass over the sums, and is taken while the
+            // workgroups are fewer than two a compute unit
+            const int64_t wgs = (int64_t)(w.rows / 16) * w.groups;
+            const int64_t per = (p.n + w.groups - 1) / w.groups;
+            p.split = (int)std::min<int64_t>((w.cols + 2047) / 2048,
+                                             std::max<int64_t>(1, 2 * ctx->n_cu / wgs));
+            p.tiles = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+        } else {
+            // in the same way, with 256 columns a split at least
+            const int64_t wgs = (int64_t)((w.rows + 127) / 128) *
+                                (p.offsets ? p.n / 128 + w.groups : (p.n + 127) / 128);
+            p.split = (int)std::max<int64_t>(1, std::min<int64_t>(w.cols / 256,
+                                                                  2 * ctx->n_cu / wgs));
+        }
         p.xh_at = c.take(n * w.cols * 2);
-        p.xs_at = c.take(n * units * sizeof(float));
+        p.xs_at = c.take(n * sizeof(float));
         p.part_at = c.take(n * w.rows * p.split * sizeof(float));
         return EXL3_OK;
     }
@@ -881,14 +900,18 @@ int run_product(exl3_ctx *ctx, const Product &p) {
     const exl3::WeightArgs &w = *p.w;
     char *ws = ctx->d_work;
     const uint16_t *v = p.ad ? reinterpret_cast<const uint16_t *>(ws + p.v_at) : nullptr;
-    if (p.few) {
+    if (p.form != kDense) {
         uint16_t *xh = reinterpret_cast<uint16_t *>(ws + p.xh_at);
         float *xs = reinterpret_cast<float *>(ws + p.xs_at);
         float *part = reinterpret_cast<float *>(ws + p.part_at);
         EXL3_HIP(ctx, exl3::launch_rotate(w, p.offsets, p.x, p.ldx, p.n, p.bf16, xh, xs,
                                           ctx->stream));
-        EXL3_HIP(ctx, exl3::launch_coded_rows(w, p.offsets, xh, xs, p.n, p.split, p.tiles, part,
-                                              ctx->stream));
+        if (p.form == kFewRows)
+            EXL3_HIP(ctx, exl3::launch_coded_rows(w, p.offsets, xh, xs, p.n, p.split, p.tiles,
+                                                  part, ctx->stream));
+        else
+            EXL3_HIP(ctx, exl3::launch_coded_tiles(w, p.offsets, xh, xs, p.n, p.split, part,
+                                                   ctx->stream));
         EXL3_HIP(ctx, exl3::launch_finish(w, p.offsets, part, p.split, p.n, p.bf16, p.ad, v, p.y,
                                           p.ldy, ctx->stream));
         return EXL3_OK;

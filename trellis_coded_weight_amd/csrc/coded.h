@@ -37,6 +37,7 @@ using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
+using f32x4u = float __attribute__((ext_vector_type(4), aligned(4)));   // unaligned
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
 // How levels are found; the values are template arguments of the kernels.
@@ -195,6 +196,27 @@ struct Act<true> {
     }
 };
 
+// Waits until at most `loads` of the wave's vector loads are under way and its
+// shared-memory reads are done (the counts' places in the instruction).
+template <int kLoads>
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((kLoads & 15) | (7 << 4) | ((kLoads >> 4) << 14));
+}
+
+// 16 bytes a lane straight into shared memory, at to + 16 lane.
+__device__ __forceinline__ void load_to_lds(const void *from, void *to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
+
+// The workgroup's barrier, across which neither memory accesses nor the
+// compiler's schedule move.
+__device__ __forceinline__ void barrier_in_place() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // The group (expert) of a row among `groups` ascending offsets[groups + 1]:
 // the number of groups that end at or before it (a row at or past the last
 // offset gives `groups`).  All 64 lanes of the wave take part.
@@ -221,10 +243,57 @@ __device__ __forceinline__ void group_rows(const int32_t *offsets, int e, int64_
     }
 }
 
-// ---- arguments and launchers of the products (linear.hip, dense.hip, adapters.hip) ----
+// Tiles of `per` rows of the groups g0 .. g0 + ng - 1, counted in order of the
+// groups (a group's last may be partly empty).  All 64 lanes take part.
+__device__ __forceinline__ int tiles_of_group(const int32_t *offsets, int e, bool in, int64_t n,
+                                              int per) {
+    int64_t a = 0, b = 0;
+    if (in) group_rows(offsets, e, n, a, b);
+    return b > a ? (int)((b - a + per - 1) / per) : 0;
+}
 
-// Columns that share one power-of-two scale of the transformed activations.
-constexpr int kUnit = 256;
+__device__ __forceinline__ int count_tiles(const int32_t *offsets, int g0, int ng, int64_t n,
+                                           int per) {
+    const int lane = threadIdx.x & 63;
+    int sum = 0;
+    for (int j = lane; j < ng + lane; j += 64) sum += tiles_of_group(offsets, g0 + j, j < ng, n, per);
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
+    return sum;
+}
+
+// The group that holds tile nt, which becomes the tile's number within it.
+__device__ __forceinline__ int group_of_tile(const int32_t *offsets, int g0, int ng, int64_t n,
+                                             int per, int &nt) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int j = 0; j < ng; j += 64) {
+        int sum = tiles_of_group(offsets, g0 + j + lane, j + lane < ng, n, per);
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const int o = __shfl_up(sum, s);
+            if (lane >= s) sum += o;
+        }
+        const uint64_t past = __ballot(before + sum > nt);
+        if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            const int prev = l ? __shfl(sum, l - 1) : 0;
+            nt -= before + prev;
+            return g0 + j + l;
+        }
+        before += __shfl(sum, 63);
+    }
+    return -1;
+}
+
+// Consecutive workgroups go to different dies: the number of a workgroup's tile
+// such that each die takes a run of the `total` tiles.
+__device__ __forceinline__ int tile_of_die(int id, int total) {
+    const int per = total / 8, rest = total % 8, die = id % 8;
+    return die * per + (die < rest ? die : rest) + id / 8;
+}
+
+// ---- arguments and launchers of the products (linear.hip, dense.hip, adapters.hip) ----
 
 struct WeightArgs {
     const uint32_t *packed;   // [groups][rows / 16][cols / 16][8 K]
@@ -241,7 +310,7 @@ struct AdapterArgs {
     int count, rank, rank_pad;
 };
 
-// x' = H_r (sv x) as binary16 [n][cols] with a scale [n][units] (a power of two).
+// x' = H_r (sv x) as binary16 [n][cols] with a scale [n] (a power of two).
 hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void *x, int64_t ldx,
                          int64_t n, bool bf16, uint16_t *xh, float *xs, hipStream_t stream);
 
@@ -249,6 +318,12 @@ hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void
 hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
                              const float *xs, int64_t n, int split, int tiles, float *part,
                              hipStream_t stream);
+
+// The same for 128 rows of x at a time, staged in shared memory.  packed is
+// 16-byte aligned and decoded by formula (lv_kind is not kLevelsTable).
+hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
+                              const float *xs, int64_t n, int split, float *part,
+                              hipStream_t stream);
 
 // y = su H_l (sum of the parts) scale / had, plus the adapters' products v B^T.
 hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const float *part, int split,

@@ -30,8 +30,6 @@ __device__ __forceinline__ uint32_t parity16(uint32_t v) { return __popc(v) & 1u
 // type.  Row-major and transposed output differ in the order of step 3's
 // operands: either way a lane holds four consecutive elements of the output.
 // The write of the weights bounds it.
-using f32x4u = float __attribute__((ext_vector_type(4), aligned(4)));
-
 template <int LV, int K, int HB, bool BF, bool TR>
 __global__ void __launch_bounds__(HB * 4, 4)
 dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols, int Kr,
@@ -213,19 +211,9 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
 // place is free for the slice after the next, whose loads get the time of a whole
 // slice to land.  A load writes a wave's 64 pieces of 16 bytes in lane order, so
 // the swizzle that spreads rows over the banks is in which piece each lane
-// fetches: piece s of row r holds k piece s ^ spread(r), so that 16 rows of one
-// piece, 8 of two and 4 of four each meet no bank twice.
-__device__ __forceinline__ int spread(int row) {
-    return ((row << 1) & 4) | ((row >> 1) & 2) | ((row >> 3) & 1);
-}
-
-// Waits until at most `loads` of the wave's vector loads are under way and its
-// shared-memory reads are done (the counts' places in the instruction).
-template <int kLoads>
-__device__ __forceinline__ void wait_loads() {
-    __builtin_amdgcn_s_waitcnt((kLoads & 15) | (7 << 4) | ((kLoads >> 4) << 14));
-}
-
+// fetches: piece s of row r holds k piece s ^ (r & 7), whose reads meet no bank
+// twice (4.2 cycles a read of 1 KiB measured, where a swizzle by three other
+// bits of r took 8.1).
 template <int BM, int BN, int WM, int WN, bool BF, bool AD>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w, int64_t n,
@@ -241,13 +229,14 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
     __shared__ __align__(16) uint16_t ring[kRing * kSlice];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4, wm = wv % WM, wn = wv / WM;
-    // consecutive workgroups go to different dies: give each die a run of tiles
-    int id = blockIdx.x;
-    {
-        const int per = total / 8, rest = total % 8, die = id % 8;
-        id = die * per + (die < rest ? die : rest) + id / 8;
+    // each die takes a run of tiles
+    if (offsets) {
+        const int tiles = count_tiles(offsets, g0, ng, n, BN) * m_tiles;
+        total = tiles < total ? tiles : total;
+        if ((int)blockIdx.x >= total) return;    // fewer tiles than the grid allows for
     }
-    // and order a run's tiles in panels eight tiles wide, so that the 32 tiles a
+    int id = tile_of_die(blockIdx.x, total);
+    // and orders them in panels eight tiles wide, so that the 32 tiles a
     // die works on at a time share their operands in its cache in both
     // directions (one row of 32 tiles fetches 2.75 times what 8 x 4 do)
     const int n_tiles = total / m_tiles, panel = id / (8 * n_tiles);
@@ -257,30 +246,10 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
     int nt = id / wide, e = 0;
     int64_t lo = 0, hi = n;
     if (offsets) {
-        // the group that holds the nt-th tile of rows, groups in order
-        int before = 0;
-        e = -1;
-        for (int j = 0; j < ng; j += 64) {
-            int64_t a = 0, b = 0;
-            if (j + lane < ng) group_rows(offsets, g0 + j + lane, n, a, b);
-            int sum = b > a ? (int)((b - a + BN - 1) / BN) : 0;
-#pragma unroll
-            for (int s = 1; s < 64; s <<= 1) {
-                const int o = __shfl_up(sum, s);
-                if (lane >= s) sum += o;
-            }
-            const uint64_t past = __ballot(before + sum > nt);
-            if (past) {
-                const int l = __ffsll((unsigned long long)past) - 1;
-                const int prev = l ? __shfl(sum, l - 1) : 0;
-                e = j + l;
-                nt -= before + prev;
-                break;
-            }
-            before += __shfl(sum, 63);
-        }
-        if (e < 0) return;                   // fewer tiles than the bound allows
-        group_rows(offsets, g0 + e, n, lo, hi);
+        e = group_of_tile(offsets, g0, ng, n, BN, nt);
+        if (e < 0) return;
+        group_rows(offsets, e, n, lo, hi);
+        e -= g0;
     }
     const int64_t row0 = lo + (int64_t)nt * BN;
     // the tile's operands from uniform bases that move along k, and 32-bit
@@ -291,7 +260,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
         const int q = (i < kPiecesW ? i : i - kPiecesW) * kThreads + threadIdx.x, row = q >> 3;
-        const int kp = ((q & 7) ^ spread(row)) * 16;
+        const int kp = ((q & 7) ^ (row & 7)) * 16;
         if (i < kPiecesW) {
             const int left = m - mt * BM - 1;    // past the edge: repeats, not stored
             piece_at[i] = (uint32_t)(row < left ? row : left) * (uint32_t)(k * 2) + kp;
@@ -303,12 +272,8 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
     const int steps = k / 64;
     auto load_piece = [&](int i, int place) {
         const int q = i < kPiecesW ? i : BM * 8 / kThreads + i - kPiecesW;
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void *)((i < kPiecesW ? w_at : x_at) +
-                                                             piece_at[i]),
-            (__attribute__((address_space(3))) void *)(ring + place * kSlice +
-                                                       (q * kThreads + wv * 64) * 8),
-            16, 0, 0);
+        load_to_lds((i < kPiecesW ? w_at : x_at) + piece_at[i],
+                    ring + place * kSlice + (q * kThreads + wv * 64) * 8);
     };
     // to the next slice; the last is repeated into the place that nobody reads
     auto advance = [&](int loaded) {
@@ -317,7 +282,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
         x_at += by;
     };
     u32x4 a[TM], b[2][TN];
-    const int at[2] = {(g ^ spread(r)) * 8, ((4 + g) ^ spread(r)) * 8};
+    const int at[2] = {(g ^ (r & 7)) * 8, ((4 + g) ^ (r & 7)) * 8};
     const uint16_t *ra = ring + (wm * SM + r) * 64, *rb = ring + (BM + wn * SN + r) * 64;
     auto read_a = [&](int i, int place, int half) {
         a[i] = *reinterpret_cast<const u32x4 *>(ra + place * kSlice + 16 * i * 64 + at[half]);
@@ -337,9 +302,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
     for (int i = 0; i < kPieces; ++i) load_piece(i, 1);
     advance(2);
     wait_loads<kPieces>();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    barrier_in_place();
 #pragma unroll
     for (int j = 0; j < TN; ++j) read_b(j, 0, 0);
 #pragma unroll
@@ -363,9 +326,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
         // the second half; the next slice's first is read, the one after loaded
         products(0, 1);
         wait_loads<0>();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        barrier_in_place();
         read_a(0, place ^ 1, 0);
 #pragma unroll
         for (int i = 1; i < TM; ++i) {
@@ -563,9 +524,15 @@ hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_
         else                                                                                     \
             EXL3_GEMM_T(BM, BN, WM, WN, false, false);                                           \
     } while (0)
-    // the large tile needs a workgroup for most compute units to be worth it
-    const int64_t large = (int64_t)((m + 255) / 256) * ((n + 255) / 256);
-    if (!offsets && large >= 3 * n_cu / 4)
+    // A round of large tiles, one a compute unit, takes about 12 parts of time
+    // where a round of small ones, two a compute unit, takes 8 and a half empty
+    // one 5 (k = 4096: 97, 65 and 40 us); a group's last tile counts as whole.
+    const int64_t large = (int64_t)((m + 255) / 256) * (offsets ? n / 256 + ng : (n + 255) / 256);
+    const int64_t small = (int64_t)((m + 127) / 128) * (offsets ? n / 128 + ng : (n + 127) / 128);
+    const int64_t rest = small % (2 * n_cu);
+    const int64_t cost_large = 12 * ((large + n_cu - 1) / n_cu);
+    const int64_t cost_small = 8 * (small / (2 * n_cu)) + (rest > n_cu ? 8 : rest > 0 ? 5 : 0);
+    if (cost_large <= cost_small)
         EXL3_GEMM(256, 256, 2, 4);
     else
         EXL3_GEMM(128, 128, 2, 2);

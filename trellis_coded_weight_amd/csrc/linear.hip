@@ -35,64 +35,110 @@ __device__ __forceinline__ void hadamard_lanes(float (&v)[E], int had) {
 }
 
 // ---- x' ----
-// Half a wave per row and unit of 256 columns, eight columns a lane.  x' is
-// held in binary16, whose products with the levels (binary16 themselves) the
-// matrix instruction sums in binary32.  The unit's scale is the power of two
-// that takes its largest magnitude into [2^13, 2^14): rounding then costs
-// 2^-12 of each value down to 2^-27 of the largest, whatever the range of the
-// activations (bfloat16's is far wider than binary16's).  A unit with a NaN or
-// an infinity becomes NaN throughout.
-template <bool BF>
-__global__ void __launch_bounds__(256)
-rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int cols, int had, int units,
+// A workgroup per row, eight columns a lane at a time, up to kKeep rounds of
+// which stay in registers until the row's largest magnitude is known (wider rows
+// are transformed a second time).  x' is held in binary16, whose products with
+// the levels (binary16 themselves) the matrix instruction sums in binary32.  The
+// row's scale is the power of two that takes its largest magnitude into
+// [2^13, 2^14): rounding then costs 2^-12 of each value down to 2^-27 of the
+// largest, whatever the range of the activations (bfloat16's is far wider than
+// binary16's).  A row with a NaN or an infinity becomes NaN throughout.
+constexpr int kKeep = 4;
+
+template <bool BF, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had, bool wide,
               const float *__restrict__ sv, const int32_t *__restrict__ offsets, int groups,
               uint16_t *__restrict__ xh, float *__restrict__ xs) {
-    const int lane = threadIdx.x & 63, pairs = (units + 1) / 2;
-    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t row = wave / pairs;
-    if (row >= n) return;
+    __shared__ float wave_big[THREADS / 64];
+    const int64_t row = blockIdx.x;
     if (offsets) {
         const int e = group_of_row(offsets, groups, row);
         sv += (size_t)(e < groups ? e : groups - 1) * cols;
     }
-    const int unit = (int)(wave - row * pairs) * 2 + (lane >> 5);
-    const int col = unit * kUnit + (lane & 31) * 8;
-    const bool in = col < cols;
-    float v[8];
+    const uint16_t *xr = x + row * ldx;
+    float v[kKeep][8];
+    auto transformed = [&](int col, float (&o)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = in ? Act<BF>::load(x[row * ldx + col + i]) * sv[col + i] : 0.0f;
-    hadamard_lanes(v, had);
-    float big = 0.0f;
-    bool bad = false;
+        for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+        if (col < cols) {
+            uint16_t q[8];
+            if (wide) {
+                const u32x4 w = *reinterpret_cast<const u32x4 *>(xr + col);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        big = fmaxf(big, fabsf(v[i]));
-        bad |= !(fabsf(v[i]) <= 3.402823466e38f);
+                for (int i = 0; i < 8; ++i) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[i] = xr[col + i];
+            }
+            const f32x4 s0 = *reinterpret_cast<const f32x4u *>(sv + col);
+            const f32x4 s1 = *reinterpret_cast<const f32x4u *>(sv + col + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = Act<BF>::load(q[i]) * (i < 4 ? s0[i] : s1[i - 4]);
+        }
+        hadamard_lanes(o, had);
+    };
+    const int rounds = (cols + THREADS * 8 - 1) / (THREADS * 8);
+    // magnitudes compare as integers; NaN and infinity come out on top
+    uint32_t big = 0;
+    auto largest = [&](const float (&o)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t m = __builtin_bit_cast(uint32_t, o[i]) & 0x7FFFFFFFu;
+            big = m > big ? m : big;
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < kKeep; ++c)
+        if (c < rounds) {
+            transformed((c * THREADS + threadIdx.x) * 8, v[c]);
+            largest(v[c]);
+        }
+    for (int c = kKeep; c < rounds; ++c) {
+        float o[8];
+        transformed((c * THREADS + threadIdx.x) * 8, o);
+        largest(o);
     }
-    for (int m = 1; m < 32; m <<= 1) {
-        big = fmaxf(big, __shfl_xor(big, m));
-        bad |= __shfl_xor((int)bad, m) != 0;
+    for (int m = 1; m < 64; m <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)big, m);
+        big = o > big ? o : big;
     }
+    if ((threadIdx.x & 63) == 0) wave_big[threadIdx.x >> 6] = __builtin_bit_cast(float, big);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) {
+        const uint32_t o = __builtin_bit_cast(uint32_t, wave_big[i]);
+        big = o > big ? o : big;
+    }
+    const bool bad = big >= 0x7F800000u;
     // exponent of the largest: big in [2^(ex - 127), 2^(ex - 126)); its scale
-    // 2^(ex - 140), held in the normal range
-    int ex = (int)(__builtin_bit_cast(uint32_t, big) >> 23);
+    // 2^(ex - 140), held in the normal range, and the inverse in two factors as
+    // it may pass the largest power
+    int ex = (int)(big >> 23);
     ex = ex < 14 ? 14 : ex;
     const float scale = __builtin_bit_cast(float, (uint32_t)(ex - 13) << 23);
-    // 1 / scale = 2^(140 - ex), in two factors as it may pass the largest power
-    const float up = __builtin_bit_cast(float, (uint32_t)(127 + (140 - ex) / 2) << 23);
-    const float up2 = __builtin_bit_cast(float, (uint32_t)(127 + (140 - ex) - (140 - ex) / 2) << 23);
-    if (!in) return;
-    u32x4 out;
+    const int back = 140 - ex;
+    const float up = __builtin_bit_cast(float, (uint32_t)(127 + back / 2) << 23);
+    const float up2 = __builtin_bit_cast(float, (uint32_t)(127 + back - back / 2) << 23);
+    auto store = [&](int col, const float (&o)[8]) {
+        if (col >= cols) return;
+        u32x4 out;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f16x2 h;
-        h[0] = (_Float16)(v[2 * i] * up * up2);
-        h[1] = (_Float16)(v[2 * i + 1] * up * up2);
-        out[i] = bad ? 0x7E007E00u : __builtin_bit_cast(uint32_t, h);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t h = Act<false>::store2(o[2 * i] * up * up2, o[2 * i + 1] * up * up2);
+            out[i] = bad ? 0x7E007E00u : h;
+        }
+        *reinterpret_cast<u32x4 *>(xh + row * cols + col) = out;
+    };
+#pragma unroll
+    for (int c = 0; c < kKeep; ++c)
+        if (c < rounds) store((c * THREADS + threadIdx.x) * 8, v[c]);
+    for (int c = kKeep; c < rounds; ++c) {
+        float o[8];
+        transformed((c * THREADS + threadIdx.x) * 8, o);
+        store((c * THREADS + threadIdx.x) * 8, o);
     }
-    *reinterpret_cast<u32x4 *>(xh + row * cols + col) = out;
-    if ((lane & 31) == 0) xs[row * units + unit] = scale;
+    if (threadIdx.x == 0) xs[row] = scale;
 }
 
 // ---- C x' ----
@@ -100,6 +146,9 @@ rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int cols, 
 // the split's units of 256 columns in turn, and their sums meet in shared
 // memory.  A wave decodes 16 x 64 weights into the operands of two steps and
 // uses them for NT tiles of 16 activation rows; x' comes from the caches.
+// Columns a wave takes at a time.
+constexpr int kUnit = 256;
+
 template <int LV, int K, int NT>
 __global__ void __launch_bounds__(512)
 coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols, int Kr,
@@ -117,15 +166,13 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
     const uint32_t *wrow = packed + ((size_t)e * row_tiles + rt) * (size_t)(cols / 16) * (8 * kk);
     for (int64_t t0 = lo; t0 < hi; t0 += 16 * NT) {
         const uint16_t *xr[NT];
-        const float *sr[NT];
-        f32x4 total[NT];
+        f32x4 acc[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             int64_t tok = t0 + 16 * t + r;
             tok = tok < hi ? tok : hi - 1;     // a row past the end repeats the last, unstored
             xr[t] = xh + tok * cols;
-            sr[t] = xs + tok * units;
-            total[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         for (int u = sp * 8 + wv; u < units; u += 8 * split) {
             const int c0 = u * kUnit;
@@ -134,9 +181,6 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
             for (int q = 0; q < 4; ++q)
                 if (c0 + 64 * q < cols)
                     load_row<K>(wrow + (size_t)(c0 / 16 + 4 * q + g) * (8 * kk), r, d[q]);
-            f32x4 acc[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (c0 + 64 * q >= cols) break;
@@ -150,15 +194,9 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
                     acc[t] = Act<false>::mfma(w[1], xp[1], acc[t]);
                 }
             }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float s = sr[t][u];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) total[t][i] += s * acc[t][i];
-            }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sums[wv][t][lane] = total[t];
+        for (int t = 0; t < NT; ++t) sums[wv][t][lane] = acc[t];
         __syncthreads();
         for (int i = threadIdx.x; i < NT * 64; i += 512) {
             const int t = i >> 6, l = i & 63;
@@ -168,9 +206,167 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
             const int64_t tok = t0 + 16 * t + (l & 15);
             if (tok < hi)
                 *reinterpret_cast<f32x4 *>(part + ((size_t)sp * n + tok) * rows + rt * 16 +
-                                           4 * (l >> 4)) = a;
+                                           4 * (l >> 4)) = a * xs[tok];
         }
         __syncthreads();
+    }
+}
+
+// ---- C x' for many rows ----
+// A workgroup of four waves per 128 rows of W, 16 NT rows of x' and split of the
+// columns.  A step of 64 columns of x' and of the codes' words comes straight
+// into one of four places in shared memory (three at K = 4), steps ahead.  A wave decodes
+// its 32 x 64 weights of the next step while the matrix instructions multiply
+// this step's with the 16 NT rows: 5.5 vector instructions a weight against
+// NT / 16 matrix instructions' time, so that at NT = 8 the decoding bounds it.
+// Piece s of 16 bytes of row r of x' holds piece p = s ^ (r & 7), counted so that
+// p = g + 4 f is what lane group g takes for its operand f, columns 16 g + 8 f on:
+// reads meet no bank twice.
+template <int LV, int K, int NT>
+__global__ void __launch_bounds__(256, 2)
+coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
+                   const int32_t *__restrict__ offsets, int groups,
+                   const uint16_t *__restrict__ xh, const float *__restrict__ xs, int64_t n,
+                   int split, int row_blocks, int total, float *__restrict__ part) {
+    constexpr int kRows = 16 * NT, kPieces = kRows * 8 / 256;   // of x', a thread and step
+    constexpr int kX = kRows * 128, kPlace = kX + 1024 * K;     // bytes of a place: x', words
+    // places: as many as leave two workgroups' worth of shared memory
+    constexpr int kRing = 4 * kPlace < 80 * 1024 ? 4 : 3;
+    __shared__ __align__(16) char ring[kRing * kPlace];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    // each die takes a run of tiles: row blocks of W one after the other for the
+    // same rows of x'
+    if (offsets) {
+        const int tiles = count_tiles(offsets, 0, groups, n, kRows) * row_blocks * split;
+        total = tiles < total ? tiles : total;
+        if ((int)blockIdx.x >= total) return;    // fewer tiles than the grid allows for
+    }
+    const int id = tile_of_die(blockIdx.x, total), rb = id % row_blocks;
+    int nt = id / row_blocks, e = 0;
+    const int sp = nt % split;
+    nt /= split;
+    int64_t lo = 0, hi = n;
+    if (offsets) {
+        e = group_of_tile(offsets, 0, groups, n, kRows, nt);
+        if (e < 0) return;
+        group_rows(offsets, e, n, lo, hi);
+    }
+    const int64_t t0 = lo + (int64_t)nt * kRows;
+    const int row_tiles = rows / 16, all = cols / 64;
+    const int first = (int)((int64_t)all * sp / split);
+    const int steps = (int)((int64_t)all * (sp + 1) / split) - first;
+
+    // x': pieces from a uniform base that moves along the columns
+    const char *x_at = reinterpret_cast<const char *>(xh + t0 * cols + (size_t)first * 64);
+    auto source_piece = [](int p) { return 2 * (p & 3) + (p >> 2); };
+    uint32_t piece_at[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int q = i * 256 + threadIdx.x, row = q >> 3;
+        const int64_t left = hi - t0 - 1;    // past the end: repeats, not stored
+        piece_at[i] = (uint32_t)(row < left ? row : left) * (uint32_t)(cols * 2) +
+                      source_piece((q & 7) ^ (row & 7)) * 16;
+    }
+    // words: 8 K pieces of 16 bytes a row tile and step, K loads of 64 lanes,
+    // one by each of the first K waves (the others repeat the last one's, so that
+    // every wave has as many loads under way)
+    const int word_wave = wv < K ? wv : K - 1;
+    const int wq = word_wave * 64 + lane;
+    int w_tile = rb * 8 + wq / (8 * K);
+    w_tile = w_tile < row_tiles ? w_tile : row_tiles - 1;
+    const char *w_at = reinterpret_cast<const char *>(packed) +
+                       (((size_t)e * row_tiles + w_tile) * (cols / 16) + (size_t)first * 4) * (32 * K) +
+                       wq % (8 * K) * 16;
+    int loaded = 0, fill = 0;
+    auto load = [&]() {
+        char *to = ring + fill * kPlace;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            load_to_lds(x_at + piece_at[i], to + (i * 256 + wv * 64) * 16);
+        load_to_lds(w_at, to + kX + word_wave * 1024);
+        ++loaded;
+        fill = fill + 1 < kRing ? fill + 1 : 0;
+        // past the last step: repeats it, into a place that nobody reads
+        x_at += loaded < steps ? 128 : 0;
+        w_at += loaded < steps ? 128 * K : 0;
+    };
+    // what a wave needs of a step: its two row tiles' words (then their levels)
+    // and the rows of x'
+    struct Operands {
+        uint32_t d[2][RowWords<K>::N];
+        u32x4 w[2][2], b[NT][2];
+    };
+    const int x_row = r * 128, p0 = (g ^ (r & 7)) * 16, p1 = ((g + 4) ^ (r & 7)) * 16;
+    auto read = [&](int place, Operands &o) {
+        const char *at = ring + place * kPlace;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            load_row<K>(reinterpret_cast<const uint32_t *>(at + kX +
+                                                           ((2 * wv + t) * 4 + g) * (32 * K)),
+                        r, o.d[t]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            o.b[j][0] = *reinterpret_cast<const u32x4 *>(at + x_row + j * 2048 + p0);
+            o.b[j][1] = *reinterpret_cast<const u32x4 *>(at + x_row + j * 2048 + p1);
+        }
+    };
+    auto decode = [&](Operands &o) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) decode_row<LV, K>(nullptr, r, o.d[t], lv, o.w[t]);
+    };
+    f32x4 acc[2][NT];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    Operands even, odd;
+    int here = 0;
+    auto step = [&](Operands &cur, Operands &next) {
+        // the next step has landed when only the loads of those after it are under way
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads<(kRing - 3) * (kPieces + 1)>();
+        barrier_in_place();
+        __builtin_amdgcn_sched_barrier(0);
+        // the next step's reads first: they finish under this step's decoding and
+        // products, which alternate
+        here = here + 1 < kRing ? here + 1 : 0;
+        read(here, next);
+        load();                              // over the step before this one
+        __builtin_amdgcn_sched_barrier(0);
+        decode(cur);
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    acc[t][j] = Act<false>::mfma(cur.w[t][f], cur.b[j][f], acc[t][j]);
+    };
+    if (steps > 0) {
+#pragma unroll
+        for (int i = 0; i < kRing - 1; ++i) load();
+        wait_loads<(kRing - 2) * (kPieces + 1)>();
+        barrier_in_place();
+        read(0, even);
+        int s = 0;
+        for (; s + 1 < steps; s += 2) {
+            step(even, odd);
+            step(odd, even);
+        }
+        if (s < steps) step(even, odd);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int row = rb * 128 + wv * 32 + t * 16 + 4 * g;
+        if (row >= rows) continue;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int64_t tok = t0 + 16 * j + r;
+            if (tok < hi)
+                *reinterpret_cast<f32x4 *>(part + ((size_t)sp * n + tok) * rows + row) =
+                    acc[t][j] * xs[tok];
+        }
     }
 }
 
@@ -248,15 +444,21 @@ hipError_t coded_rows_t(const WeightArgs &w, const int32_t *offsets, const uint1
 
 hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void *x, int64_t ldx,
                          int64_t n, bool bf16, uint16_t *xh, float *xs, hipStream_t stream) {
-    const int units = (w.cols + kUnit - 1) / kUnit;
-    const unsigned grid = (unsigned)((n * ((units + 1) / 2) + 3) / 4);
     const uint16_t *xx = static_cast<const uint16_t *>(x);
-    if (bf16)
-        hipLaunchKernelGGL((rotate_kernel<true>), dim3(grid), dim3(256), 0, stream, xx, ldx, n,
-                           w.cols, w.had, units, w.sv, offsets, w.groups, xh, xs);
+    const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % 8 == 0;
+#define EXL3_ROTATE(BF, THREADS)                                                               \
+    hipLaunchKernelGGL((rotate_kernel<BF, THREADS>), dim3((unsigned)n), dim3(THREADS), 0, stream, \
+                       xx, ldx, w.cols, w.had, wide, w.sv, offsets, w.groups, xh, xs)
+    // a round a row while that takes at most 512 lanes
+    if (bf16 && w.cols <= 2048)
+        EXL3_ROTATE(true, 256);
+    else if (bf16)
+        EXL3_ROTATE(true, 512);
+    else if (w.cols <= 2048)
+        EXL3_ROTATE(false, 256);
     else
-        hipLaunchKernelGGL((rotate_kernel<false>), dim3(grid), dim3(256), 0, stream, xx, ldx, n,
-                           w.cols, w.had, units, w.sv, offsets, w.groups, xh, xs);
+        EXL3_ROTATE(false, 512);
+#undef EXL3_ROTATE
     return hipGetLastError();
 }
 
@@ -281,6 +483,41 @@ hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const 
         }
 #undef EXL3_ROWS_K
     return coded_rows_t<kLevelsTable, 0>(w, offsets, xh, xs, n, split, tiles, part, stream);
+}
+
+hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
+                              const float *xs, int64_t n, int split, float *part,
+                              hipStream_t stream) {
+    constexpr int NT = 8;
+    const int row_blocks = (w.rows + 127) / 128;
+    const int64_t n_tiles = offsets ? n / (16 * NT) + w.groups : (n + 16 * NT - 1) / (16 * NT);
+    const int total = (int)(n_tiles * row_blocks * split);
+#define EXL3_TILES(LV, KK)                                                                      \
+    case KK:                                                                                    \
+        hipLaunchKernelGGL((coded_tiles_kernel<LV, KK, NT>), dim3((unsigned)total), dim3(256),  \
+                           0, stream, w.packed, w.lv, w.rows, w.cols, offsets, w.groups, xh, xs, \
+                           n, split, row_blocks, total, part);                                  \
+        break
+    if (w.lv_kind == kLevelsMul1)
+        switch (w.K) {
+            EXL3_TILES(kLevelsMul1, 1);
+            EXL3_TILES(kLevelsMul1, 2);
+            EXL3_TILES(kLevelsMul1, 3);
+            EXL3_TILES(kLevelsMul1, 4);
+            default: return hipErrorInvalidValue;
+        }
+    else if (w.lv_kind == kLevelsHalves)
+        switch (w.K) {
+            EXL3_TILES(kLevelsHalves, 1);
+            EXL3_TILES(kLevelsHalves, 2);
+            EXL3_TILES(kLevelsHalves, 3);
+            EXL3_TILES(kLevelsHalves, 4);
+            default: return hipErrorInvalidValue;
+        }
+    else
+        return hipErrorInvalidValue;
+#undef EXL3_TILES
+    return hipGetLastError();
 }
 
 hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const float *part, int split,
