@@ -38,6 +38,7 @@ using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using f32x4u = float __attribute__((ext_vector_type(4), aligned(4)));   // unaligned
+using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
 // How levels are found; the values are template arguments of the kernels.

@@ -217,10 +217,12 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
 // columns.  A step of 64 columns of x' and of the codes' words comes straight
 // into one of four places in shared memory (three at K = 4), steps ahead.  A wave decodes
 // its 32 x 64 weights of the next step while the matrix instructions multiply
-// this step's with the 16 NT rows: 5.5 vector instructions a weight against
-// NT / 16 matrix instructions' time, so that at NT = 8 the decoding bounds it.
-// Piece s of 16 bytes of row r of x' holds piece p = s ^ (r & 7), counted so that
-// p = g + 4 f is what lane group g takes for its operand f, columns 16 g + 8 f on:
+// this step's with the 16 NT rows.  The 32 x 32 x 16 instruction holds the issue
+// port for half of its 32 cycles, so about four vector instructions run under
+// each (the 16 x 16 x 32 one holds it throughout: the two kinds of work then add
+// up, measured).  A lane takes one row of one of two tiles for every 32 columns,
+// 16 weights, the operands of two products: columns 16 g + 8 f on, g its half of
+// the wave.  Piece s of 16 bytes of row r of x' holds its piece s ^ (r / 2 & 7):
 // reads meet no bank twice.
 template <int LV, int K, int NT>
 __global__ void __launch_bounds__(256, 2)
@@ -234,7 +236,7 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
     constexpr int kRing = 4 * kPlace < 80 * 1024 ? 4 : 3;
     __shared__ __align__(16) char ring[kRing * kPlace];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
+    const int r = lane & 31, g = lane >> 5;
     // each die takes a run of tiles: row blocks of W one after the other for the
     // same rows of x'
     if (offsets) {
@@ -259,14 +261,13 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
 
     // x': pieces from a uniform base that moves along the columns
     const char *x_at = reinterpret_cast<const char *>(xh + t0 * cols + (size_t)first * 64);
-    auto source_piece = [](int p) { return 2 * (p & 3) + (p >> 2); };
     uint32_t piece_at[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
         const int q = i * 256 + threadIdx.x, row = q >> 3;
         const int64_t left = hi - t0 - 1;    // past the end: repeats, not stored
         piece_at[i] = (uint32_t)(row < left ? row : left) * (uint32_t)(cols * 2) +
-                      source_piece((q & 7) ^ (row & 7)) * 16;
+                      ((q & 7) ^ ((row >> 1) & 7)) * 16;
     }
     // words: 8 K pieces of 16 bytes a row tile and step, K loads of 64 lanes,
     // one by each of the first K waves (the others repeat the last one's, so that
@@ -291,35 +292,43 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
         x_at += loaded < steps ? 128 : 0;
         w_at += loaded < steps ? 128 * K : 0;
     };
-    // what a wave needs of a step: its two row tiles' words (then their levels)
-    // and the rows of x'
+    // what a wave needs of a step: its rows' words (then their levels) and the
+    // rows of x', for two times 32 columns
+    constexpr int NJ = NT / 2;
     struct Operands {
         uint32_t d[2][RowWords<K>::N];
-        u32x4 w[2][2], b[NT][2];
+        u32x4 w[2][2], b[NJ][2][2];
     };
-    const int x_row = r * 128, p0 = (g ^ (r & 7)) * 16, p1 = ((g + 4) ^ (r & 7)) * 16;
+    int piece[2][2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+            piece[c][f] = r * 128 + ((4 * c + 2 * g + f) ^ ((r >> 1) & 7)) * 16;
+    const int words_at = kX + ((2 * wv + (r >> 4)) * 4 + g) * (32 * K);
     auto read = [&](int place, Operands &o) {
         const char *at = ring + place * kPlace;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-            load_row<K>(reinterpret_cast<const uint32_t *>(at + kX +
-                                                           ((2 * wv + t) * 4 + g) * (32 * K)),
-                        r, o.d[t]);
+        for (int c = 0; c < 2; ++c)
+            load_row<K>(reinterpret_cast<const uint32_t *>(at + words_at + 2 * c * 32 * K), r & 15,
+                        o.d[c]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            o.b[j][0] = *reinterpret_cast<const u32x4 *>(at + x_row + j * 2048 + p0);
-            o.b[j][1] = *reinterpret_cast<const u32x4 *>(at + x_row + j * 2048 + p1);
-        }
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    o.b[j][c][f] = *reinterpret_cast<const u32x4 *>(at + j * 4096 + piece[c][f]);
     };
     auto decode = [&](Operands &o) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) decode_row<LV, K>(nullptr, r, o.d[t], lv, o.w[t]);
+        for (int c = 0; c < 2; ++c) decode_row<LV, K>(nullptr, r & 15, o.d[c], lv, o.w[c]);
     };
-    f32x4 acc[2][NT];
+    f32x16 acc[NJ];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < 16; ++i) acc[j][i] = 0.0f;
     Operands even, odd;
     int here = 0;
     auto step = [&](Operands &cur, Operands &next) {
@@ -334,14 +343,23 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
         read(here, next);
         load();                              // over the step before this one
         __builtin_amdgcn_sched_barrier(0);
-        decode(cur);
+        decode(next);
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int f = 0; f < 2; ++f)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    acc[t][j] = Act<false>::mfma(cur.w[t][f], cur.b[j][f], acc[t][j]);
+                for (int j = 0; j < NJ; ++j)
+                    acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(f16x8, cur.w[c][f]),
+                        __builtin_bit_cast(f16x8, cur.b[j][c][f]), acc[j], 0, 0, 0);
+        // the first products cover the reads' latency
+        __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+#pragma unroll
+        for (int q = 0; q < 4 * NJ - 2; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x2, 12, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        }
     };
     if (steps > 0) {
 #pragma unroll
@@ -349,6 +367,7 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
         wait_loads<(kRing - 2) * (kPieces + 1)>();
         barrier_in_place();
         read(0, even);
+        decode(even);
         int s = 0;
         for (; s + 1 < steps; s += 2) {
             step(even, odd);
@@ -356,17 +375,20 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
         }
         if (s < steps) step(even, odd);
     }
+    // column (row of x') 32 j + r, rows 8 q + 4 g .. of the wave's 32
+    const int row0 = rb * 128 + wv * 32 + 4 * g;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int row = rb * 128 + wv * 32 + t * 16 + 4 * g;
-        if (row >= rows) continue;
+    for (int j = 0; j < NJ; ++j) {
+        const int64_t tok = t0 + 32 * j + r;
+        if (tok >= hi) continue;
+        const float s = xs[tok];
+        float *o = part + ((size_t)sp * n + tok) * rows + row0;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int64_t tok = t0 + 16 * j + r;
-            if (tok < hi)
-                *reinterpret_cast<f32x4 *>(part + ((size_t)sp * n + tok) * rows + row) =
-                    acc[t][j] * xs[tok];
-        }
+        for (int q = 0; q < 4; ++q)
+            if (row0 + 8 * q < rows)
+                *reinterpret_cast<f32x4 *>(o + 8 * q) =
+                    f32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2],
+                          acc[j][4 * q + 3]} * s;
     }
 }
 
