@@ -22,53 +22,55 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *p, bool wide) {
 // ---- v = alpha A x ----
 // A workgroup per 16 rows of x, and in grid.y the share of the rows' distinct
 // adapters it takes in turn (many requests: one each, so that they run beside
-// each other; long prompts: one share).  Eight waves split the contraction,
-// four steps of 32 loaded ahead of their use, and their sums meet in shared
-// memory.  The matrix instruction multiplies all 16 rows by each adapter and
-// keeps those that have it: its rate is far from the bound, which is reading A
-// once per 16 rows from the caches.  grid.z: up to two such products.
+// each other; long prompts: one share).  The waves split the contraction and
+// their sums meet in shared memory.  The matrix instruction multiplies all 16
+// rows by each adapter and keeps those that have it: its rate is far from the
+// bound, which is the loads' latency (a wave has a few steps only, all loaded at
+// once up to 4,096 columns and rank 16) and reading A once per 16 rows from the
+// caches.  grid.z: up to two such products.
 template <bool BF, int RT>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(RT <= 4 ? 1024 : 512)
 shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
-    __shared__ f32x4 sums[8][RT][64];
-    __shared__ int ids[16];
+    constexpr int kWaves = RT <= 4 ? 16 : 8;
+    __shared__ f32x4 sums[kWaves][RT][64];
     const ShrinkArgs p = blockIdx.z ? p1 : p0;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4, k = p.k;
     const int64_t t0 = (int64_t)blockIdx.x * 16;
-    if (threadIdx.x < 16) {
-        const int64_t tok = t0 + threadIdx.x;
-        const int id = tok < n ? ad.ids[tok] : -1;
-        ids[threadIdx.x] = id >= 0 && id < ad.count ? id : -1;
+    const int64_t tok = t0 + r < n ? t0 + r : n - 1;
+    int id_r = t0 + r < n ? ad.ids[tok] : -1;    // of the lane's row; -1: none
+    if (id_r < 0 || id_r >= ad.count) id_r = -1;
+    // rows that are the first of their adapter
+    bool seen = id_r < 0 || lane >= 16;
+#pragma unroll
+    for (int q = 0; q < 15; ++q) {
+        const int other = __shfl(id_r, q);
+        seen |= q < r && other == id_r;
     }
-    __syncthreads();
+    uint32_t firsts = (uint32_t)__ballot(!seen) & 0xFFFFu;
     if (blockIdx.y == 0) {
         // rows without an adapter, and the padding that no tile of ranks covers
-        for (int i = threadIdx.x; i < 16 * ad.rank_pad; i += 512) {
-            const int t = i / ad.rank_pad, c = i % ad.rank_pad;
-            if (t0 + t < n && (ids[t] < 0 || c >= 16 * RT))
-                p.v[(t0 + t) * ad.rank_pad + c] = 0;
-        }
+        for (int c = 16 * RT + 4 * (wv * 4 + g); c < ad.rank_pad; c += 16 * kWaves)
+            if (t0 + r < n) *reinterpret_cast<uint2 *>(p.v + tok * ad.rank_pad + c) = uint2{0u, 0u};
+        for (int c = 4 * (wv * 4 + g); c < ad.rank_pad; c += 16 * kWaves)
+            if (t0 + r < n && id_r < 0)
+                *reinterpret_cast<uint2 *>(p.v + tok * ad.rank_pad + c) = uint2{0u, 0u};
     }
-    const int64_t tok = t0 + r < n ? t0 + r : n - 1;
     const uint16_t *xr = p.x + tok * p.ldx + 8 * g;
-    int turn = 0;
-    for (int s = 0; s < 16; ++s) {
-        const int id = ids[s];
-        bool seen = id < 0;
-        for (int q = 0; q < s; ++q) seen |= ids[q] == id;
-        if (seen) continue;
-        if (turn++ % (int)gridDim.y != (int)blockIdx.y) continue;
+    uint32_t turn = 0;
+    for (; firsts; firsts &= firsts - 1, ++turn) {
+        if ((turn & (gridDim.y - 1)) != blockIdx.y) continue;      // gridDim.y: a power of two
+        const int id = __shfl(id_r, __ffs(firsts) - 1);
         const uint16_t *ar = p.a + (size_t)id * ad.rank * k + 8 * g;
         f32x4 acc[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr int U = RT <= 4 ? 4 : 2;
-        for (int c0 = wv * 32; c0 < k; c0 += 256 * U) {
+        constexpr int U = RT == 1 ? 8 : RT == 8 ? 2 : 4;
+        for (int c0 = wv * 32; c0 < k; c0 += 32 * kWaves * U) {
             u32x4 xv[U], av[U][RT];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const int c = c0 + 256 * j;
+                const int c = c0 + 32 * kWaves * j;
                 xv[j] = u32x4{0u, 0u, 0u, 0u};
                 if (c < k) xv[j] = load8(xr + c, p.wide_x);
 #pragma unroll
@@ -86,20 +88,18 @@ shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) sums[wv][t][lane] = acc[t];
         __syncthreads();
-        for (int i = threadIdx.x; i < RT * 64; i += 512) {
-            const int t = i >> 6, l = i & 63;
-            f32x4 z = sums[0][t][l];
+        if (wv < RT) {                           // a wave a tile of ranks
+            f32x4 z = sums[0][wv][lane];
 #pragma unroll
-            for (int w = 1; w < 8; ++w) z += sums[w][t][l];
-            const int c = 16 * t + 4 * (l >> 4);
-            if (ids[l & 15] == id && c < ad.rank_pad) {
+            for (int w = 1; w < kWaves; ++w) z += sums[w][wv][lane];
+            const int c = 16 * wv + 4 * g;
+            if (id_r == id && c < ad.rank_pad) {
                 const float al = ad.alpha[id];
-                const int64_t to = t0 + (l & 15);
                 const uint32_t lo = Act<BF>::store2(al * z[0], al * z[1]);
                 const uint32_t hi = Act<BF>::store2(al * z[2], al * z[3]);
-                *reinterpret_cast<uint2 *>(p.v + to * ad.rank_pad + c) = uint2{lo, hi};
+                *reinterpret_cast<uint2 *>(p.v + tok * ad.rank_pad + c) = uint2{lo, hi};
                 if (p.vt) {
-                    uint16_t *o = p.vt + (size_t)c * p.ldvt + to;
+                    uint16_t *o = p.vt + (size_t)c * p.ldvt + tok;
                     o[0] = (uint16_t)lo;
                     o[p.ldvt] = (uint16_t)(lo >> 16);
                     o[2 * p.ldvt] = (uint16_t)hi;
@@ -138,14 +138,16 @@ transpose16_kernel(TransposeArgs t0, TransposeArgs t1, int count) {
 // 4 r + c of tile c).  Rows of other adapters enter as zeros on both sides,
 // chosen and not multiplied, so that whatever they hold stays out; blocks of
 // 32 rows without the adapter are passed over.  The rows are split in parts,
-// summed in order afterwards: the result does not depend on scheduling.
+// those that have the adapter are summed in order afterwards: the result does
+// not depend on scheduling.
 // grid: blocks of 256 columns of the first product, then of the second;
 // adapters; parts.
 constexpr int kGradBlocks = 16;            // blocks of 32 rows whose adapters are read at once
 
 template <bool BF, int RT>
 __global__ void __launch_bounds__(256)
-adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t per_split) {
+adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t per_split,
+                    uint8_t *__restrict__ used) {
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4, id = blockIdx.y;
     const int first = (g0.k + 255) / 256;
@@ -213,6 +215,7 @@ adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t
             for (int c = 0; c < 4; ++c) acc[t][c] = Act<BF>::mfma(u, b[c], acc[t][c]);
         }
     };
+    bool any = false;
     for (int64_t c0 = t_lo; c0 < t_hi; c0 += 32 * kGradBlocks) {
         // which rows of each block have the adapter: bits of 16 words, one a lane
         uint32_t mine = 0;
@@ -225,6 +228,7 @@ adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t
         }
         uint64_t left = __ballot(mine != 0);
         if (!left) continue;
+        any = true;
         Step s[2];
         int b = __ffsll((unsigned long long)left) - 1;
         left &= left - 1;
@@ -238,6 +242,8 @@ adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t
         }
         use(s[0]);
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) used[blockIdx.z * ad.count + id] = any;
+    if (!any) return;
     // column j0 + 4 r + c, ranks 16 t + 4 g ..
     float *o = p.part + ((size_t)blockIdx.z * ad.count + id) * ad.rank * p.k;
 #pragma unroll
@@ -260,13 +266,16 @@ adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t
 // The parts' sums of both products (grid.y), four elements a thread.
 template <bool BF>
 __global__ void __launch_bounds__(256)
-adapter_sum_kernel(GradArgs g0, GradArgs g1, int splits, int count, int rank) {
+adapter_sum_kernel(GradArgs g0, GradArgs g1, int splits, int count, int rank,
+                   const uint8_t *__restrict__ used) {
     const GradArgs p = blockIdx.y ? g1 : g0;
     const size_t all = (size_t)count * rank * p.k;
     const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= all) return;
-    f32x4 s = *reinterpret_cast<const f32x4 *>(p.part + i);
-    for (int q = 1; q < splits; ++q) s += *reinterpret_cast<const f32x4 *>(p.part + q * all + i);
+    const int id = (int)(i / ((size_t)rank * p.k));
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q = 0; q < splits; ++q)
+        if (used[q * count + id]) s += *reinterpret_cast<const f32x4 *>(p.part + q * all + i);
     const uint32_t lo = Act<BF>::store2(s[0], s[1]), hi = Act<BF>::store2(s[2], s[3]);
     uint16_t *o = p.out + i;
     if (p.wide_out) {
@@ -292,7 +301,16 @@ hipError_t launch_shrink(const AdapterArgs &ad, const ShrinkArgs *p, int product
     const unsigned tiles = (unsigned)((n + 15) / 16);
     // up to 16 distinct adapters a tile: a workgroup each while there are few tiles
     const dim3 grid(tiles, tiles <= 32 ? 16u : tiles <= 128 ? 4u : 1u, (unsigned)products);
-#define EXL3_SHRINK(RT)                                                                             do {                                                                                                if (bf16)                                                                                           hipLaunchKernelGGL((shrink_kernel<true, RT>), grid, dim3(512), 0, stream, ad, q[0],                                q[1], n);                                                                else                                                                                                hipLaunchKernelGGL((shrink_kernel<false, RT>), grid, dim3(512), 0, stream, ad,                                     q[0], q[1], n);                                                      } while (0)
+#define EXL3_SHRINK(RT)                                                                     \
+    do {                                                                                    \
+        const dim3 block(RT <= 4 ? 1024 : 512);                                             \
+        if (bf16)                                                                           \
+            hipLaunchKernelGGL((shrink_kernel<true, RT>), grid, block, 0, stream, ad, q[0], \
+                               q[1], n);                                                    \
+        else                                                                                \
+            hipLaunchKernelGGL((shrink_kernel<false, RT>), grid, block, 0, stream, ad, q[0],\
+                               q[1], n);                                                    \
+    } while (0)
     if (ad.rank <= 16)
         EXL3_SHRINK(1);
     else if (ad.rank <= 32)
@@ -315,14 +333,13 @@ hipError_t launch_transpose16(const TransposeArgs *t, int arrays, int count, hip
 }
 
 int adapter_grad_splits(int64_t n, int count) {
-    // parts of 512 rows, one round of reading their adapters, up to 16 parts;
-    // many adapters fill the chip without
-    const int64_t s = (n + 32 * kGradBlocks - 1) / (32 * kGradBlocks), most = 64 / count;
-    return (int)(s < 1 || most < 1 ? 1 : s < most ? (s < 16 ? s : 16) : most < 16 ? most : 16);
+    // parts of 128 rows, up to 32 of them; many adapters fill the chip with fewer
+    const int64_t s = (n + 127) / 128, most = 128 / count;
+    return (int)(s < 1 || most < 1 ? 1 : s < most ? (s < 32 ? s : 32) : most < 32 ? most : 32);
 }
 
 hipError_t launch_adapter_grad(const AdapterArgs &ad, const GradArgs *p, int products, int64_t n,
-                               bool bf16, int splits, hipStream_t stream) {
+                               bool bf16, int splits, uint8_t *used, hipStream_t stream) {
     GradArgs q[2];
     for (int i = 0; i < 2; ++i) {
         q[i] = p[i < products ? i : 0];
@@ -332,7 +349,15 @@ hipError_t launch_adapter_grad(const AdapterArgs &ad, const GradArgs *p, int pro
     const int64_t per = ((n + splits - 1) / splits + 31) / 32 * 32;
     const int blocks = (q[0].k + 255) / 256 + (products > 1 ? (q[1].k + 255) / 256 : 0);
     const dim3 grid((unsigned)blocks, (unsigned)ad.count, (unsigned)splits);
-#define EXL3_GRAD(RT)                                                                                do {                                                                                                 if (bf16)                                                                                            hipLaunchKernelGGL((adapter_grad_kernel<true, RT>), grid, dim3(256), 0, stream, ad,                                 q[0], q[1], n, per);                                                      else                                                                                                 hipLaunchKernelGGL((adapter_grad_kernel<false, RT>), grid, dim3(256), 0, stream, ad,                                q[0], q[1], n, per);                                                  } while (0)
+#define EXL3_GRAD(RT)                                                                       \
+    do {                                                                                    \
+        if (bf16)                                                                           \
+            hipLaunchKernelGGL((adapter_grad_kernel<true, RT>), grid, dim3(256), 0, stream, \
+                               ad, q[0], q[1], n, per, used);                               \
+        else                                                                                \
+            hipLaunchKernelGGL((adapter_grad_kernel<false, RT>), grid, dim3(256), 0, stream,\
+                               ad, q[0], q[1], n, per, used);                               \
+    } while (0)
     if (ad.rank <= 16)
         EXL3_GRAD(1);
     else if (ad.rank <= 32)
@@ -348,10 +373,10 @@ hipError_t launch_adapter_grad(const AdapterArgs &ad, const GradArgs *p, int pro
     const unsigned groups = (unsigned)(((size_t)ad.count * ad.rank * k / 4 + 255) / 256);
     if (bf16)
         hipLaunchKernelGGL((adapter_sum_kernel<true>), dim3(groups, (unsigned)products), dim3(256),
-                           0, stream, q[0], q[1], splits, ad.count, ad.rank);
+                           0, stream, q[0], q[1], splits, ad.count, ad.rank, used);
     else
         hipLaunchKernelGGL((adapter_sum_kernel<false>), dim3(groups, (unsigned)products),
-                           dim3(256), 0, stream, q[0], q[1], splits, ad.count, ad.rank);
+                           dim3(256), 0, stream, q[0], q[1], splits, ad.count, ad.rank, used);
     return hipGetLastError();
 }
 

@@ -120,6 +120,9 @@ struct exl3_ctx {
     size_t work_cap = 0;
     void *old_work[64] = {};
     int n_old = 0;
+    // arrival counts of the products' workgroups, zero between calls
+    uint32_t *d_count = nullptr;
+    size_t count_cap = 0;
     std::string err;
     // optional per-launch timing (HIP events on the context's stream)
     struct Timed {
@@ -689,15 +692,21 @@ struct Carve {
     }
 };
 
-int work_space(exl3_ctx *ctx, size_t bytes) {
-    if (bytes <= ctx->work_cap) return EXL3_OK;
+int refuse_in_capture(exl3_ctx *ctx) {
     hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(ctx->stream, &st) != hipSuccess) (void)hipGetLastError();
     if (st != hipStreamCaptureStatusNone)
         return fail(ctx, EXL3_ENOMEM,
-                    "the workspace (%zu bytes) would have to grow to %zu during a capture: make "
-                    "the call once before it", ctx->work_cap, bytes);
+                    "the workspace would have to grow during a capture: make the call once "
+                    "before it");
     if (ctx->n_old == 64) return fail(ctx, EXL3_ENOMEM, "the workspace has grown 64 times");
+    return EXL3_OK;
+}
+
+int work_space(exl3_ctx *ctx, size_t bytes) {
+    if (bytes <= ctx->work_cap) return EXL3_OK;
+    int rc;
+    if ((rc = refuse_in_capture(ctx)) != EXL3_OK) return rc;
     // twice the last where there is room, so that what is kept stays below what is used
     size_t want = std::max(bytes, 2 * ctx->work_cap);
     void *p = nullptr;
@@ -715,6 +724,29 @@ int work_space(exl3_ctx *ctx, size_t bytes) {
     if (ctx->d_work) ctx->old_work[ctx->n_old++] = ctx->d_work;
     ctx->d_work = static_cast<char *>(p);
     ctx->work_cap = want;
+    return EXL3_OK;
+}
+
+int count_space(exl3_ctx *ctx, size_t counts) {
+    if (counts <= ctx->count_cap) return EXL3_OK;
+    int rc;
+    if ((rc = refuse_in_capture(ctx)) != EXL3_OK) return rc;
+    const size_t want = std::max<size_t>(std::max(counts, 2 * ctx->count_cap), 4096);
+    void *p = nullptr;
+    hipError_t e = hipMalloc(&p, want * sizeof(uint32_t));
+    if (e != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(ctx, EXL3_ENOMEM, "device allocation of %zu bytes failed: %s",
+                    want * sizeof(uint32_t), hipGetErrorString(e));
+    }
+    e = hipMemsetAsync(p, 0, want * sizeof(uint32_t), ctx->stream);
+    if (e != hipSuccess) {
+        (void)hipFree(p);
+        return fail(ctx, EXL3_EHIP, "hipMemsetAsync failed: %s", hipGetErrorString(e));
+    }
+    if (ctx->d_count) ctx->old_work[ctx->n_old++] = ctx->d_count;
+    ctx->d_count = static_cast<uint32_t *>(p);
+    ctx->count_cap = want;
     return EXL3_OK;
 }
 
@@ -821,16 +853,16 @@ bool rows_aligned(const void *p, int64_t ld) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 && ld < (1 << 22);
 }
 
-// The three forms of a product.  Few rows a group: a workgroup per 16 rows of W
-// streams the codes once.  Some: tiles of 128 rows of x, the codes decoded once
-// a tile.  Many: the dense weights are written first, which pays when a group's
+// The three forms of a product.  Few rows a group: workgroups stream the codes
+// once for 16 rows.  Some: tiles of 32 to 128 rows of x, the codes decoded once a
+// tile.  Many: the dense weights are written first, which pays when a group's
 // rows pass a few tiles; also the form of the other direction and of decoding by
 // table.
 enum Form { kFewRows, kTiles, kDense };
 
 Form form_of(const exl3::WeightArgs &w, bool transpose, int64_t n) {
     if (transpose) return kDense;
-    if (n <= (int64_t)32 * w.groups) return kFewRows;
+    if (n <= (int64_t)16 * w.groups) return kFewRows;
     const bool tiles = w.lv_kind != exl3::kLevelsTable &&
                        reinterpret_cast<uintptr_t>(w.packed) % 16 == 0;
     if (tiles && n <= (int64_t)512 * w.groups) return kTiles;
@@ -854,9 +886,9 @@ struct Product {
     size_t v_at;               // of v in the workspace
     // set by plan_product
     Form form;
-    int split, tiles, batch;
+    int split, run, per, batch;
     size_t xh_at, xs_at, part_at, dense_at, xpack_at;
-    bool pack;
+    bool pack, own_x, finish;
 };
 
 int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
@@ -865,23 +897,32 @@ int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
     p.form = form_of(w, p.transpose, p.n);
     if (p.form != kDense) {
         if (p.form == kFewRows) {
-            // eight waves take 256 columns each before the columns are split further;
-            // a split more costs a pass over the sums, and is taken while the
-            // workgroups are fewer than two a compute unit
-            const int64_t wgs = (int64_t)(w.rows / 16) * w.groups;
-            const int64_t per = (p.n + w.groups - 1) / w.groups;
-            p.split = (int)std::min<int64_t>((w.cols + 2047) / 2048,
-                                             std::max<int64_t>(1, 2 * ctx->n_cu / wgs));
-            p.tiles = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+            // a wave has 256 columns; a workgroup up to four tiles of rows, as many as
+            // leave two workgroups a compute unit (12288 x 4096 at K = 4: 13.8 us with
+            // three, 15.7 with one, 15.2 with six)
+            p.split = (w.cols + 2047) / 2048;
+            const int64_t tiles = (int64_t)(w.rows / 16) * p.split * w.groups;
+            p.run = (int)std::min<int64_t>(4, (tiles + 2 * ctx->n_cu - 1) / (2 * ctx->n_cu));
+            // up to four rows a group the kernel transforms x itself, and finishes y
+            // itself where the workgroups run all at once
+            p.own_x = p.n <= (int64_t)4 * w.groups;
+            p.finish = p.own_x && tiles <= ctx->n_cu;
         } else {
-            // in the same way, with 256 columns a split at least
+            // about two workgroups a compute unit, with 256 columns a split at least
+            const int64_t avg = (p.n + w.groups - 1) / w.groups;
+            p.per = avg <= 32 ? 32 : avg <= 64 ? 64 : 128;
             const int64_t wgs = (int64_t)((w.rows + 127) / 128) *
-                                (p.offsets ? p.n / 128 + w.groups : (p.n + 127) / 128);
+                                (p.offsets ? p.n / p.per + w.groups : (p.n + p.per - 1) / p.per);
             p.split = (int)std::max<int64_t>(1, std::min<int64_t>(w.cols / 256,
                                                                   2 * ctx->n_cu / wgs));
         }
-        p.xh_at = c.take(n * w.cols * 2);
-        p.xs_at = c.take(n * sizeof(float));
+        if (p.finish) {
+            int rc;
+            if ((rc = count_space(ctx, (size_t)w.groups * ((w.rows + 127) / 128))) != EXL3_OK)
+                return rc;
+        }
+        p.xh_at = p.own_x ? 0 : c.take(n * w.cols * 2);
+        p.xs_at = p.own_x ? 0 : c.take(n * sizeof(float));
         p.part_at = c.take(n * w.rows * p.split * sizeof(float));
         return EXL3_OK;
     }
@@ -904,14 +945,20 @@ int run_product(exl3_ctx *ctx, const Product &p) {
         uint16_t *xh = reinterpret_cast<uint16_t *>(ws + p.xh_at);
         float *xs = reinterpret_cast<float *>(ws + p.xs_at);
         float *part = reinterpret_cast<float *>(ws + p.part_at);
-        EXL3_HIP(ctx, exl3::launch_rotate(w, p.offsets, p.x, p.ldx, p.n, p.bf16, xh, xs,
-                                          ctx->stream));
-        if (p.form == kFewRows)
-            EXL3_HIP(ctx, exl3::launch_coded_rows(w, p.offsets, xh, xs, p.n, p.split, p.tiles,
-                                                  part, ctx->stream));
-        else
-            EXL3_HIP(ctx, exl3::launch_coded_tiles(w, p.offsets, xh, xs, p.n, p.split, part,
+        if (!p.own_x)
+            EXL3_HIP(ctx, exl3::launch_rotate(w, p.offsets, p.x, p.ldx, p.n, p.bf16, xh, xs,
+                                              ctx->stream));
+        if (p.form == kFewRows) {
+            const exl3::RowsArgs a{p.own_x ? nullptr : xh, xs, p.x, p.ldx,
+                                   reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0,
+                                   p.bf16, p.n, p.split, p.run, part,
+                                   p.finish ? ctx->d_count : nullptr, p.ad, v, p.y, p.ldy};
+            EXL3_HIP(ctx, exl3::launch_coded_rows(w, p.offsets, a, ctx->stream));
+            if (p.finish) return EXL3_OK;
+        } else {
+            EXL3_HIP(ctx, exl3::launch_coded_tiles(w, p.offsets, xh, xs, p.n, p.per, p.split, part,
                                                    ctx->stream));
+        }
         EXL3_HIP(ctx, exl3::launch_finish(w, p.offsets, part, p.split, p.n, p.bf16, p.ad, v, p.y,
                                           p.ldy, ctx->stream));
         return EXL3_OK;
@@ -1030,7 +1077,7 @@ void exl3_ctx_destroy(exl3_ctx *ctx) {
                     ctx->d_sse,         ctx->d_flag,        ctx->d_err_tiles,   ctx->d_span_target,
                     ctx->d_span_what,   ctx->d_span_packed, ctx->d_gs,          ctx->d_x16,
                     ctx->d_pk,          ctx->d_order,       ctx->d_gss,         ctx->d_bidx,
-                    ctx->d_bscale,      ctx->d_work};
+                    ctx->d_bscale,      ctx->d_work,        ctx->d_count};
     for (void *p : bufs)
         if (p) (void)hipFree(p);
     for (int i = 0; i < ctx->n_old; ++i) (void)hipFree(ctx->old_work[i]);
@@ -1940,6 +1987,7 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
     const int splits = exl3::adapter_grad_splits(n, aa.count);
     const size_t pa_at = c.take(splits * m * w->cols * sizeof(float));
     const size_t pb_at = c.take(splits * m * w->rows * sizeof(float));
+    const size_t used_at = c.take((size_t)splits * aa.count);
     if (wants_dx && (rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
     char *ws = ctx->d_work;
@@ -1980,7 +2028,10 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
         gr[ng++] = exl3::GradArgs{at16(vt_at), dy16, (int64_t)pitch, lddy, w->rows, true,
                                   reinterpret_cast<float *>(ws + pb_at),
                                   static_cast<uint16_t *>(db), false, false};
-    if (ng) EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, gr, ng, n, bf16, splits, ctx->stream));
+    if (ng)
+        EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, gr, ng, n, bf16, splits,
+                                                reinterpret_cast<uint8_t *>(ws + used_at),
+                                                ctx->stream));
     close_timed(ctx, id);
     return EXL3_OK;
 }

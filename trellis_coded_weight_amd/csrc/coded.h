@@ -37,7 +37,8 @@ using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
-using f32x4u = float __attribute__((ext_vector_type(4), aligned(4)));   // unaligned
+// 4-byte aligned
+using f32x4u = float __attribute__((ext_vector_type(4), aligned(4)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
@@ -158,6 +159,16 @@ __device__ __forceinline__ void decode_row(const uint32_t *tile, int r,
 // Binary16 and bfloat16 activations: conversions and the matrix instruction.
 template <bool BF>
 struct Act;
+
+// The type chosen at run time.
+__device__ __forceinline__ float act_load(bool bf, uint16_t v) {
+    return bf ? __builtin_bit_cast(float, (uint32_t)v << 16)
+              : (float)__builtin_bit_cast(_Float16, v);
+}
+__device__ __forceinline__ uint16_t act_store(bool bf, float v) {
+    return bf ? __builtin_bit_cast(uint16_t, (__bf16)v) : __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
 template <>
 struct Act<false> {
     static __device__ __forceinline__ float load(uint16_t v) {
@@ -216,6 +227,65 @@ __device__ __forceinline__ void barrier_in_place() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// v of lane ^ M, M = 1, 2, 4 or 8, by moves within rows of 16 lanes.
+template <int M>
+__device__ __forceinline__ float lane_xor(float v) {
+    int i = __builtin_bit_cast(int, v);
+    if (M == 1) i = __builtin_amdgcn_mov_dpp(i, 0xB1, 0xF, 0xF, true);    // quad 1, 0, 3, 2
+    if (M == 2) i = __builtin_amdgcn_mov_dpp(i, 0x4E, 0xF, 0xF, true);    // quad 2, 3, 0, 1
+    if (M == 4) {                                                         // ^ 7, then ^ 3
+        i = __builtin_amdgcn_mov_dpp(i, 0x141, 0xF, 0xF, true);
+        i = __builtin_amdgcn_mov_dpp(i, 0x1B, 0xF, 0xF, true);
+    }
+    if (M == 8) i = __builtin_amdgcn_mov_dpp(i, 0x128, 0xF, 0xF, true);   // rotation by 8
+    return __builtin_bit_cast(float, i);
+}
+
+// Natural-order Sylvester Hadamard transform, without its factor, of blocks of
+// `had` (64 or 128) consecutive values, eight a lane: three stages in
+// registers, three or four across lanes.
+template <int M>
+__device__ __forceinline__ void hadamard_stage(float (&v)[8]) {
+    const float sign = ((threadIdx.x & 63) & M) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(v[i], sign, lane_xor<M>(v[i]));
+}
+__device__ __forceinline__ void hadamard8(float (&v)[8], int had) {
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & s)) {
+                const float a = v[i], b = v[i + s];
+                v[i] = a + b;
+                v[i + s] = a - b;
+            }
+    hadamard_stage<1>(v);
+    hadamard_stage<2>(v);
+    hadamard_stage<4>(v);
+    if (had == 128) hadamard_stage<8>(v);
+}
+
+// The power of two that takes a largest magnitude (its bits as an integer) into
+// [2^13, 2^14): `scale` its inverse, held in the normal range, and up * up2 the
+// power itself, in two factors as it may pass the largest.
+struct PowerOfTwo {
+    float scale, up, up2;
+    bool bad;                 // the largest is NaN or infinite
+};
+__device__ __forceinline__ PowerOfTwo scale_for(uint32_t big) {
+    PowerOfTwo p;
+    p.bad = big >= 0x7F800000u;
+    // big in [2^(ex - 127), 2^(ex - 126)); its scale 2^(ex - 140)
+    int ex = (int)(big >> 23);
+    ex = ex < 14 ? 14 : ex;
+    p.scale = __builtin_bit_cast(float, (uint32_t)(ex - 13) << 23);
+    const int back = 140 - ex;
+    p.up = __builtin_bit_cast(float, (uint32_t)(127 + back / 2) << 23);
+    p.up2 = __builtin_bit_cast(float, (uint32_t)(127 + back - back / 2) << 23);
+    return p;
 }
 
 // The group (expert) of a row among `groups` ascending offsets[groups + 1]:
@@ -315,15 +385,33 @@ struct AdapterArgs {
 hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void *x, int64_t ldx,
                          int64_t n, bool bf16, uint16_t *xh, float *xs, hipStream_t stream);
 
-// part[split][n][rows]: sums over a split's columns of x' and the levels.
-hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
-                             const float *xs, int64_t n, int split, int tiles, float *part,
+// Few rows: part[split][n][rows], sums over a split's columns of x' and the
+// levels, from x' and its scales or, where xh is null, from x itself (wide_x: its
+// rows start on 16 bytes).  With xh null and arrived not (run = 1), also y itself;
+// arrived: zero, one count for each group and 128 rows of W, zero again afterwards.
+struct RowsArgs {
+    const uint16_t *xh;
+    const float *xs;
+    const void *x;
+    int64_t ldx;
+    bool wide_x, bf16;
+    int64_t n;
+    int split, run;           // splits of 2,048 columns; tiles of 16 rows of W a workgroup
+    float *part;
+    uint32_t *arrived;
+    const AdapterArgs *ad;
+    const uint16_t *v;
+    void *y;
+    int64_t ldy;
+};
+hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const RowsArgs &a,
                              hipStream_t stream);
 
-// The same for 128 rows of x at a time, staged in shared memory.  packed is
+// part[split][n][rows]: sums over a split's columns of x' and the levels, `per`
+// (32, 64 or 128) rows of x at a time, staged in shared memory.  packed is
 // 16-byte aligned and decoded by formula (lv_kind is not kLevelsTable).
 hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
-                              const float *xs, int64_t n, int split, float *part,
+                              const float *xs, int64_t n, int per, int split, float *part,
                               hipStream_t stream);
 
 // y = su H_l (sum of the parts) scale / had, plus the adapters' products v B^T.
@@ -385,8 +473,10 @@ struct GradArgs {
     uint16_t *out;
     bool wide_q, wide_out;    // set by the launcher
 };
+// used: [splits][count] bytes, set to whether a split has rows of an adapter (the
+// parts of those that have none are not written).
 int adapter_grad_splits(int64_t n, int count);
 hipError_t launch_adapter_grad(const AdapterArgs &ad, const GradArgs *p, int products, int64_t n,
-                               bool bf16, int splits, hipStream_t stream);
+                               bool bf16, int splits, uint8_t *used, hipStream_t stream);
 
 }  // namespace exl3

@@ -2,37 +2,15 @@
 //
 // W = diag(su) H_l (scale C) H_r diag(sv) with C the codes' levels, so
 //   y = scale / had * su (H_l (C x')),   x' = H_r (sv x)
-// (H here without its factor 1 / sqrt(had), which enters twice).  Three
-// launches: x' (rotate_kernel), C x' from the codes (coded_rows_kernel), and
-// the sum, the left transform and the factors (finish_kernel).
+// (H here without its factor 1 / sqrt(had), which enters twice).  x' comes from
+// rotate_kernel, C x' from the codes in coded_rows_kernel, which also takes the
+// left transform and the factors, or for more rows in coded_tiles_kernel, after
+// which finish_kernel takes them.
 #include "coded.h"
 
 namespace exl3 {
 
 namespace {
-
-// Butterflies of the natural-order Sylvester Hadamard over `had` consecutive
-// values, E per lane: log2(E) stages in registers, the rest across lanes.
-template <int E>
-__device__ __forceinline__ void hadamard_lanes(float (&v)[E], int had) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int s = 1; s < E; s <<= 1)
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (!(i & s)) {
-                const float a = v[i], b = v[i + s];
-                v[i] = a + b;
-                v[i + s] = a - b;
-            }
-    for (int m = 1; m * E < had; m <<= 1) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float o = __shfl_xor(v[i], m);
-            v[i] = (lane & m) ? o - v[i] : v[i] + o;
-        }
-    }
-}
 
 // ---- x' ----
 // A workgroup per row, eight columns a lane at a time, up to kKeep rounds of
@@ -76,7 +54,7 @@ rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had, bo
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = Act<BF>::load(q[i]) * (i < 4 ? s0[i] : s1[i - 4]);
         }
-        hadamard_lanes(o, had);
+        hadamard8(o, had);
     };
     const int rounds = (cols + THREADS * 8 - 1) / (THREADS * 8);
     // magnitudes compare as integers; NaN and infinity come out on top
@@ -110,23 +88,15 @@ rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had, bo
         const uint32_t o = __builtin_bit_cast(uint32_t, wave_big[i]);
         big = o > big ? o : big;
     }
-    const bool bad = big >= 0x7F800000u;
-    // exponent of the largest: big in [2^(ex - 127), 2^(ex - 126)); its scale
-    // 2^(ex - 140), held in the normal range, and the inverse in two factors as
-    // it may pass the largest power
-    int ex = (int)(big >> 23);
-    ex = ex < 14 ? 14 : ex;
-    const float scale = __builtin_bit_cast(float, (uint32_t)(ex - 13) << 23);
-    const int back = 140 - ex;
-    const float up = __builtin_bit_cast(float, (uint32_t)(127 + back / 2) << 23);
-    const float up2 = __builtin_bit_cast(float, (uint32_t)(127 + back - back / 2) << 23);
+    const PowerOfTwo p2 = scale_for(big);
     auto store = [&](int col, const float (&o)[8]) {
         if (col >= cols) return;
         u32x4 out;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t h = Act<false>::store2(o[2 * i] * up * up2, o[2 * i + 1] * up * up2);
-            out[i] = bad ? 0x7E007E00u : h;
+            const uint32_t h = Act<false>::store2(o[2 * i] * p2.up * p2.up2,
+                                                  o[2 * i + 1] * p2.up * p2.up2);
+            out[i] = p2.bad ? 0x7E007E00u : h;
         }
         *reinterpret_cast<u32x4 *>(xh + row * cols + col) = out;
     };
@@ -138,77 +108,283 @@ rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had, bo
         transformed((c * THREADS + threadIdx.x) * 8, o);
         store((c * THREADS + threadIdx.x) * 8, o);
     }
-    if (threadIdx.x == 0) xs[row] = scale;
+    if (threadIdx.x == 0) xs[row] = p2.scale;
 }
 
-// ---- C x' ----
-// A workgroup of eight waves per 16 rows of W, group and split; the waves take
-// the split's units of 256 columns in turn, and their sums meet in shared
-// memory.  A wave decodes 16 x 64 weights into the operands of two steps and
-// uses them for NT tiles of 16 activation rows; x' comes from the caches.
-// Columns a wave takes at a time.
-constexpr int kUnit = 256;
-
-template <int LV, int K, int NT>
-__global__ void __launch_bounds__(512)
-coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols, int Kr,
-                  const int32_t *__restrict__ offsets, const uint16_t *__restrict__ xh,
-                  const float *__restrict__ xs, int64_t n, int split,
-                  float *__restrict__ part) {
-    __shared__ f32x4 sums[8][NT][64];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
-    const int row_tiles = rows / 16, units = (cols + kUnit - 1) / kUnit;
-    const int rt = blockIdx.x % row_tiles, sp = blockIdx.x / row_tiles, e = blockIdx.y;
-    int64_t lo, hi;
-    group_rows(offsets, e, n, lo, hi);
-    const int kk = K ? K : Kr;
-    const uint32_t *wrow = packed + ((size_t)e * row_tiles + rt) * (size_t)(cols / 16) * (8 * kk);
-    for (int64_t t0 = lo; t0 < hi; t0 += 16 * NT) {
-        const uint16_t *xr[NT];
-        f32x4 acc[NT];
+// Eight columns of a row of y, row .. row + 7 of W, from their left transform:
+// the factors, the adapter's product v b^T, one rounding.
+__device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *su,
+                                           const AdapterArgs &ad, const uint16_t *v, int64_t tok,
+                                           int row, int rows, bool bf16, uint16_t *y) {
+    const f32x4 s0 = *reinterpret_cast<const f32x4u *>(su);
+    const f32x4 s1 = *reinterpret_cast<const f32x4u *>(su + 4);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            int64_t tok = t0 + 16 * t + r;
-            tok = tok < hi ? tok : hi - 1;     // a row past the end repeats the last, unstored
-            xr[t] = xh + tok * cols;
-            acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        for (int u = sp * 8 + wv; u < units; u += 8 * split) {
-            const int c0 = u * kUnit;
-            uint32_t d[4][RowWords<K>::N];
+    for (int i = 0; i < 8; ++i) z[i] *= f * (i < 4 ? s0[i] : s1[i - 4]);
+    if (v) {
+        const int id = ad.ids[tok];
+        if (id >= 0 && id < ad.count) {
+            const uint16_t *b = static_cast<const uint16_t *>(ad.b) +
+                                ((size_t)id * rows + row) * ad.rank;
+            const uint16_t *vt = v + tok * ad.rank_pad;
+            const bool wide = reinterpret_cast<uintptr_t>(ad.b) % 16 == 0 && ad.rank % 8 == 0;
+            for (int k = 0; k < ad.rank; k += 8) {
+                const u32x4 vk = *reinterpret_cast<const u32x4 *>(vt + k);
+                float vf[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (c0 + 64 * q < cols)
-                    load_row<K>(wrow + (size_t)(c0 / 16 + 4 * q + g) * (8 * kk), r, d[q]);
+                for (int c = 0; c < 8; ++c)
+                    vf[c] = act_load(bf16, (uint16_t)(vk[c >> 1] >> (16 * (c & 1))));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (c0 + 64 * q >= cols) break;
-                u32x4 w[2];
-                decode_row<LV, K>(wrow + (size_t)(c0 / 16 + 4 * q + g) * (8 * kk), r, d[q], lv, w);
+                for (int i = 0; i < 8; ++i) {
+                    const uint16_t *bi = b + (size_t)i * ad.rank + k;
+                    if (wide) {
+                        const u32x4 bk = *reinterpret_cast<const u32x4 *>(bi);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const u32x4 *xp =
-                        reinterpret_cast<const u32x4 *>(xr[t] + c0 + 64 * q + 16 * g);
-                    acc[t] = Act<false>::mfma(w[0], xp[0], acc[t]);
-                    acc[t] = Act<false>::mfma(w[1], xp[1], acc[t]);
+                        for (int c = 0; c < 8; ++c)
+                            z[i] += vf[c] * act_load(bf16, (uint16_t)(bk[c >> 1] >> (16 * (c & 1))));
+                    } else {
+                        for (int c = 0; c < 8 && k + c < ad.rank; ++c)
+                            z[i] += vf[c] * act_load(bf16, bi[c]);
+                    }
                 }
             }
         }
+    }
+    uint32_t o[4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sums[wv][t][lane] = acc[t];
-        __syncthreads();
-        for (int i = threadIdx.x; i < NT * 64; i += 512) {
-            const int t = i >> 6, l = i & 63;
-            f32x4 a = sums[0][t][l];
+    for (int i = 0; i < 4; ++i)
+        o[i] = bf16 ? Act<true>::store2(z[2 * i], z[2 * i + 1])
+                    : Act<false>::store2(z[2 * i], z[2 * i + 1]);
+    if (reinterpret_cast<uintptr_t>(y) % 16 == 0) {
+        *reinterpret_cast<u32x4 *>(y) = u32x4{o[0], o[1], o[2], o[3]};
+    } else {
 #pragma unroll
-            for (int w = 1; w < 8; ++w) a += sums[w][t][l];
-            const int64_t tok = t0 + 16 * t + (l & 15);
-            if (tok < hi)
-                *reinterpret_cast<f32x4 *>(part + ((size_t)sp * n + tok) * rows + rt * 16 +
-                                           4 * (l >> 4)) = a * xs[tok];
+        for (int i = 0; i < 8; ++i) y[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// ---- few rows ----
+// A workgroup of eight waves takes `run` tiles of 16 rows of W in turn, for one
+// group and split.  A split is eight units of 256 columns, and each wave has one
+// of them throughout: the operands of x' (16 rows of activations) stay in its
+// registers, the words of the next tile are under way while it decodes and
+// multiplies this one's, and the eight waves' sums meet in shared memory, in two
+// places by turns (one barrier a tile).  Decoding bounds it: 5 vector
+// instructions a weight and 4.4 cycles each, 4.6 us for the 50 M weights of
+// 12288 x 4096 at 1,024 SIMDs and 2.2 GHz, beside reading the codes.
+//
+// x' comes from rotate_kernel, or (OWN, up to kOwn rows at a time) each wave
+// transforms its own unit of x, with a scale for the unit.
+//
+// The left transform mixes 128 rows of W, eight tiles' sums.  It is left to
+// finish_kernel, but for the smallest calls (FINISH, run = 1): there each
+// workgroup stores its sums past its die's cache, waits until they are there,
+// and counts itself, and the last of a block reads all sums, in the order of the
+// splits, and finishes the rows of y.  One launch in place of three: 10.7 us
+// against 15.3 for one row and 1024 x 4096; with more workgroups than compute
+// units the late finish costs more than the launches.
+constexpr int kUnit = 256, kOwn = 8;
+constexpr int kOwnPitch = kUnit * 2 + 16;        // bytes of a row of a wave's own x'
+
+template <int LV, int K, bool OWN, bool FINISH>
+__global__ void __launch_bounds__(512)
+coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols, int Kr,
+                  int had, const float *__restrict__ scale, const float *__restrict__ su,
+                  const float *__restrict__ sv, const int32_t *__restrict__ offsets, int groups,
+                  RowsArgs a, AdapterArgs ad) {
+    constexpr int kStep = OWN ? kOwn : 16;
+    __shared__ f32x4 sums[2][8][64];
+    __shared__ __align__(16) char own[OWN ? 8 * kOwn * kOwnPitch : 16];
+    __shared__ uint32_t before;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    const int row_tiles = rows / 16, runs = (row_tiles + a.run - 1) / a.run;
+    const int rt0 = blockIdx.x % runs * a.run, sp = blockIdx.x / runs, e = blockIdx.y;
+    const int rt1 = rt0 + a.run < row_tiles ? rt0 + a.run : row_tiles;
+    const int64_t n = a.n;
+    uint16_t *y = static_cast<uint16_t *>(a.y);
+    if (FINISH && offsets) {
+        // rows of no group, by all workgroups
+        const int64_t from = offsets[0], to = offsets[groups];
+        const int64_t all = (int64_t)gridDim.x * gridDim.y;
+        const int64_t me = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+        for (int64_t t = me; t < n && t < from; t += all)
+            for (int c = threadIdx.x; c < rows; c += 512) y[t * a.ldy + c] = 0;
+        for (int64_t t = (to > 0 ? to : 0) + me; t < n; t += all)
+            for (int c = threadIdx.x; c < rows; c += 512) y[t * a.ldy + c] = 0;
+    }
+    int64_t lo, hi;
+    group_rows(offsets, e, n, lo, hi);
+    if (lo >= hi) return;
+    const int kk = K ? K : Kr;
+    const int c0 = (sp * 8 + wv) * kUnit;        // the wave's columns; past the last: none
+    const int quads = c0 >= cols ? 0 : cols - c0 >= kUnit ? 4 : (cols - c0) / 64;
+    const uint32_t *wcol = packed + ((size_t)e * row_tiles * (cols / 16) + c0 / 16 + g) * (8 * kk);
+    const size_t wrow = (size_t)(cols / 16) * (8 * kk);
+    uint32_t d[4][RowWords<K>::N];
+    auto load_tile = [&](int rt) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (q < quads) load_row<K>(wcol + rt * wrow + q * 32 * kk, r, d[q]);
+    };
+    for (int64_t t0 = lo; t0 < hi; t0 += kStep) {
+        load_tile(rt0);
+        u32x4 x[4][2];
+        float x_scale = 0.0f;                    // of the lane's row of x'
+        if (OWN) {
+            char *mine = own + wv * kOwn * kOwnPitch;
+            const int here = hi - t0 < kOwn ? (int)(hi - t0) : kOwn;
+            // two rows at a time, half a wave each, eight columns a lane
+            const int col = c0 + (lane & 31) * 8;
+            const bool in = col < cols;
+            f32x4 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
+            if (in) {
+                const float *svp = sv + (size_t)e * cols + col;
+                s0 = *reinterpret_cast<const f32x4u *>(svp);
+                s1 = *reinterpret_cast<const f32x4u *>(svp + 4);
+            }
+            for (int t = 0; t < here; t += 2) {
+                const int row = t + (lane >> 5);
+                float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                if (in && row < here) {
+                    const uint16_t *xp = static_cast<const uint16_t *>(a.x) +
+                                         (t0 + row) * a.ldx + col;
+                    uint16_t q[8];
+                    if (a.wide_x) {
+                        const u32x4 w = *reinterpret_cast<const u32x4 *>(xp);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) q[i] = xp[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = act_load(a.bf16, q[i]) * (i < 4 ? s0[i] : s1[i - 4]);
+                }
+                hadamard8(o, had);
+                // magnitudes compare as integers; NaN and infinity come out on top
+                uint32_t big = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t m = __builtin_bit_cast(uint32_t, o[i]) & 0x7FFFFFFFu;
+                    big = m > big ? m : big;
+                }
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const uint32_t q = (uint32_t)__shfl_xor((int)big, m);
+                    big = q > big ? q : big;
+                }
+                const PowerOfTwo p2 = scale_for(big);
+                u32x4 h;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = Act<false>::store2(o[2 * i] * p2.up * p2.up2,
+                                              o[2 * i + 1] * p2.up * p2.up2);
+                    if (p2.bad) h[i] = 0x7E007E00u;
+                }
+                if (row < here)
+                    *reinterpret_cast<u32x4 *>(mine + row * kOwnPitch + (lane & 31) * 16) = h;
+                const float first = __shfl(p2.scale, 0), second = __shfl(p2.scale, 32);
+                if (r == t) x_scale = first;
+                if (r == t + 1) x_scale = second;
+            }
+            // the wave's own stores, read back by other lanes of the same wave
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const u32x4 *xp = reinterpret_cast<const u32x4 *>(
+                    mine + (r < here ? r : here - 1) * kOwnPitch + q * 128 + g * 32);
+                x[q][0] = xp[0];
+                x[q][1] = xp[1];
+            }
+            // these reads are done before the next rows' stores
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        } else {
+            int64_t tok = t0 + r;
+            tok = tok < hi ? tok : hi - 1;       // past the end: repeats, not stored
+            x_scale = a.xs[tok];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < quads) {
+                    const u32x4 *xp = reinterpret_cast<const u32x4 *>(a.xh + tok * cols + c0 +
+                                                                      64 * q + 16 * g);
+                    x[q][0] = xp[0];
+                    x[q][1] = xp[1];
+                }
         }
-        __syncthreads();
+        for (int rt = rt0; rt < rt1; ++rt) {
+            f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+            uint32_t now[4][RowWords<K>::N];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < RowWords<K>::N; ++i) now[q][i] = d[q][i];
+            if (rt + 1 < rt1) load_tile(rt + 1);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q >= quads) break;
+                u32x4 w[2];
+                decode_row<LV, K>(wcol + rt * wrow + q * 32 * kk, r, now[q], lv, w);
+                acc[0] = Act<false>::mfma(w[0], x[q][0], acc[0]);
+                acc[1] = Act<false>::mfma(w[1], x[q][1], acc[1]);
+            }
+            const int place = rt & 1;
+            sums[place][wv][lane] = (acc[0] + acc[1]) * x_scale;
+            __syncthreads();
+            if (wv == (rt & 7)) {
+                f32x4 z = sums[place][0][lane];
+#pragma unroll
+                for (int w = 1; w < 8; ++w) z += sums[place][w][lane];
+                const int64_t tok = t0 + r;
+                if (tok < hi && r < kStep) {
+                    float *o = a.part + ((size_t)sp * n + tok) * rows + rt * 16 + 4 * g;
+                    if (FINISH) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            __hip_atomic_store(o + c, z[c], __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+                    } else {
+                        *reinterpret_cast<f32x4 *>(o) = z;
+                    }
+                }
+            }
+        }
+        // the next rows' sums may meet in the place that was just read
+        if (t0 + kStep < hi) __syncthreads();
+    }
+    if (!FINISH) return;
+    // count this workgroup once its sums are stored (each wave waits for its own:
+    // stores and loads of device scope go past the die's cache, so the count
+    // needs to order nothing else)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    const int rb = rt0 / 8, row_blocks = (row_tiles + 7) / 8;
+    uint32_t *count = a.arrived + (size_t)e * row_blocks + rb;
+    if (threadIdx.x == 0)
+        before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const int of_block = row_tiles - 8 * rb < 8 ? row_tiles - 8 * rb : 8;
+    if (before != (uint32_t)(of_block * a.split) - 1u) return;
+    if (threadIdx.x == 0)
+        __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // 16 lanes a row of y, eight of the block's 128 columns a lane
+    const int row = rb * 128 + r * 8;
+    const bool in = row < rows;
+    const float f = scale[e] / (float)had;
+    for (int64_t tok0 = lo + wv * 4; tok0 < hi; tok0 += 32) {
+        const int64_t tok = tok0 + g;
+        float z[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        const bool has = in && tok < hi;
+        if (has)
+            for (int s = 0; s < a.split; ++s) {
+                const float *p = a.part + ((size_t)s * n + tok) * rows + row;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    z[i] += __hip_atomic_load(p + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        hadamard8(z, had);
+        if (has) finish_row(z, f, su + (size_t)e * rows + row, ad, a.v, tok, row, rows, a.bf16,
+                            y + tok * a.ldy + row);
     }
 }
 
@@ -225,14 +401,14 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
 // the wave.  Piece s of 16 bytes of row r of x' holds its piece s ^ (r / 2 & 7):
 // reads meet no bank twice.
 template <int LV, int K, int NT>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, NT == 8 ? 2 : NT == 4 ? 3 : 4)
 coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
                    const int32_t *__restrict__ offsets, int groups,
                    const uint16_t *__restrict__ xh, const float *__restrict__ xs, int64_t n,
                    int split, int row_blocks, int total, float *__restrict__ part) {
     constexpr int kRows = 16 * NT, kPieces = kRows * 8 / 256;   // of x', a thread and step
     constexpr int kX = kRows * 128, kPlace = kX + 1024 * K;     // bytes of a place: x', words
-    // places: as many as leave two workgroups' worth of shared memory
+    // places: as many as leave room for two workgroups
     constexpr int kRing = 4 * kPlace < 80 * 1024 ? 4 : 3;
     __shared__ __align__(16) char ring[kRing * kPlace];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -393,71 +569,69 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
 }
 
 // ---- y ----
-// A wave per row of y and 256 of its columns, four a lane.
-template <bool BF>
+// A wave per row of y and 512 of its columns, eight a lane.
 __global__ void __launch_bounds__(256)
 finish_kernel(const float *__restrict__ part, int split, int64_t n, int rows, int had,
               const float *__restrict__ scale, const float *__restrict__ su,
               const int32_t *__restrict__ offsets, int groups, AdapterArgs ad,
-              const uint16_t *__restrict__ v, uint16_t *__restrict__ y, int64_t ldy) {
-    const int lane = threadIdx.x & 63, blocks = (rows + 255) / 256;
+              const uint16_t *__restrict__ v, bool bf16, uint16_t *__restrict__ y, int64_t ldy) {
+    const int lane = threadIdx.x & 63, blocks = (rows + 511) / 512;
     const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int64_t tok = wave / blocks;
     if (tok >= n) return;
-    const int row = (int)(wave - tok * blocks) * 256 + lane * 4;
+    const int row = (int)(wave - tok * blocks) * 512 + lane * 8;
     const bool in = row < rows;
     int e = 0;
     if (offsets) {
         e = group_of_row(offsets, groups, tok);
         if (e >= groups || tok < offsets[0]) {
             if (in)
-                for (int i = 0; i < 4; ++i) y[tok * ldy + row + i] = 0;
+                for (int i = 0; i < 8; ++i) y[tok * ldy + row + i] = 0;
             return;
         }
     }
-    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (in)
-        for (int s = 0; s < split; ++s) {
-            const f32x4 p = *reinterpret_cast<const f32x4 *>(part + ((size_t)s * n + tok) * rows + row);
+    float z[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (in) {
+        // eight splits' loads under way at a time
+        const float *at = part + tok * rows + row;
+        const size_t pitch = (size_t)n * rows;
+        for (int s0 = 0; s0 < split; s0 += 8) {
+            f32x4 p[8][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] += p[i];
-        }
-    hadamard_lanes(a, had);
-    if (!in) return;
-    const float f = scale[e] / (float)had;
+            for (int s = 0; s < 8; ++s)
+                if (s0 + s < split) {
+                    const f32x4 *q = reinterpret_cast<const f32x4 *>(at + (s0 + s) * pitch);
+                    p[s][0] = q[0];
+                    p[s][1] = q[1];
+                }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] *= f * su[(size_t)e * rows + row + i];
-    if (v) {
-        const int id = ad.ids[tok];
-        if (id >= 0 && id < ad.count) {
-            const uint16_t *b = static_cast<const uint16_t *>(ad.b) +
-                                ((size_t)id * rows + row) * ad.rank;
-            const uint16_t *vt = v + tok * ad.rank_pad;
-            for (int k = 0; k < ad.rank; ++k) {
-                const float vk = Act<BF>::load(vt[k]);
+            for (int s = 0; s < 8; ++s)
+                if (s0 + s < split)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] += vk * Act<BF>::load(b[i * ad.rank + k]);
-            }
+                    for (int i = 0; i < 8; ++i) z[i] += p[s][i >> 2][i & 3];
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[tok * ldy + row + i] = Act<BF>::store(a[i]);
+    hadamard8(z, had);
+    if (in) finish_row(z, scale[e] / (float)had, su + (size_t)e * rows + row, ad, v, tok, row,
+                       rows, bf16, y + tok * ldy + row);
 }
 
 template <int LV, int K>
-hipError_t coded_rows_t(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
-                        const float *xs, int64_t n, int split, int tiles, float *part,
+hipError_t coded_rows_t(const WeightArgs &w, const int32_t *offsets, const RowsArgs &a,
                         hipStream_t stream) {
-    const dim3 grid((unsigned)(w.rows / 16 * split), (unsigned)w.groups);
-#define EXL3_ROWS(NT)                                                                        \
-    hipLaunchKernelGGL((coded_rows_kernel<LV, K, NT>), grid, dim3(512), 0, stream, w.packed, \
-                       w.lv, w.rows, w.cols, w.K, offsets, xh, xs, n, split, part)
-    if (tiles <= 1)
-        EXL3_ROWS(1);
-    else if (tiles <= 2)
-        EXL3_ROWS(2);
+    const int runs = (w.rows / 16 + a.run - 1) / a.run;
+    const dim3 grid((unsigned)(runs * a.split), (unsigned)w.groups);
+    const AdapterArgs ad = a.ad ? *a.ad : AdapterArgs{};
+#define EXL3_ROWS(OWN, FINISH)                                                               \
+    hipLaunchKernelGGL((coded_rows_kernel<LV, K, OWN, FINISH>), grid, dim3(512), 0, stream,  \
+                       w.packed, w.lv, w.rows, w.cols, w.K, w.had, w.scale, w.su, w.sv,      \
+                       offsets, w.groups, a, ad)
+    if (a.xh)
+        EXL3_ROWS(false, false);
+    else if (a.arrived)
+        EXL3_ROWS(true, true);
     else
-        EXL3_ROWS(4);
+        EXL3_ROWS(true, false);
 #undef EXL3_ROWS
     return hipGetLastError();
 }
@@ -484,11 +658,10 @@ hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void
     return hipGetLastError();
 }
 
-hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
-                             const float *xs, int64_t n, int split, int tiles, float *part,
+hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const RowsArgs &a,
                              hipStream_t stream) {
 #define EXL3_ROWS_K(LV, KK) \
-    case KK: return coded_rows_t<LV, KK>(w, offsets, xh, xs, n, split, tiles, part, stream)
+    case KK: return coded_rows_t<LV, KK>(w, offsets, a, stream)
     if (w.lv_kind == kLevelsMul1)
         switch (w.K) {
             EXL3_ROWS_K(kLevelsMul1, 1);
@@ -504,21 +677,27 @@ hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const 
             EXL3_ROWS_K(kLevelsHalves, 4);
         }
 #undef EXL3_ROWS_K
-    return coded_rows_t<kLevelsTable, 0>(w, offsets, xh, xs, n, split, tiles, part, stream);
+    return coded_rows_t<kLevelsTable, 0>(w, offsets, a, stream);
 }
 
 hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
-                              const float *xs, int64_t n, int split, float *part,
+                              const float *xs, int64_t n, int per, int split, float *part,
                               hipStream_t stream) {
-    constexpr int NT = 8;
     const int row_blocks = (w.rows + 127) / 128;
-    const int64_t n_tiles = offsets ? n / (16 * NT) + w.groups : (n + 16 * NT - 1) / (16 * NT);
+    const int64_t n_tiles = offsets ? n / per + w.groups : (n + per - 1) / per;
     const int total = (int)(n_tiles * row_blocks * split);
+#define EXL3_TILES_NT(LV, KK, NT)                                                               \
+    hipLaunchKernelGGL((coded_tiles_kernel<LV, KK, NT>), dim3((unsigned)total), dim3(256), 0,   \
+                       stream, w.packed, w.lv, w.rows, w.cols, offsets, w.groups, xh, xs, n,    \
+                       split, row_blocks, total, part)
 #define EXL3_TILES(LV, KK)                                                                      \
     case KK:                                                                                    \
-        hipLaunchKernelGGL((coded_tiles_kernel<LV, KK, NT>), dim3((unsigned)total), dim3(256),  \
-                           0, stream, w.packed, w.lv, w.rows, w.cols, offsets, w.groups, xh, xs, \
-                           n, split, row_blocks, total, part);                                  \
+        if (per == 32)                                                                          \
+            EXL3_TILES_NT(LV, KK, 2);                                                           \
+        else if (per == 64)                                                                     \
+            EXL3_TILES_NT(LV, KK, 4);                                                           \
+        else                                                                                    \
+            EXL3_TILES_NT(LV, KK, 8);                                                           \
         break
     if (w.lv_kind == kLevelsMul1)
         switch (w.K) {
@@ -539,21 +718,18 @@ hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const
     else
         return hipErrorInvalidValue;
 #undef EXL3_TILES
+#undef EXL3_TILES_NT
     return hipGetLastError();
 }
 
 hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const float *part, int split,
                          int64_t n, bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
                          int64_t ldy, hipStream_t stream) {
-    const unsigned grid = (unsigned)((n * ((w.rows + 255) / 256) + 3) / 4);
+    const unsigned grid = (unsigned)((n * ((w.rows + 511) / 512) + 3) / 4);
     const AdapterArgs args = ad ? *ad : AdapterArgs{};
-    uint16_t *yy = static_cast<uint16_t *>(y);
-    if (bf16)
-        hipLaunchKernelGGL((finish_kernel<true>), dim3(grid), dim3(256), 0, stream, part, split, n,
-                           w.rows, w.had, w.scale, w.su, offsets, w.groups, args, v, yy, ldy);
-    else
-        hipLaunchKernelGGL((finish_kernel<false>), dim3(grid), dim3(256), 0, stream, part, split,
-                           n, w.rows, w.had, w.scale, w.su, offsets, w.groups, args, v, yy, ldy);
+    hipLaunchKernelGGL(finish_kernel, dim3(grid), dim3(256), 0, stream, part, split, n, w.rows,
+                       w.had, w.scale, w.su, offsets, w.groups, args, v, bf16,
+                       static_cast<uint16_t *>(y), ldy);
     return hipGetLastError();
 }
 
