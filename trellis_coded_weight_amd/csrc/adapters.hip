@@ -10,13 +10,9 @@ namespace exl3 {
 
 namespace {
 
-// Eight consecutive 16-bit elements; `wide` where they start on 16 bytes.
-__device__ __forceinline__ u32x4 load8(const uint16_t *p, bool wide) {
-    if (wide) return *reinterpret_cast<const u32x4 *>(p);
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
-    return o;
+// Eight consecutive 16-bit elements, on any two bytes.
+__device__ __forceinline__ u32x4 load8(const uint16_t *p) {
+    return *reinterpret_cast<const u32x4u *>(p);
 }
 
 // ---- v = alpha A x ----
@@ -72,12 +68,12 @@ shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
             for (int j = 0; j < U; ++j) {
                 const int c = c0 + 32 * kWaves * j;
                 xv[j] = u32x4{0u, 0u, 0u, 0u};
-                if (c < k) xv[j] = load8(xr + c, p.wide_x);
+                if (c < k) xv[j] = load8(xr + c);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
                     av[j][t] = u32x4{0u, 0u, 0u, 0u};
                     if (c < k && 16 * t + r < ad.rank)
-                        av[j][t] = load8(ar + (size_t)(16 * t + r) * k + c, p.wide_a);
+                        av[j][t] = load8(ar + (size_t)(16 * t + r) * k + c);
                 }
             }
 #pragma unroll
@@ -176,11 +172,8 @@ adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t
             s.x[t] = uint2{0u, 0u};
             if ((has >> (8 * g + t)) & 1u) {
                 const uint16_t *at = qc + (b + 8 * g + t) * p.ldq;
-                if (p.wide_q)
-                    s.x[t] = *reinterpret_cast<const uint2 *>(at);
-                else
-                    s.x[t] = uint2{at[0] | ((uint32_t)at[1] << 16),
-                                   at[2] | ((uint32_t)at[3] << 16)};
+                const u32x2u two = *reinterpret_cast<const u32x2u *>(at);
+                s.x[t] = uint2{two[0], two[1]};
             }
         }
 #pragma unroll
@@ -274,18 +267,21 @@ adapter_sum_kernel(GradArgs g0, GradArgs g1, int splits, int count, int rank,
     if (i >= all) return;
     const int id = (int)(i / ((size_t)rank * p.k));
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int q = 0; q < splits; ++q)
-        if (used[q * count + id]) s += *reinterpret_cast<const f32x4 *>(p.part + q * all + i);
-    const uint32_t lo = Act<BF>::store2(s[0], s[1]), hi = Act<BF>::store2(s[2], s[3]);
-    uint16_t *o = p.out + i;
-    if (p.wide_out) {
-        *reinterpret_cast<uint2 *>(o) = uint2{lo, hi};
-    } else {
-        o[0] = (uint16_t)lo;
-        o[1] = (uint16_t)(lo >> 16);
-        o[2] = (uint16_t)hi;
-        o[3] = (uint16_t)(hi >> 16);
+    // eight parts' loads under way at a time
+    for (int q0 = 0; q0 < splits; q0 += 8) {
+        bool has[8];
+        f32x4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) has[q] = q0 + q < splits && used[(q0 + q) * count + id];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (has[q]) v[q] = *reinterpret_cast<const f32x4 *>(p.part + (q0 + q) * all + i);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (has[q]) s += v[q];
     }
+    *reinterpret_cast<u32x2u *>(p.out + i) =
+        u32x2u{Act<BF>::store2(s[0], s[1]), Act<BF>::store2(s[2], s[3])};
 }
 
 }  // namespace
@@ -293,14 +289,13 @@ adapter_sum_kernel(GradArgs g0, GradArgs g1, int splits, int count, int rank,
 hipError_t launch_shrink(const AdapterArgs &ad, const ShrinkArgs *p, int products, int64_t n,
                          bool bf16, hipStream_t stream) {
     ShrinkArgs q[2];
-    for (int i = 0; i < 2; ++i) {
-        q[i] = p[i < products ? i : 0];
-        q[i].wide_a = reinterpret_cast<uintptr_t>(q[i].a) % 16 == 0;
-        q[i].wide_x = reinterpret_cast<uintptr_t>(q[i].x) % 16 == 0 && q[i].ldx % 8 == 0;
-    }
+    for (int i = 0; i < 2; ++i) q[i] = p[i < products ? i : 0];
     const unsigned tiles = (unsigned)((n + 15) / 16);
-    // up to 16 distinct adapters a tile: a workgroup each while there are few tiles
-    const dim3 grid(tiles, tiles <= 32 ? 16u : tiles <= 128 ? 4u : 1u, (unsigned)products);
+    // up to 16 distinct adapters a tile: a workgroup each while all workgroups run
+    // at once (one a compute unit; those without work would hold up the others)
+    unsigned share = 16;
+    while (share > 1 && tiles * share * (unsigned)products > 256) share /= 2;
+    const dim3 grid(tiles, share, (unsigned)products);
 #define EXL3_SHRINK(RT)                                                                     \
     do {                                                                                    \
         const dim3 block(RT <= 4 ? 1024 : 512);                                             \
@@ -341,11 +336,7 @@ int adapter_grad_splits(int64_t n, int count) {
 hipError_t launch_adapter_grad(const AdapterArgs &ad, const GradArgs *p, int products, int64_t n,
                                bool bf16, int splits, uint8_t *used, hipStream_t stream) {
     GradArgs q[2];
-    for (int i = 0; i < 2; ++i) {
-        q[i] = p[i < products ? i : 0];
-        q[i].wide_q = reinterpret_cast<uintptr_t>(q[i].q) % 8 == 0 && q[i].ldq % 4 == 0;
-        q[i].wide_out = reinterpret_cast<uintptr_t>(q[i].out) % 8 == 0;
-    }
+    for (int i = 0; i < 2; ++i) q[i] = p[i < products ? i : 0];
     const int64_t per = ((n + splits - 1) / splits + 31) / 32 * 32;
     const int blocks = (q[0].k + 255) / 256 + (products > 1 ? (q[1].k + 255) / 256 : 0);
     const dim3 grid((unsigned)blocks, (unsigned)ad.count, (unsigned)splits);

@@ -950,7 +950,6 @@ int run_product(exl3_ctx *ctx, const Product &p) {
                                               ctx->stream));
         if (p.form == kFewRows) {
             const exl3::RowsArgs a{p.own_x ? nullptr : xh, xs, p.x, p.ldx,
-                                   reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0,
                                    p.bf16, p.n, p.split, p.run, part,
                                    p.finish ? ctx->d_count : nullptr, p.ad, v, p.y, p.ldy};
             EXL3_HIP(ctx, exl3::launch_coded_rows(w, p.offsets, a, ctx->stream));
@@ -1934,8 +1933,7 @@ int exl3_adapter_linear(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters
     const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
     const exl3::ShrinkArgs sh{static_cast<const uint16_t *>(aa.a),
                               static_cast<const uint16_t *>(x), ldx, w->cols,
-                              reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at), nullptr, 0,
-                              false, false};
+                              reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at), nullptr, 0};
     EXL3_HIP(ctx, exl3::launch_shrink(aa, &sh, 1, n, p.bf16, ctx->stream));
     rc = run_product(ctx, p);
     close_timed(ctx, id);
@@ -2005,12 +2003,12 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
         if (needs_u) {
             tr[nt++] = exl3::TransposeArgs{b16, at16(bt_at), w->rows, aa.rank};
             sh[ns++] = exl3::ShrinkArgs{at16(bt_at), dy16, lddy, w->rows, at16(p.v_at),
-                                        da ? at16(ut_at) : nullptr, (int64_t)pitch, false, false};
+                                        da ? at16(ut_at) : nullptr, (int64_t)pitch};
         }
         if (wants_dx) tr[nt++] = exl3::TransposeArgs{a16, at16(at_at), aa.rank, w->cols};
         if (db)
             sh[ns++] = exl3::ShrinkArgs{a16, x16, ldx, w->cols, at16(v_at), at16(vt_at),
-                                        (int64_t)pitch, false, false};
+                                        (int64_t)pitch};
         if (nt) EXL3_HIP(ctx, exl3::launch_transpose16(tr, nt, aa.count, ctx->stream));
         if (ns) EXL3_HIP(ctx, exl3::launch_shrink(aa, sh, ns, n, bf16, ctx->stream));
     }
@@ -2023,11 +2021,11 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
     if (da)
         gr[ng++] = exl3::GradArgs{at16(ut_at), x16, (int64_t)pitch, ldx, w->cols, false,
                                   reinterpret_cast<float *>(ws + pa_at),
-                                  static_cast<uint16_t *>(da), false, false};
+                                  static_cast<uint16_t *>(da)};
     if (db)
         gr[ng++] = exl3::GradArgs{at16(vt_at), dy16, (int64_t)pitch, lddy, w->rows, true,
                                   reinterpret_cast<float *>(ws + pb_at),
-                                  static_cast<uint16_t *>(db), false, false};
+                                  static_cast<uint16_t *>(db)};
     if (ng)
         EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, gr, ng, n, bf16, splits,
                                                 reinterpret_cast<uint8_t *>(ws + used_at),

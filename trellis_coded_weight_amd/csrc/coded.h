@@ -15,8 +15,9 @@
 // compute unit a fill as large as its share of many a matrix's codes, and 64
 // random LDS reads of a wave meet in few banks.
 //   mul1: h = A s mod 2^32 (one 32-bit product; two 24-bit ones and a shift-add
-//     measured 0-7 % slower), beta = the sum of h's bytes (v_sad_u8), taken as the binary16 number 1024 + beta by placing
-//     it in that number's mantissa, two states in one register.  Then
+//     measured 0-7 % slower), beta = the sum of h's bytes (v_sad_u8), taken as the
+//     binary16 number 1024 + beta by placing it in that number's mantissa, two
+//     states in one register.  Then
 //     d = beta - 510 (exact) and level = fma(d, k_hi, fma(d, k_lo, e)) in
 //     binary16 with k_hi + k_lo = 1 / std and e = (510 - mean) / std: equal bit
 //     for bit to the table's binary16 rounding for every beta in 0..1020 that
@@ -37,8 +38,10 @@ using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
-// 4-byte aligned
+// with the alignment of their elements
 using f32x4u = float __attribute__((ext_vector_type(4), aligned(4)));
+using u32x4u = uint32_t __attribute__((ext_vector_type(4), aligned(2)));
+using u32x2u = uint32_t __attribute__((ext_vector_type(2), aligned(2)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
@@ -386,15 +389,15 @@ hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void
                          int64_t n, bool bf16, uint16_t *xh, float *xs, hipStream_t stream);
 
 // Few rows: part[split][n][rows], sums over a split's columns of x' and the
-// levels, from x' and its scales or, where xh is null, from x itself (wide_x: its
-// rows start on 16 bytes).  With xh null and arrived not (run = 1), also y itself;
-// arrived: zero, one count for each group and 128 rows of W, zero again afterwards.
+// levels, from x' and its scales or, where xh is null, from x itself.  With xh null
+// and arrived not (run = 1), also y itself; arrived: zero, one count for each group
+// and 128 rows of W, zero again afterwards.
 struct RowsArgs {
     const uint16_t *xh;
     const float *xs;
     const void *x;
     int64_t ldx;
-    bool wide_x, bf16;
+    bool bf16;
     int64_t n;
     int split, run;           // splits of 2,048 columns; tiles of 16 rows of W a workgroup
     float *part;
@@ -447,7 +450,6 @@ struct ShrinkArgs {
     int k;
     uint16_t *v, *vt;
     int64_t ldvt;
-    bool wide_a, wide_x;      // set by the launcher
 };
 hipError_t launch_shrink(const AdapterArgs &ad, const ShrinkArgs *p, int products, int64_t n,
                          bool bf16, hipStream_t stream);
@@ -471,7 +473,6 @@ struct GradArgs {
     bool transposed;
     float *part;
     uint16_t *out;
-    bool wide_q, wide_out;    // set by the launcher
 };
 // used: [splits][count] bytes, set to whether a split has rows of an adapter (the
 // parts of those that have none are not written).

@@ -218,8 +218,8 @@ template <int BM, int BN, int WM, int WN, bool BF, bool AD>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w, int64_t n,
             int m, int k, const int32_t *__restrict__ offsets, int g0, int ng, int m_tiles,
-            int total, AdapterArgs ad, const uint16_t *__restrict__ ad_b, bool wide_b,
-            const uint16_t *__restrict__ v, uint16_t *__restrict__ y, int64_t ldy, bool wide_y) {
+            int total, AdapterArgs ad, const uint16_t *__restrict__ ad_b,
+            const uint16_t *__restrict__ v, uint16_t *__restrict__ y, int64_t ldy) {
     constexpr int kThreads = 64 * WM * WN, SM = BM / WM, SN = BN / WN, TM = SM / 16, TN = SN / 16;
     constexpr int kPiecesW = BM * 8 / kThreads, kPiecesX = BN * 8 / kThreads;
     constexpr int kPieces = kPiecesW + kPiecesX;          // 16-byte pieces a thread loads a slice
@@ -377,8 +377,8 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
                 for (int kk = 0; kk < ad.rank_pad; kk += 32) {
                     const uint16_t *ap = ab + (size_t)mr * ad.rank + kk + 8 * g;
                     u32x4 a = {0u, 0u, 0u, 0u};
-                    if (wide_b) {
-                        if (kk + 8 * g < ad.rank) a = *reinterpret_cast<const u32x4 *>(ap);
+                    if (kk + 8 * g + 8 <= ad.rank) {
+                        a = *reinterpret_cast<const u32x4u *>(ap);
                     } else {
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
@@ -420,12 +420,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
             const int64_t tok = t0 + 16 * j + row;
             if (tok >= hi || m0 + c >= m) continue;
             uint16_t *yo = y + tok * ldy + m0 + c;
-            if (wide_y) {
-                *reinterpret_cast<u32x4 *>(yo) = o;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) yo[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
-            }
+            *reinterpret_cast<u32x4u *>(yo) = o;
         }
     }
 }
@@ -437,8 +432,8 @@ pack_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int k,
     if (i >= n * (k / 8)) return;
     const int64_t row = i / (k / 8);
     const int c = (int)(i - row * (k / 8)) * 8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) out[row * k + c + j] = x[row * ldx + c + j];
+    *reinterpret_cast<u32x4 *>(out + row * k + c) =
+        *reinterpret_cast<const u32x4u *>(x + row * ldx + c);
 }
 
 template <int LV, int K, int HB>
@@ -504,12 +499,10 @@ hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_
     const AdapterArgs args = ad ? *ad : AdapterArgs{};
     const uint16_t *xx = static_cast<const uint16_t *>(x), *bb = static_cast<const uint16_t *>(b);
     uint16_t *yy = static_cast<uint16_t *>(y);
-    const bool wide_b = reinterpret_cast<uintptr_t>(b) % 16 == 0 && args.rank % 8 == 0;
-    const bool wide_y = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy % 8 == 0;
 #define EXL3_GEMM_T(BM, BN, WM, WN, BF, AD)                                                      \
     hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, BF, AD>), dim3((unsigned)total),             \
                        dim3(64 * WM * WN), 0, stream, xx, ldx, dense, n, m, k, offsets, g0, ng,  \
-                       m_tiles, total, args, bb, wide_b, v, yy, ldy, wide_y)
+                       m_tiles, total, args, bb, v, yy, ldy)
 #define EXL3_GEMM(BM, BN, WM, WN)                                                                \
     do {                                                                                         \
         const int m_tiles = (m + BM - 1) / BM;                                                   \

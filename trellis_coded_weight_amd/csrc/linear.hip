@@ -25,7 +25,7 @@ constexpr int kKeep = 4;
 
 template <bool BF, int THREADS>
 __global__ void __launch_bounds__(THREADS)
-rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had, bool wide,
+rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had,
               const float *__restrict__ sv, const int32_t *__restrict__ offsets, int groups,
               uint16_t *__restrict__ xh, float *__restrict__ xs) {
     __shared__ float wave_big[THREADS / 64];
@@ -40,15 +40,10 @@ rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had, bo
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = 0.0f;
         if (col < cols) {
+            const u32x4 w = *reinterpret_cast<const u32x4u *>(xr + col);
             uint16_t q[8];
-            if (wide) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(xr + col);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) q[i] = xr[col + i];
-            }
+            for (int i = 0; i < 8; ++i) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
             const f32x4 s0 = *reinterpret_cast<const f32x4u *>(sv + col);
             const f32x4 s1 = *reinterpret_cast<const f32x4u *>(sv + col + 4);
 #pragma unroll
@@ -126,7 +121,6 @@ __device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *
             const uint16_t *b = static_cast<const uint16_t *>(ad.b) +
                                 ((size_t)id * rows + row) * ad.rank;
             const uint16_t *vt = v + tok * ad.rank_pad;
-            const bool wide = reinterpret_cast<uintptr_t>(ad.b) % 16 == 0 && ad.rank % 8 == 0;
             for (int k = 0; k < ad.rank; k += 8) {
                 const u32x4 vk = *reinterpret_cast<const u32x4 *>(vt + k);
                 float vf[8];
@@ -136,8 +130,8 @@ __device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint16_t *bi = b + (size_t)i * ad.rank + k;
-                    if (wide) {
-                        const u32x4 bk = *reinterpret_cast<const u32x4 *>(bi);
+                    if (k + 8 <= ad.rank) {
+                        const u32x4 bk = *reinterpret_cast<const u32x4u *>(bi);
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             z[i] += vf[c] * act_load(bf16, (uint16_t)(bk[c >> 1] >> (16 * (c & 1))));
@@ -154,12 +148,7 @@ __device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *
     for (int i = 0; i < 4; ++i)
         o[i] = bf16 ? Act<true>::store2(z[2 * i], z[2 * i + 1])
                     : Act<false>::store2(z[2 * i], z[2 * i + 1]);
-    if (reinterpret_cast<uintptr_t>(y) % 16 == 0) {
-        *reinterpret_cast<u32x4 *>(y) = u32x4{o[0], o[1], o[2], o[3]};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
-    }
+    *reinterpret_cast<u32x4u *>(y) = u32x4u{o[0], o[1], o[2], o[3]};
 }
 
 // ---- few rows ----
@@ -248,15 +237,10 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
                 if (in && row < here) {
                     const uint16_t *xp = static_cast<const uint16_t *>(a.x) +
                                          (t0 + row) * a.ldx + col;
+                    const u32x4 w = *reinterpret_cast<const u32x4u *>(xp);
                     uint16_t q[8];
-                    if (a.wide_x) {
-                        const u32x4 w = *reinterpret_cast<const u32x4 *>(xp);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) q[i] = xp[i];
-                    }
+                    for (int i = 0; i < 8; ++i) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         o[i] = act_load(a.bf16, q[i]) * (i < 4 ? s0[i] : s1[i - 4]);
@@ -641,10 +625,9 @@ hipError_t coded_rows_t(const WeightArgs &w, const int32_t *offsets, const RowsA
 hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void *x, int64_t ldx,
                          int64_t n, bool bf16, uint16_t *xh, float *xs, hipStream_t stream) {
     const uint16_t *xx = static_cast<const uint16_t *>(x);
-    const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % 8 == 0;
 #define EXL3_ROTATE(BF, THREADS)                                                               \
     hipLaunchKernelGGL((rotate_kernel<BF, THREADS>), dim3((unsigned)n), dim3(THREADS), 0, stream, \
-                       xx, ldx, w.cols, w.had, wide, w.sv, offsets, w.groups, xh, xs)
+                       xx, ldx, w.cols, w.had, w.sv, offsets, w.groups, xh, xs)
     // a round a row while that takes at most 512 lanes
     if (bf16 && w.cols <= 2048)
         EXL3_ROTATE(true, 256);
