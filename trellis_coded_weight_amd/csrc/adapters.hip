@@ -58,28 +58,33 @@ shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
         if ((turn & (gridDim.y - 1)) != blockIdx.y) continue;      // gridDim.y: a power of two
         const int id = __shfl(id_r, __ffs(firsts) - 1);
         const uint16_t *ar = p.a + (size_t)id * ad.rank * k + 8 * g;
+        uint32_t row_at[RT];                     // past the rank: the last, made zero
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+            row_at[t] = (uint32_t)(16 * t + r < ad.rank ? 16 * t + r : ad.rank - 1) * (uint32_t)k;
         f32x4 acc[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr int U = RT == 1 ? 8 : RT == 8 ? 2 : 4;
+        constexpr int U = RT == 1 ? 8 : RT == 2 ? 4 : 2;
+        const u32x4 zero = {0u, 0u, 0u, 0u};
         for (int c0 = wv * 32; c0 < k; c0 += 32 * kWaves * U) {
+            // all loads at once; past the end they repeat the first step's, made zero
             u32x4 xv[U], av[U][RT];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const int c = c0 + 32 * kWaves * j;
-                xv[j] = u32x4{0u, 0u, 0u, 0u};
-                if (c < k) xv[j] = load8(xr + c);
+                const int c = c0 + 32 * kWaves * j < k ? c0 + 32 * kWaves * j : c0;
+                xv[j] = load8(xr + c);
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    av[j][t] = u32x4{0u, 0u, 0u, 0u};
-                    if (c < k && 16 * t + r < ad.rank)
-                        av[j][t] = load8(ar + (size_t)(16 * t + r) * k + c);
-                }
+                for (int t = 0; t < RT; ++t) av[j][t] = load8(ar + row_at[t] + c);
             }
 #pragma unroll
-            for (int j = 0; j < U; ++j)
+            for (int j = 0; j < U; ++j) {
+                const bool in = c0 + 32 * kWaves * j < k;
+                const u32x4 xj = in ? xv[j] : zero;
 #pragma unroll
-                for (int t = 0; t < RT; ++t) acc[t] = Act<BF>::mfma(av[j][t], xv[j], acc[t]);
+                for (int t = 0; t < RT; ++t)
+                    acc[t] = Act<BF>::mfma(in && 16 * t + r < ad.rank ? av[j][t] : zero, xj, acc[t]);
+            }
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) sums[wv][t][lane] = acc[t];
