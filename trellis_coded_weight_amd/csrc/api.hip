@@ -923,7 +923,8 @@ int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
         }
         p.xh_at = p.own_x ? 0 : c.take(n * w.cols * 2);
         p.xs_at = p.own_x ? 0 : c.take(n * sizeof(float));
-        p.part_at = c.take(n * w.rows * p.split * sizeof(float));
+        if (p.form == kFewRows || p.split > 1)
+            p.part_at = c.take(n * w.rows * p.split * sizeof(float));
         return EXL3_OK;
     }
     const size_t one = (size_t)w.rows * w.cols * 2;
@@ -956,7 +957,8 @@ int run_product(exl3_ctx *ctx, const Product &p) {
             if (p.finish) return EXL3_OK;
         } else {
             EXL3_HIP(ctx, exl3::launch_coded_tiles(w, p.offsets, xh, xs, p.n, p.per, p.split, part,
-                                                   ctx->stream));
+                                                   p.bf16, p.ad, v, p.y, p.ldy, ctx->stream));
+            if (p.split == 1) return EXL3_OK;
         }
         EXL3_HIP(ctx, exl3::launch_finish(w, p.offsets, part, p.split, p.n, p.bf16, p.ad, v, p.y,
                                           p.ldy, ctx->stream));

@@ -411,11 +411,13 @@ hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const 
                              hipStream_t stream);
 
 // part[split][n][rows]: sums over a split's columns of x' and the levels, `per`
-// (32, 64 or 128) rows of x at a time, staged in shared memory.  packed is
-// 16-byte aligned and decoded by formula (lv_kind is not kLevelsTable).
+// (32, 64 or 128) rows of x at a time, staged in shared memory; with split = 1 y
+// itself instead.  packed is 16-byte aligned and decoded by formula (lv_kind is
+// not kLevelsTable).
 hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
                               const float *xs, int64_t n, int per, int split, float *part,
-                              hipStream_t stream);
+                              bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
+                              int64_t ldy, hipStream_t stream);
 
 // y = su H_l (sum of the parts) scale / had, plus the adapters' products v B^T.
 hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const float *part, int split,

@@ -517,16 +517,21 @@ hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_
         else                                                                                     \
             EXL3_GEMM_T(BM, BN, WM, WN, false, false);                                           \
     } while (0)
-    // A round of large tiles, one a compute unit, takes about 12 parts of time
-    // where a round of small ones, two a compute unit, takes 8 and a half empty
-    // one 5 (k = 4096: 97, 65 and 40 us); a group's last tile counts as whole.
-    const int64_t large = (int64_t)((m + 255) / 256) * (offsets ? n / 256 + ng : (n + 255) / 256);
-    const int64_t small = (int64_t)((m + 127) / 128) * (offsets ? n / 128 + ng : (n + 127) / 128);
-    const int64_t rest = small % (2 * n_cu);
-    const int64_t cost_large = 12 * ((large + n_cu - 1) / n_cu);
-    const int64_t cost_small = 8 * (small / (2 * n_cu)) + (rest > n_cu ? 8 : rest > 0 ? 5 : 0);
-    if (cost_large <= cost_small)
+    // A round of large tiles, one a compute unit, takes 97 us at k = 4096, one of
+    // 128 x 256 tiles 62, one of small tiles, two a compute unit, 65, and half a
+    // round of these 40; a group's last tile counts as whole.
+    auto tiles = [&](int bm, int bn) {
+        return (int64_t)((m + bm - 1) / bm) * (offsets ? n / bn + ng : (n + bn - 1) / bn);
+    };
+    auto rounds = [&](int64_t t) { return (t + n_cu - 1) / n_cu; };
+    const int64_t small = tiles(128, 128), rest = small % (2 * n_cu);
+    const int64_t cost_small = 65 * (small / (2 * n_cu)) + (rest > n_cu ? 65 : rest > 0 ? 40 : 0);
+    const int64_t cost_mid = 62 * rounds(tiles(128, 256));
+    const int64_t cost_large = 97 * rounds(tiles(256, 256));
+    if (cost_large <= cost_mid && cost_large <= cost_small)
         EXL3_GEMM(256, 256, 2, 4);
+    else if (cost_mid < cost_small)
+        EXL3_GEMM(128, 256, 2, 4);
     else
         EXL3_GEMM(128, 128, 2, 2);
 #undef EXL3_GEMM_T

@@ -384,12 +384,23 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
 // 16 weights, the operands of two products: columns 16 g + 8 f on, g its half of
 // the wave.  Piece s of 16 bytes of row r of x' holds its piece s ^ (r / 2 & 7):
 // reads meet no bank twice.
+// What the kernel needs to finish y itself (y null: it stores sums).
+struct TilesOut {
+    const float *scale, *su;
+    int had;
+    AdapterArgs ad;
+    const uint16_t *v;
+    bool bf16;
+    uint16_t *y;
+    int64_t ldy;
+};
+
 template <int LV, int K, int NT>
 __global__ void __launch_bounds__(256, NT == 8 ? 2 : NT == 4 ? 3 : 4)
 coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
                    const int32_t *__restrict__ offsets, int groups,
                    const uint16_t *__restrict__ xh, const float *__restrict__ xs, int64_t n,
-                   int split, int row_blocks, int total, float *__restrict__ part) {
+                   int split, int row_blocks, int total, float *__restrict__ part, TilesOut out) {
     constexpr int kRows = 16 * NT, kPieces = kRows * 8 / 256;   // of x', a thread and step
     constexpr int kX = kRows * 128, kPlace = kX + 1024 * K;     // bytes of a place: x', words
     // places: as many as leave room for two workgroups
@@ -397,6 +408,14 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
     __shared__ __align__(16) char ring[kRing * kPlace];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int r = lane & 31, g = lane >> 5;
+    if (offsets && out.y) {
+        // rows of no group, by all workgroups
+        const int64_t from = offsets[0], to = offsets[groups];
+        for (int64_t t = blockIdx.x; t < n && t < from; t += gridDim.x)
+            for (int c = threadIdx.x; c < rows; c += 256) out.y[t * out.ldy + c] = 0;
+        for (int64_t t = (to > 0 ? to : 0) + blockIdx.x; t < n; t += gridDim.x)
+            for (int c = threadIdx.x; c < rows; c += 256) out.y[t * out.ldy + c] = 0;
+    }
     // each die takes a run of tiles: row blocks of W one after the other for the
     // same rows of x'
     if (offsets) {
@@ -535,6 +554,75 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
         }
         if (s < steps) step(even, odd);
     }
+    if (out.y) {
+        // The left transform over the 128 rows and the factors, 64 rows of x' at a
+        // time.  A lane holds rows 8 q + 4 g + i of its wave's 32: the stages over i
+        // and q are in registers; those over g and the waves after shared memory,
+        // where a thread takes rows 8 p .. 8 p + 7 of every 32 of one row of x'.
+        constexpr int kPitch = 132;              // floats a row of x'
+        static_assert((kRows < 64 ? kRows : 64) * kPitch * 4 <= kRing * kPlace, "the sums fit");
+        float *sums = reinterpret_cast<float *>(ring);
+        wait_loads<0>();
+        barrier_in_place();
+        const float f = out.scale[e] / (float)out.had;
+        const float *su = out.su + (size_t)e * rows + rb * 128;
+#pragma unroll
+        for (int j0 = 0; j0 < NJ; j0 += 2) {
+            if (j0) __syncthreads();             // the last 64 have been read
+#pragma unroll
+            for (int j = j0; j < j0 + 2 && j < NJ; ++j) {
+                f32x16 z = acc[j];
+#pragma unroll
+                for (int s = 1; s < 16; s <<= 1)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!(i & s)) {
+                            const float a = z[i], b = z[i + s];
+                            z[i] = a + b;
+                            z[i + s] = a - b;
+                        }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<f32x4 *>(sums + (32 * (j - j0) + r) * kPitch + 32 * wv + 8 * q +
+                                               4 * g) =
+                        f32x4{z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]};
+            }
+            __syncthreads();
+            const int t = threadIdx.x >> 2, p = threadIdx.x & 3;
+            const int64_t tok = t0 + 32 * j0 + t;
+            if (tok >= hi || 32 * j0 + t >= kRows) continue;
+            float z[4][8];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const f32x4 *at = reinterpret_cast<const f32x4 *>(sums + t * kPitch + 32 * w + 8 * p);
+                const f32x4 a = at[0], b = at[1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    z[w][i] = a[i] + b[i];
+                    z[w][i + 4] = a[i] - b[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = z[0][i] + z[1][i], b = z[0][i] - z[1][i];
+                const float c = z[2][i] + z[3][i], d = z[2][i] - z[3][i];
+                const bool whole = out.had == 128;
+                z[0][i] = whole ? a + c : a;
+                z[1][i] = whole ? b + d : b;
+                z[2][i] = whole ? a - c : c;
+                z[3][i] = whole ? b - d : d;
+            }
+            const float ft = f * xs[tok];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int row = 32 * w + 8 * p;
+                if (rb * 128 + row < rows)
+                    finish_row(z[w], ft, su + row, out.ad, out.v, tok, rb * 128 + row, rows,
+                               out.bf16, out.y + tok * out.ldy + rb * 128 + row);
+            }
+        }
+        return;
+    }
     // column (row of x') 32 j + r, rows 8 q + 4 g .. of the wave's 32
     const int row0 = rb * 128 + wv * 32 + 4 * g;
 #pragma unroll
@@ -665,14 +753,18 @@ hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const 
 
 hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
                               const float *xs, int64_t n, int per, int split, float *part,
-                              hipStream_t stream) {
+                              bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
+                              int64_t ldy, hipStream_t stream) {
+    // one split: the kernel finishes y
+    const TilesOut out{w.scale, w.su, w.had, ad ? *ad : AdapterArgs{}, v, bf16,
+                       split == 1 ? static_cast<uint16_t *>(y) : nullptr, ldy};
     const int row_blocks = (w.rows + 127) / 128;
     const int64_t n_tiles = offsets ? n / per + w.groups : (n + per - 1) / per;
     const int total = (int)(n_tiles * row_blocks * split);
 #define EXL3_TILES_NT(LV, KK, NT)                                                               \
     hipLaunchKernelGGL((coded_tiles_kernel<LV, KK, NT>), dim3((unsigned)total), dim3(256), 0,   \
                        stream, w.packed, w.lv, w.rows, w.cols, offsets, w.groups, xh, xs, n,    \
-                       split, row_blocks, total, part)
+                       split, row_blocks, total, part, out)
 #define EXL3_TILES(LV, KK)                                                                      \
     case KK:                                                                                    \
         if (per == 32)                                                                          \
