@@ -423,16 +423,19 @@ typedef struct {
  *          elements apart; in = cols, or rows when transposed
  *   y      [n][out] of the same type, rows ldy elements apart; out = the other
  *          side.  x and y share no element.
- * Products are summed in binary32 and rounded once to the type of y.  Few rows
- * (not transposed) are multiplied by the levels themselves, with the
- * transformed activations in binary16 under a power-of-two scale for each 256
- * columns; many rows by W rounded to the type of x.  A row of x with a NaN or
- * an infinity gives a row of y without finite values; other rows are not
- * affected.  n may be 0; at most 2^24 rows.
+ * Products are summed in binary32 and rounded once to the type of y.  Up to 512
+ * rows (not transposed) are multiplied by the levels themselves, with the
+ * transformed activations in binary16 under a power-of-two scale of each row
+ * (each 256 columns of it); more rows, and the other direction, by W rounded to
+ * the type of x.  A row of x with a NaN or an infinity gives a row of y without
+ * finite values; other rows are not affected.  Results do not depend on
+ * scheduling.  n may be 0; at most 2^24 rows.
  * Asynchronous.  The context's workspace grows on demand: to capture the call
  * in a graph, make a call with the same arguments on the same stream first
  * (a growth during capture is refused with EXL3_ENOMEM).  Workspaces are kept
- * until the context is destroyed, so a captured graph stays valid until then.
+ * until the context is destroyed, so a captured graph stays valid until then;
+ * its replays use the context's workspace and are ordered against the context's
+ * other calls by the caller.
  * Errors: EXL3_EINVAL, EXL3_EUNSUPPORTED, EXL3_ENOMEM (also when one dense
  * matrix does not fit the context's scratch bound), EXL3_EHIP.
  */

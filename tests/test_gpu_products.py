@@ -483,7 +483,7 @@ def _calls(T, n):
     return run
 
 
-@pytest.mark.parametrize("n", [12, 300])
+@pytest.mark.parametrize("n", [3, 12, 300])
 def test_repeats_are_bit_equal_on_any_stream(T, n):
     run = _calls(T, n)
     x, _ = rows_of(n, 384, BF, 225)
@@ -501,7 +501,7 @@ def test_repeats_are_bit_equal_on_any_stream(T, n):
         assert torch.equal(a, b) and torch.equal(a, d)
 
 
-@pytest.mark.parametrize("n", [12, 300])
+@pytest.mark.parametrize("n", [3, 12, 300])
 def test_graph_replays(T, n):
     run = _calls(T, n)
     c = T.Context(0)
@@ -662,3 +662,47 @@ def test_timing_counts_a_product(T, ctx):
     ms, launches, tiles = ctx.read_timing("product")
     ctx.set_timing(False)
     assert launches == 1 and tiles == 8 * 16 and ms > 0
+
+
+@pytest.mark.parametrize("pitch", [1 << 22, (1 << 22) + 8])
+def test_rows_far_apart(T, ctx, pitch):
+    """Rows of x so far apart that their offsets pass 2^27 bytes, and the pitch from which rows
+    are packed before the product."""
+    w = random_weight(128, 128, 2, 64, 311)
+    x, x64 = rows_of(20, 128, FP, 312)
+    far = torch.empty(19 * pitch + 128, dtype=FP, device=DEV)
+    far = torch.as_strided(far, (20, 128), (pitch, 1))
+    far.copy_(x)
+    m = dense(w)
+    y = ctx.linear(far, on_gpu(T, w), transpose=True)
+    check(y, x64 @ m, spread_of(x64, m.T), inner_of(False, FP))
+    y = ctx.linear(far, on_gpu(T, w))
+    check(y, x64 @ m.T, spread_of(x64, m), inner_of(False, FP))
+
+
+@pytest.mark.parametrize("sizes", [[9, 0, 30, 17, 1], [8, 8, 8, 8], [33, 0, 0, 0, 0, 0, 0, 0]])
+def test_few_rows_a_group_on_average(T, ctx, sizes):
+    """Groups with more rows than the kernel takes at a time."""
+    w = random_weight(192, 320, 2, 64, 321, groups=len(sizes))
+    n = sum(sizes)
+    x, x64 = rows_of(n, 320, BF, 322)
+    cut = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    for repeat in range(2):          # the second call finds the first's counts at zero
+        y = ctx.grouped_linear(x, on_gpu(T, w), torch.from_numpy(cut).to(DEV))
+        for e in range(len(sizes)):
+            if sizes[e]:
+                m = dense(w, group=e)
+                xe = x64[cut[e]:cut[e + 1]]
+                check(y[cut[e]:cut[e + 1]], xe @ m.T, spread_of(xe, m), inner_of(True, BF))
+
+
+@pytest.mark.parametrize("n", [1, 3, 4])
+def test_one_launch_and_three_agree(T, ctx, n):
+    """Rows that the smallest calls' kernel finishes itself, and the same among others."""
+    w = random_weight(384, 2304, 2, 128, 331)
+    x, x64 = rows_of(16, 2304, FP, 332)
+    m = dense(w)
+    g = on_gpu(T, w)
+    want, spread = x64 @ m.T, spread_of(x64, m)
+    check(ctx.linear(x[:n], g), want[:n], spread[:n], inner_of(True, FP))
+    check(ctx.linear(x, g), want, spread, inner_of(True, FP))

@@ -9,3 +9,4 @@ from .binding import (  # noqa: F401
     EXL3_EINVAL, EXL3_ENOMEM, EXL3_ENONFINITE, EXL3_EUNSUPPORTED, EXL3_F16, EXL3_F32, EXL3_OK, EXL3_ROW_MAJOR, EXL3_TILE_MAJOR, library_path, load_library,
     quantize_matrix, scratch_per_tile, version,
 )
+from .autograd import coded_adapter_linear, coded_grouped_linear, coded_linear  # noqa: F401

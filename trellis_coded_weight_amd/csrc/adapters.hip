@@ -30,7 +30,7 @@ shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
     constexpr int kWaves = RT <= 4 ? 16 : 8;
     __shared__ f32x4 sums[kWaves][RT][64];
     const ShrinkArgs p = blockIdx.z ? p1 : p0;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 15, g = lane >> 4, k = p.k;
     const int64_t t0 = (int64_t)blockIdx.x * 16;
     const int64_t tok = t0 + r < n ? t0 + r : n - 1;
@@ -149,7 +149,7 @@ template <bool BF, int RT>
 __global__ void __launch_bounds__(256)
 adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t per_split,
                     uint8_t *__restrict__ used) {
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 15, g = lane >> 4, id = blockIdx.y;
     const int first = (g0.k + 255) / 256;
     const bool second = (int)blockIdx.x >= first;

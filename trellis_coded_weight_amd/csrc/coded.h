@@ -45,6 +45,12 @@ using u32x2u = uint32_t __attribute__((ext_vector_type(2), aligned(2)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
+// The wave's number in its workgroup, as a value the compiler knows to be the
+// same for all lanes.
+__device__ __forceinline__ int wave_number() {
+    return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+
 // How levels are found; the values are template arguments of the kernels.
 enum { kLevelsMul1 = 0, kLevelsHalves = 1, kLevelsTable = 2 };
 

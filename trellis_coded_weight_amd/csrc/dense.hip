@@ -40,7 +40,7 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
     constexpr int kPitch = HB * 2 + 16;          // bytes a column of the block takes in LDS
     constexpr int kParts = BF ? 1 : 2, NT = HB / 16, NP = HB / 32;
     __shared__ __align__(16) char mid[kParts][HB * kPitch];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 15, g = lane >> 4;
     const int e = g0 + blockIdx.y, blocks = cols / HB;
     const int br = blockIdx.x / blocks, bc = blockIdx.x % blocks;
@@ -227,7 +227,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
     constexpr int kPitch = SM * 2 + 16;                   // bytes a row of y takes in the epilogue
     static_assert(WM * WN * 16 * kPitch <= kRing * kSlice * 2, "the epilogue fits the ring");
     __shared__ __align__(16) uint16_t ring[kRing * kSlice];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 15, g = lane >> 4, wm = wv % WM, wn = wv / WM;
     // each die takes a run of tiles
     if (offsets) {

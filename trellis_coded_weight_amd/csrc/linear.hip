@@ -175,7 +175,7 @@ constexpr int kUnit = 256, kOwn = 8;
 constexpr int kOwnPitch = kUnit * 2 + 16;        // bytes of a row of a wave's own x'
 
 template <int LV, int K, bool OWN, bool FINISH>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, 4)     // two workgroups a compute unit
 coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols, int Kr,
                   int had, const float *__restrict__ scale, const float *__restrict__ su,
                   const float *__restrict__ sv, const int32_t *__restrict__ offsets, int groups,
@@ -184,7 +184,7 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
     __shared__ f32x4 sums[2][8][64];
     __shared__ __align__(16) char own[OWN ? 8 * kOwn * kOwnPitch : 16];
     __shared__ uint32_t before;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 15, g = lane >> 4;
     const int row_tiles = rows / 16, runs = (row_tiles + a.run - 1) / a.run;
     const int rt0 = blockIdx.x % runs * a.run, sp = blockIdx.x / runs, e = blockIdx.y;
@@ -209,14 +209,15 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
     const int quads = c0 >= cols ? 0 : cols - c0 >= kUnit ? 4 : (cols - c0) / 64;
     const uint32_t *wcol = packed + ((size_t)e * row_tiles * (cols / 16) + c0 / 16 + g) * (8 * kk);
     const size_t wrow = (size_t)(cols / 16) * (8 * kk);
-    uint32_t d[4][RowWords<K>::N];
-    auto load_tile = [&](int rt) {
+    using Words = uint32_t[4][RowWords<K>::N];
+    auto load_tile = [&](int rt, Words &d) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             if (q < quads) load_row<K>(wcol + rt * wrow + q * 32 * kk, r, d[q]);
     };
     for (int64_t t0 = lo; t0 < hi; t0 += kStep) {
-        load_tile(rt0);
+        Words even, odd;
+        load_tile(rt0, even);
         u32x4 x[4][2];
         float x_scale = 0.0f;                    // of the lane's row of x'
         if (OWN) {
@@ -296,14 +297,9 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
                     x[q][1] = xp[1];
                 }
         }
-        for (int rt = rt0; rt < rt1; ++rt) {
+        auto one_tile = [&](int rt, Words &now, Words &next) {
             f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-            uint32_t now[4][RowWords<K>::N];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int i = 0; i < RowWords<K>::N; ++i) now[q][i] = d[q][i];
-            if (rt + 1 < rt1) load_tile(rt + 1);
+            if (rt + 1 < rt1) load_tile(rt + 1, next);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (q >= quads) break;
@@ -332,6 +328,10 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
                     }
                 }
             }
+        };
+        for (int rt = rt0; rt < rt1; rt += 2) {
+            one_tile(rt, even, odd);
+            if (rt + 1 < rt1) one_tile(rt + 1, odd, even);
         }
         // the next rows' sums may meet in the place that was just read
         if (t0 + kStep < hi) __syncthreads();
@@ -406,7 +406,7 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
     // places: as many as leave room for two workgroups
     constexpr int kRing = 4 * kPlace < 80 * 1024 ? 4 : 3;
     __shared__ __align__(16) char ring[kRing * kPlace];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 31, g = lane >> 5;
     if (offsets && out.y) {
         // rows of no group, by all workgroups
