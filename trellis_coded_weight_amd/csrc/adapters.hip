@@ -21,13 +21,13 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *p) {
 // each other; long prompts: one share).  The waves split the contraction and
 // their sums meet in shared memory.  The matrix instruction multiplies all 16
 // rows by each adapter and keeps those that have it: its rate is far from the
-// bound, which is the loads' latency (a wave has a few steps only, all loaded at
-// once up to 4,096 columns and rank 16) and reading A once per 16 rows from the
-// caches.  grid.z: up to two such products.
+// bound, which is what one compute unit can have under way of its misses (x and
+// A for 16 rows; 4,096 columns at rank 16 take 6 us beside 4.5 us of start and
+// sums).  grid.z: up to two such products.
 template <bool BF, int RT>
-__global__ void __launch_bounds__(RT <= 4 ? 1024 : 512)
+__global__ void __launch_bounds__(512)
 shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
-    constexpr int kWaves = RT <= 4 ? 16 : 8;
+    constexpr int kWaves = 8;
     __shared__ f32x4 sums[kWaves][RT][64];
     const ShrinkArgs p = blockIdx.z ? p1 : p0;
     const int lane = threadIdx.x & 63, wv = wave_number();
@@ -65,7 +65,7 @@ shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
         f32x4 acc[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr int U = RT == 1 ? 8 : RT == 2 ? 4 : 2;
+        constexpr int U = RT <= 2 ? 4 : 2;
         const u32x4 zero = {0u, 0u, 0u, 0u};
         for (int c0 = wv * 32; c0 < k; c0 += 32 * kWaves * U) {
             // all loads at once; past the end they repeat the first step's, made zero
@@ -303,12 +303,11 @@ hipError_t launch_shrink(const AdapterArgs &ad, const ShrinkArgs *p, int product
     const dim3 grid(tiles, share, (unsigned)products);
 #define EXL3_SHRINK(RT)                                                                     \
     do {                                                                                    \
-        const dim3 block(RT <= 4 ? 1024 : 512);                                             \
         if (bf16)                                                                           \
-            hipLaunchKernelGGL((shrink_kernel<true, RT>), grid, block, 0, stream, ad, q[0], \
+            hipLaunchKernelGGL((shrink_kernel<true, RT>), grid, dim3(512), 0, stream, ad, q[0], \
                                q[1], n);                                                    \
         else                                                                                \
-            hipLaunchKernelGGL((shrink_kernel<false, RT>), grid, block, 0, stream, ad, q[0],\
+            hipLaunchKernelGGL((shrink_kernel<false, RT>), grid, dim3(512), 0, stream, ad, q[0],\
                                q[1], n);                                                    \
     } while (0)
     if (ad.rank <= 16)

@@ -367,36 +367,44 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
             if (next == 0x7FFFFFFF) break;
             last = next;
             const uint16_t *ab = ad_b + (size_t)next * m * ad.rank;
+            const uint16_t *end = ad_b + (size_t)ad.count * m * ad.rank;
+            for (int kk = 0; kk < ad.rank_pad; kk += 32) {
+                // operands ahead of their products, the weights' side made zero past
+                // the rank
+                const int valid = ad.rank - kk - 8 * g;
+                u32x4 keep, av[TM], bv[TN];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                int mr = m0 + 16 * i + r;
-                mr = mr < m ? mr : m - 1;
-                f32x4 p[TN];
+                for (int c = 0; c < 4; ++c)
+                    keep[c] = valid >= 2 * c + 2 ? 0xFFFFFFFFu : valid == 2 * c + 1 ? 0xFFFFu : 0u;
 #pragma unroll
-                for (int j = 0; j < TN; ++j) p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                for (int kk = 0; kk < ad.rank_pad; kk += 32) {
+                for (int i = 0; i < TM; ++i) {
+                    int mr = m0 + 16 * i + r;
+                    mr = mr < m ? mr : m - 1;
                     const uint16_t *ap = ab + (size_t)mr * ad.rank + kk + 8 * g;
-                    u32x4 a = {0u, 0u, 0u, 0u};
-                    if (kk + 8 * g + 8 <= ad.rank) {
-                        a = *reinterpret_cast<const u32x4u *>(ap);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            if (kk + 8 * g + c < ad.rank)
-                                a[c >> 1] |= (uint32_t)ap[c] << (16 * (c & 1));
-                    }
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) {
-                        int64_t tok = t0 + 16 * j + r;
-                        tok = tok < hi ? tok : hi - 1;
-                        const u32x4 b = *reinterpret_cast<const u32x4 *>(v + tok * ad.rank_pad + kk + 8 * g);
-                        p[j] = Act<BF>::mfma(a, b, p[j]);
+                    av[i] = u32x4{0u, 0u, 0u, 0u};
+                    if (valid > 0) {
+                        if (end - ap >= 8)
+                            av[i] = *reinterpret_cast<const u32x4u *>(ap);
+                        else
+                            for (int c = 0; c < valid; ++c)
+                                av[i][c >> 1] |= (uint32_t)ap[c] << (16 * (c & 1));
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
+                for (int j = 0; j < TN; ++j) {
+                    int64_t tok = t0 + 16 * j + r;
+                    tok = tok < hi ? tok : hi - 1;
+                    bv[j] = *reinterpret_cast<const u32x4 *>(v + tok * ad.rank_pad + kk + 8 * g);
+                }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) acc[i][j][c] += idj[j] == next ? p[j][c] : 0.0f;
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+                        z = Act<BF>::mfma(av[i] & keep, bv[j], z);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[i][j][c] += idj[j] == next ? z[c] : 0.0f;
+                    }
             }
         }
     }
