@@ -243,6 +243,48 @@ def test_a_bad_row_stays_alone(T, ctx, n, bad):
     assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("n", [8, 200])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_row_stays_alone_in_the_other_direction(T, ctx, n, bad):
+    w = random_weight(384, 256, 3, 128, 145)
+    x, _ = rows_of(n, 384, BF, 146)
+    g = on_gpu(T, w)
+    clean = ctx.linear(x, g, transpose=True)
+    x[5, 200] = bad
+    y = ctx.linear(x, g, transpose=True)
+    assert not torch.isfinite(y[5]).any()
+    keep = torch.arange(n, device=DEV) != 5
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("n,per", [(1, 0), (31, 0), (3, 4), (90, 40)])
+@pytest.mark.parametrize("K,codebook", [(1, "mul1"), (2, "mcg"), (3, "mul1"), (4, "3inst")])
+def test_the_other_direction_in_tiles_meets_the_dense_form(T, ctx_of, n, per, K, codebook):
+    """Words that start on 8 bytes take the dense weights, aligned ones the tiles: both are within
+    their bounds of the 64-bit product.  Rows long enough to be split; the last tile of columns
+    is partly filled."""
+    groups = 3 if per else None
+    w = random_weight(2176, 192, K, 64, 147 + K, groups=groups)
+    c, g = ctx_of(codebook), on_gpu(T, w)
+    flat = torch.zeros(g.packed.numel() + 4, dtype=torch.int16, device=DEV)
+    flat[4:] = g.packed.reshape(-1)
+    h = T.CodedWeight(flat[4:].view(g.packed.shape), K, g.scale, g.su, g.sv, had_block=64)
+    assert h.packed.data_ptr() % 16 == 8
+    x, x64 = rows_of(n, 2176, FP, 148)
+    if groups is None:
+        m = dense(w, codebook).T
+        for u in (g, h):
+            check(c.linear(x, u, transpose=True), x64 @ m.T, spread_of(x64, m), inner_of(False, FP))
+        return
+    cut = np.array([0, n - per if n > per else 1, n - 1, n], np.int32)
+    at = torch.from_numpy(cut).to(DEV)
+    for u in (g, h):
+        y = c.grouped_linear(x, u, at, transpose=True)
+        for e in range(3):
+            m, xe = dense(w, codebook, group=e).T, x64[cut[e]:cut[e + 1]]
+            check(y[cut[e]:cut[e + 1]], xe @ m.T, spread_of(xe, m), inner_of(False, FP), "%d" % e)
+
+
 def test_zero_rows_and_zero_input(T, ctx):
     w = random_weight(128, 256, 2, 128, 151)
     g = on_gpu(T, w)
@@ -627,9 +669,9 @@ def test_refusals_leave_the_output(T, ctx):
     torch.cuda.synchronize()
     assert (y == 3.0).all()
     with T.Context(0, scratch_bytes=1000) as tiny:
-        wide = torch.zeros(100, 128, dtype=BF, device=DEV)
+        wide = torch.zeros(1000, 128, dtype=BF, device=DEV)      # rows that take dense weights
         with pytest.raises(T.Exl3Error) as e:
-            tiny.linear(wide, w, transpose=True)     # the direction that takes dense weights
+            tiny.linear(wide, w, transpose=True)
         assert e.value.code == T.EXL3_ENOMEM
 
 

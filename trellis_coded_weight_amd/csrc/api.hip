@@ -856,15 +856,18 @@ bool rows_aligned(const void *p, int64_t ld) {
 // The three forms of a product.  Few rows a group: workgroups stream the codes
 // once for 16 rows.  Some: tiles of 32 to 128 rows of x, the codes decoded once a
 // tile.  Many: the dense weights are written first, which pays when a group's
-// rows pass a few tiles; also the form of the other direction and of decoding by
-// table.
+// rows pass a few tiles; also the form of decoding by table.  The other direction
+// has the last two, and its tiles turn the levels: 4096 x 4096, K = 2, in tiles
+// and dense, us: 4 rows 17 and 58, 200 rows 35 and 56, 400 rows 44 and 55;
+// 4096 x 12288, K = 3: 100 rows 40 and 69, 300 rows 101 and 86; 16 of
+// 1408 x 2048, K = 2: 100 rows each 46 and 52, 400 rows 93 and 85.
 enum Form { kFewRows, kTiles, kDense };
 
 Form form_of(const exl3::WeightArgs &w, bool transpose, int64_t n) {
-    if (transpose) return kDense;
-    if (n <= (int64_t)16 * w.groups) return kFewRows;
     const bool tiles = w.lv_kind != exl3::kLevelsTable &&
                        reinterpret_cast<uintptr_t>(w.packed) % 16 == 0;
+    if (transpose) return tiles && n <= (int64_t)256 * w.groups ? kTiles : kDense;
+    if (n <= (int64_t)16 * w.groups) return kFewRows;
     if (tiles && n <= (int64_t)512 * w.groups) return kTiles;
     return n <= (int64_t)64 * w.groups ? kFewRows : kDense;
 }
@@ -891,10 +894,20 @@ struct Product {
     bool pack, own_x, finish;
 };
 
+// W's arguments as the product's direction sees them: rows the result's side.
+exl3::WeightArgs directed(const Product &p) {
+    exl3::WeightArgs w = *p.w;
+    if (p.transpose) {
+        std::swap(w.rows, w.cols);
+        std::swap(w.su, w.sv);
+    }
+    return w;
+}
+
 int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
-    const exl3::WeightArgs &w = *p.w;
+    const exl3::WeightArgs w = directed(p);
     const size_t n = (size_t)p.n;
-    p.form = form_of(w, p.transpose, p.n);
+    p.form = form_of(*p.w, p.transpose, p.n);
     if (p.form != kDense) {
         if (p.form == kFewRows) {
             // a wave has 256 columns; a workgroup up to four tiles of rows, as many as
@@ -934,12 +947,18 @@ int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
     p.batch = (int)std::min<size_t>((size_t)w.groups, ctx->scratch_limit / one);
     p.dense_at = c.take(one * p.batch);
     p.pack = !rows_aligned(p.x, p.ldx);
-    p.xpack_at = p.pack ? c.take(n * (p.transpose ? w.rows : w.cols) * 2) : 0;
+    p.xpack_at = p.pack ? c.take(n * w.cols * 2) : 0;
     return EXL3_OK;
 }
 
 int run_product(exl3_ctx *ctx, const Product &p) {
-    const exl3::WeightArgs &w = *p.w;
+    const exl3::WeightArgs w = directed(p);
+    exl3::AdapterArgs ad_args{};
+    if (p.ad) {
+        ad_args = *p.ad;
+        ad_args.b = p.ad_b;
+    }
+    const exl3::AdapterArgs *ad = p.ad ? &ad_args : nullptr;
     char *ws = ctx->d_work;
     const uint16_t *v = p.ad ? reinterpret_cast<const uint16_t *>(ws + p.v_at) : nullptr;
     if (p.form != kDense) {
@@ -952,19 +971,19 @@ int run_product(exl3_ctx *ctx, const Product &p) {
         if (p.form == kFewRows) {
             const exl3::RowsArgs a{p.own_x ? nullptr : xh, xs, p.x, p.ldx,
                                    p.bf16, p.n, p.split, p.run, part,
-                                   p.finish ? ctx->d_count : nullptr, p.ad, v, p.y, p.ldy};
+                                   p.finish ? ctx->d_count : nullptr, ad, v, p.y, p.ldy};
             EXL3_HIP(ctx, exl3::launch_coded_rows(w, p.offsets, a, ctx->stream));
             if (p.finish) return EXL3_OK;
         } else {
-            EXL3_HIP(ctx, exl3::launch_coded_tiles(w, p.offsets, xh, xs, p.n, p.per, p.split, part,
-                                                   p.bf16, p.ad, v, p.y, p.ldy, ctx->stream));
+            EXL3_HIP(ctx, exl3::launch_coded_tiles(w, p.offsets, xh, xs, p.n, p.transpose, p.per,
+                                                   p.split, part, p.bf16, ad, v, p.y, p.ldy, ctx->stream));
             if (p.split == 1) return EXL3_OK;
         }
-        EXL3_HIP(ctx, exl3::launch_finish(w, p.offsets, part, p.split, p.n, p.bf16, p.ad, v, p.y,
+        EXL3_HIP(ctx, exl3::launch_finish(w, p.offsets, part, p.split, p.n, p.bf16, ad, v, p.y,
                                           p.ldy, ctx->stream));
         return EXL3_OK;
     }
-    const int m = p.transpose ? w.cols : w.rows, k = p.transpose ? w.rows : w.cols;
+    const int m = w.rows, k = w.cols;
     uint16_t *dense = reinterpret_cast<uint16_t *>(ws + p.dense_at);
     const void *x = p.x;
     int64_t ldx = p.ldx;
@@ -976,7 +995,7 @@ int run_product(exl3_ctx *ctx, const Product &p) {
     }
     for (int g0 = 0; g0 < w.groups; g0 += p.batch) {
         const int ng = std::min(p.batch, w.groups - g0);
-        EXL3_HIP(ctx, exl3::launch_dense(w, p.offsets, p.n, g0, ng, p.transpose, p.bf16, dense,
+        EXL3_HIP(ctx, exl3::launch_dense(*p.w, p.offsets, p.n, g0, ng, p.transpose, p.bf16, dense,
                                          p.y, p.ldy, ctx->stream));
         EXL3_HIP(ctx, exl3::launch_gemm(x, ldx, dense, p.n, m, k, p.offsets, g0, ng, p.bf16, p.ad,
                                         p.ad_b, v, p.y, p.ldy, ctx->n_cu, ctx->stream));

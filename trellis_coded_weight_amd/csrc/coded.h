@@ -44,6 +44,8 @@ using u32x4u = uint32_t __attribute__((ext_vector_type(4), aligned(2)));
 using u32x2u = uint32_t __attribute__((ext_vector_type(2), aligned(2)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+using i16x4 = short __attribute__((ext_vector_type(4)));
 
 // The wave's number in its workgroup, as a value the compiler knows to be the
 // same for all lanes.
@@ -228,6 +230,13 @@ __device__ __forceinline__ void wait_loads() {
 __device__ __forceinline__ void load_to_lds(const void *from, void *to) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
                                      (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
+
+// Turns 4 x 16 elements of 16 bits: of 16 lanes, lane 4 j + q names elements
+// 4 q .. 4 q + 3 of row j, and lane i gets element i of rows 0..3.
+__device__ __forceinline__ u32x2 read_turned(const char *from) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) i16x4 *)from));
 }
 
 // The workgroup's barrier, across which neither memory accesses nor the
@@ -419,10 +428,12 @@ hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const 
 // part[split][n][rows]: sums over a split's columns of x' and the levels, `per`
 // (32, 64 or 128) rows of x at a time, staged in shared memory; with split = 1 y
 // itself instead.  packed is 16-byte aligned and decoded by formula (lv_kind is
-// not kLevelsTable).
+// not kLevelsTable).  transposed: the other direction, where w holds the sizes
+// and factors the other way round (rows and su are those of W's columns); packed
+// is as it was.
 hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
-                              const float *xs, int64_t n, int per, int split, float *part,
-                              bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
+                              const float *xs, int64_t n, bool transposed, int per, int split,
+                              float *part, bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
                               int64_t ldy, hipStream_t stream);
 
 // y = su H_l (sum of the parts) scale / had, plus the adapters' products v B^T.

@@ -395,8 +395,14 @@ struct TilesOut {
     int64_t ldy;
 };
 
-template <int LV, int K, int NT>
-__global__ void __launch_bounds__(256, NT == 8 ? 2 : NT == 4 ? 3 : 4)
+// The other direction, x C (T; rows and cols are then C's columns and rows): a
+// lane's 16 levels belong to 16 columns of the result, so the 16 lanes of a tile
+// hand them over as they are decoded, through 512 bytes of shared memory and the
+// reads that turn 4 x 16 elements; piece h of a row is at h ^ (row / 8), so that
+// neither side meets a bank twice.  A quarter of the decoding's time, on another
+// unit.
+template <int LV, int K, int NT, bool T>
+__global__ void __launch_bounds__(256, NT == 8 || (T && K == 4) ? 2 : NT == 4 || T ? 3 : 4)
 coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
                    const int32_t *__restrict__ offsets, int groups,
                    const uint16_t *__restrict__ xh, const float *__restrict__ xs, int64_t n,
@@ -404,8 +410,9 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
     constexpr int kRows = 16 * NT, kPieces = kRows * 8 / 256;   // of x', a thread and step
     constexpr int kX = kRows * 128, kPlace = kX + 1024 * K;     // bytes of a place: x', words
     // places: as many as leave room for two workgroups
-    constexpr int kRing = 4 * kPlace < 80 * 1024 ? 4 : 3;
-    __shared__ __align__(16) char ring[kRing * kPlace];
+    constexpr int kTurn = T ? 4 * 2048 : 0;                     // 2 KiB a wave
+    constexpr int kRing = 4 * kPlace + kTurn < 80 * 1024 ? 4 : 3;
+    __shared__ __align__(16) char ring[kRing * kPlace + kTurn];
     const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 31, g = lane >> 5;
     if (offsets && out.y) {
@@ -455,9 +462,14 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
     const int wq = word_wave * 64 + lane;
     int w_tile = rb * 8 + wq / (8 * K);
     w_tile = w_tile < row_tiles ? w_tile : row_tiles - 1;
-    const char *w_at = reinterpret_cast<const char *>(packed) +
-                       (((size_t)e * row_tiles + w_tile) * (cols / 16) + (size_t)first * 4) * (32 * K) +
-                       wq % (8 * K) * 16;
+    const char *w_at = reinterpret_cast<const char *>(packed);
+    if (T)
+        w_at += (((size_t)e * (cols / 16) + first * 4 + wq % (8 * K) / (2 * K)) * row_tiles + w_tile) *
+                    (32 * K) + wq % (2 * K) * 16;
+    else
+        w_at += (((size_t)e * row_tiles + w_tile) * (cols / 16) + (size_t)first * 4) * (32 * K) +
+                wq % (8 * K) * 16;
+    const size_t w_step = (size_t)(T ? row_tiles : 1) * (128 * K);
     int loaded = 0, fill = 0;
     auto load = [&]() {
         char *to = ring + fill * kPlace;
@@ -469,7 +481,7 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
         fill = fill + 1 < kRing ? fill + 1 : 0;
         // past the last step: repeats it, into a place that nobody reads
         x_at += loaded < steps ? 128 : 0;
-        w_at += loaded < steps ? 128 * K : 0;
+        w_at += loaded < steps ? w_step : 0;
     };
     // what a wave needs of a step: its rows' words (then their levels) and the
     // rows of x', for two times 32 columns
@@ -501,7 +513,24 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
     };
     auto decode = [&](Operands &o) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) decode_row<LV, K>(nullptr, r & 15, o.d[c], lv, o.w[c]);
+        for (int c = 0; c < 2; ++c) {
+            decode_row<LV, K>(nullptr, r & 15, o.d[c], lv, o.w[c]);
+            if constexpr (T) {
+                // (a wave's accesses of shared memory are done in their order)
+                char *tile = ring + kRing * kPlace + wv * 2048 + (lane >> 4) * 512;
+                const int row = lane & 15, q = lane & 3;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<u32x4 *>(tile + row * 32 + (h ^ (row >> 3)) * 16) = o.w[c][h];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const u32x2 v = read_turned(tile + (4 * j + (row >> 2)) * 32 +
+                                                ((q >> 1) ^ (j >> 1)) * 16 + 8 * (q & 1));
+                    o.w[c][j >> 1][2 * (j & 1)] = v[0];
+                    o.w[c][j >> 1][2 * (j & 1) + 1] = v[1];
+                }
+            }
+        }
     };
     f32x16 acc[NJ];
 #pragma unroll
@@ -752,8 +781,8 @@ hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const 
 }
 
 hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const uint16_t *xh,
-                              const float *xs, int64_t n, int per, int split, float *part,
-                              bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
+                              const float *xs, int64_t n, bool transposed, int per, int split,
+                              float *part, bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
                               int64_t ldy, hipStream_t stream) {
     // one split: the kernel finishes y
     const TilesOut out{w.scale, w.su, w.had, ad ? *ad : AdapterArgs{}, v, bf16,
@@ -761,10 +790,17 @@ hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const
     const int row_blocks = (w.rows + 127) / 128;
     const int64_t n_tiles = offsets ? n / per + w.groups : (n + per - 1) / per;
     const int total = (int)(n_tiles * row_blocks * split);
-#define EXL3_TILES_NT(LV, KK, NT)                                                               \
-    hipLaunchKernelGGL((coded_tiles_kernel<LV, KK, NT>), dim3((unsigned)total), dim3(256), 0,   \
-                       stream, w.packed, w.lv, w.rows, w.cols, offsets, w.groups, xh, xs, n,    \
+#define EXL3_TILES_T(LV, KK, NT, T)                                                             \
+    hipLaunchKernelGGL((coded_tiles_kernel<LV, KK, NT, T>), dim3((unsigned)total), dim3(256),   \
+                       0, stream, w.packed, w.lv, w.rows, w.cols, offsets, w.groups, xh, xs, n, \
                        split, row_blocks, total, part, out)
+#define EXL3_TILES_NT(LV, KK, NT)                                                               \
+    do {                                                                                        \
+        if (transposed)                                                                         \
+            EXL3_TILES_T(LV, KK, NT, true);                                                     \
+        else                                                                                    \
+            EXL3_TILES_T(LV, KK, NT, false);                                                    \
+    } while (0)
 #define EXL3_TILES(LV, KK)                                                                      \
     case KK:                                                                                    \
         if (per == 32)                                                                          \
@@ -794,6 +830,7 @@ hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const
         return hipErrorInvalidValue;
 #undef EXL3_TILES
 #undef EXL3_TILES_NT
+#undef EXL3_TILES_T
     return hipGetLastError();
 }
 
