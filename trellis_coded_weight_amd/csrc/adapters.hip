@@ -18,12 +18,16 @@ __device__ __forceinline__ u32x4 load8(const uint16_t *p) {
 // ---- v = alpha A x ----
 // A workgroup per 16 rows of x, and in grid.y the share of the rows' distinct
 // adapters it takes in turn (many requests: one each, so that they run beside
-// each other; long prompts: one share).  The waves split the contraction and
-// their sums meet in shared memory.  The matrix instruction multiplies all 16
-// rows by each adapter and keeps those that have it: its rate is far from the
-// bound, which is what one compute unit can have under way of its misses (x and
-// A for 16 rows; 4,096 columns at rank 16 take 6 us beside 4.5 us of start and
-// sums).  grid.z: up to two such products.
+// each other; long prompts: one or two shares).  The waves take 32 U columns of
+// the contraction at a time and their sums meet in shared memory.  The matrix
+// instruction multiplies all 16 rows by each adapter and keeps those that have
+// it: its rate is far from the bound, which is what one compute unit can have
+// under way of its misses, about 15 bytes a cycle: x and A for 16 rows, 4,096
+// columns, take 10 us at rank 16 and 21 us at rank 64, and neither loads in
+// larger groups (21 us) nor a workgroup for each 16 ranks (24 us) nor the
+// contraction in two workgroups (16 us with one adapter, 25 us with eight) nor
+// rows of one adapter on one die (as without) shorten them.  grid.z: up to two
+// such products.
 template <bool BF, int RT>
 __global__ void __launch_bounds__(512)
 shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
@@ -67,19 +71,19 @@ shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
         for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         constexpr int U = RT <= 2 ? 4 : 2;
         const u32x4 zero = {0u, 0u, 0u, 0u};
-        for (int c0 = wv * 32; c0 < k; c0 += 32 * kWaves * U) {
+        for (int c0 = wv * 32 * U; c0 < k; c0 += 32 * kWaves * U) {
             // all loads at once; past the end they repeat the first step's, made zero
             u32x4 xv[U], av[U][RT];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const int c = c0 + 32 * kWaves * j < k ? c0 + 32 * kWaves * j : c0;
+                const int c = c0 + 32 * j < k ? c0 + 32 * j : c0;
                 xv[j] = load8(xr + c);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) av[j][t] = load8(ar + row_at[t] + c);
             }
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const bool in = c0 + 32 * kWaves * j < k;
+                const bool in = c0 + 32 * j < k;
                 const u32x4 xj = in ? xv[j] : zero;
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
@@ -297,9 +301,9 @@ hipError_t launch_shrink(const AdapterArgs &ad, const ShrinkArgs *p, int product
     for (int i = 0; i < 2; ++i) q[i] = p[i < products ? i : 0];
     const unsigned tiles = (unsigned)((n + 15) / 16);
     // up to 16 distinct adapters a tile: a workgroup each while all workgroups run
-    // at once (one a compute unit; those without work would hold up the others)
+    // at once (two a compute unit; those without work would hold up the others)
     unsigned share = 16;
-    while (share > 1 && tiles * share * (unsigned)products > 256) share /= 2;
+    while (share > 1 && tiles * share * (unsigned)products > 512) share /= 2;
     const dim3 grid(tiles, share, (unsigned)products);
 #define EXL3_SHRINK(RT)                                                                     \
     do {                                                                                    \
