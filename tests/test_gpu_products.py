@@ -409,6 +409,27 @@ def test_adapter_linear(T, ctx, n, rows, cols, K, had, dtype, count, rank):
     check(y, x64 @ m.T + part, spread_of(x64, m) + s, inner_of(False, dtype))
 
 
+# sizes at which each tile of the matrix product takes the fewest rounds of 256 compute units, none
+# of them a multiple of the tile
+TILES = [(1450, 1470, 4032), (700, 2900, 4032), (901, 1500, 4160), (5, 4000, 4032)]
+
+
+@pytest.mark.parametrize("seed,n,rows", TILES)
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_every_tile_of_the_matrix_product(T, ctx, seed, n, rows, dtype):
+    """With the shortest contractions, alone and with adapters of an unaligned rank."""
+    cols = 64 if dtype is BF else 192
+    w = random_weight(rows, cols, 2, 64, seed)
+    g, m = on_gpu(T, w), dense(w)
+    x, x64 = rows_of(n, cols, dtype, seed + 1)
+    check(ctx.linear(x, g), x64 @ m.T, spread_of(x64, m), inner_of(False, dtype))
+    ad, A, B, al = adapters_of(T, rows, cols, 3, 7, dtype, seed + 2)
+    ids = ids_of(n, 3, seed + 3)
+    y = ctx.adapter_linear(x, g, ad, torch.from_numpy(ids).to(DEV))
+    part, s = adapter_forward(x64, A, B, al, ids)
+    check(y, x64 @ m.T + part, spread_of(x64, m) + s, inner_of(False, dtype))
+
+
 @pytest.mark.parametrize("n", [20, 200])
 def test_a_bad_adapter_stays_alone(T, ctx, n):
     """NaN and infinity in one adapter reach its own rows only."""

@@ -21,7 +21,7 @@
 //     d = beta - 510 (exact) and level = fma(d, k_hi, fma(d, k_lo, e)) in
 //     binary16 with k_hi + k_lo = 1 / std and e = (510 - mean) / std: equal bit
 //     for bit to the table's binary16 rounding for every beta in 0..1020 that
-//     the table holds (the tests compare all 65,536 states).  5.5 instructions
+//     the table holds (the tests compare all 65,536 states).  4.75 instructions
 //     a weight with the window.
 //   mcg, 3INST: w = a s + b mod 2^32 in the same way, masked, and the sum of
 //     its two binary16 halves for two states at once.

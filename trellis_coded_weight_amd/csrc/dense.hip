@@ -29,7 +29,9 @@ __device__ __forceinline__ uint32_t parity16(uint32_t v) { return __popc(v) & 1u
 // Then the scale, su and sv in binary32 and one rounding to the activations'
 // type.  Row-major and transposed output differ in the order of step 3's
 // operands: either way a lane holds four consecutive elements of the output.
-// The write of the weights bounds it.
+// 4096 x 4096, K = 2: 13.3 to 15 us, 2.5 TB/s written; the chain of decoding,
+// products and two passes through shared memory in each workgroup bounds it more
+// than the write (7.1 us) does.
 template <int LV, int K, int HB, bool BF, bool TR>
 __global__ void __launch_bounds__(HB * 4, 4)
 dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols, int Kr,
@@ -213,7 +215,9 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
 // the swizzle that spreads rows over the banks is in which piece each lane
 // fetches: piece s of row r holds k piece s ^ (r & 7), whose reads meet no bank
 // twice (4.2 cycles a read of 1 KiB measured, where a swizzle by three other
-// bits of r took 8.1).
+// bits of r took 8.1).  4,096 rows, 12288 x 4096, bfloat16: 300 us, 1,375 TFLOP/s,
+// its matrix units busy for 72 % of the cycles; the rest is mostly the barrier and
+// the reads it waits for, once a slice.
 template <int BM, int BN, int WM, int WN, bool BF, bool AD>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
 gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w, int64_t n,
@@ -525,23 +529,29 @@ hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_
         else                                                                                     \
             EXL3_GEMM_T(BM, BN, WM, WN, false, false);                                           \
     } while (0)
-    // A round of large tiles, one a compute unit, takes 97 us at k = 4096, one of
-    // 128 x 256 tiles 62, one of small tiles, two a compute unit, 65, and half a
-    // round of these 40; a group's last tile counts as whole.
+    // What a round of tiles takes at k = 4096, us: one tile a compute unit, of the
+    // smallest two (40 for half a round of these); a group's last tile counts as
+    // whole.  1,500 rows x 4,096 columns: 56 in 256 tiles of 128 x 192, 64 in 192 of
+    // 128 x 256; 5,000 rows: 149 in two rounds of 256 x 192, 194 in two of 256 x 256.
     auto tiles = [&](int bm, int bn) {
         return (int64_t)((m + bm - 1) / bm) * (offsets ? n / bn + ng : (n + bn - 1) / bn);
     };
     auto rounds = [&](int64_t t) { return (t + n_cu - 1) / n_cu; };
     const int64_t small = tiles(128, 128), rest = small % (2 * n_cu);
-    const int64_t cost_small = 65 * (small / (2 * n_cu)) + (rest > n_cu ? 65 : rest > 0 ? 40 : 0);
-    const int64_t cost_mid = 62 * rounds(tiles(128, 256));
-    const int64_t cost_large = 97 * rounds(tiles(256, 256));
-    if (cost_large <= cost_mid && cost_large <= cost_small)
-        EXL3_GEMM(256, 256, 2, 4);
-    else if (cost_mid < cost_small)
-        EXL3_GEMM(128, 256, 2, 4);
-    else
-        EXL3_GEMM(128, 128, 2, 2);
+    const int64_t cost[5] = {97 * rounds(tiles(256, 256)), 82 * rounds(tiles(256, 192)),
+                             62 * rounds(tiles(128, 256)), 54 * rounds(tiles(128, 192)),
+                             65 * (small / (2 * n_cu)) +
+                                 (rest > n_cu ? 65 : rest > 0 ? 40 : 0)};
+    int best = 0;
+    for (int i = 1; i < 5; ++i)
+        if (cost[i] < cost[best]) best = i;
+    switch (best) {
+        case 0: EXL3_GEMM(256, 256, 2, 4); break;
+        case 1: EXL3_GEMM(256, 192, 2, 4); break;
+        case 2: EXL3_GEMM(128, 256, 2, 4); break;
+        case 3: EXL3_GEMM(128, 192, 2, 4); break;
+        default: EXL3_GEMM(128, 128, 2, 2);
+    }
 #undef EXL3_GEMM_T
 #undef EXL3_GEMM
     return hipGetLastError();
