@@ -108,21 +108,46 @@ rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had,
 }
 
 // Eight columns of a row of y, row .. row + 7 of W, from their left transform:
-// the factors, the adapter's product v b^T, one rounding.
+// the factors, the adapter's product v b^T, one rounding.  AHEAD: 16 ranks' loads
+// at once, where there are registers.
+template <bool AHEAD>
 __device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *su,
-                                           const AdapterArgs &ad, const uint16_t *v, int64_t tok,
-                                           int row, int rows, bool bf16, uint16_t *y) {
+                                           const AdapterArgs &ad, const uint16_t *v, int id,
+                                           int64_t tok, int row, int rows, bool bf16,
+                                           uint16_t *y) {
     const f32x4 s0 = *reinterpret_cast<const f32x4u *>(su);
     const f32x4 s1 = *reinterpret_cast<const f32x4u *>(su + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= f * (i < 4 ? s0[i] : s1[i - 4]);
     if (v) {
-        const int id = ad.ids[tok];
         if (id >= 0 && id < ad.count) {
             const uint16_t *b = static_cast<const uint16_t *>(ad.b) +
                                 ((size_t)id * rows + row) * ad.rank;
             const uint16_t *vt = v + tok * ad.rank_pad;
-            for (int k = 0; k < ad.rank; k += 8) {
+            int k = 0;
+            for (; AHEAD && k + 16 <= ad.rank; k += 16) {
+                u32x4 vk[2], bk[8][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    vk[h] = *reinterpret_cast<const u32x4 *>(vt + k + 8 * h);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        bk[i][h] = *reinterpret_cast<const u32x4u *>(b + (size_t)i * ad.rank + k +
+                                                                     8 * h);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float vf =
+                            act_load(bf16, (uint16_t)(vk[h][c >> 1] >> (16 * (c & 1))));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            z[i] += vf * act_load(bf16, (uint16_t)(bk[i][h][c >> 1] >>
+                                                                   (16 * (c & 1))));
+                    }
+            }
+            for (; k < ad.rank; k += 8) {
                 const u32x4 vk = *reinterpret_cast<const u32x4 *>(vt + k);
                 float vf[8];
 #pragma unroll
@@ -361,6 +386,7 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
         const int64_t tok = tok0 + g;
         float z[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         const bool has = in && tok < hi;
+        const int id = has && a.v ? ad.ids[tok] : -1;
         if (has)
             for (int s = 0; s < a.split; ++s) {
                 const float *p = a.part + ((size_t)s * n + tok) * rows + row;
@@ -369,8 +395,9 @@ coded_rows_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int 
                     z[i] += __hip_atomic_load(p + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
         hadamard8(z, had);
-        if (has) finish_row(z, f, su + (size_t)e * rows + row, ad, a.v, tok, row, rows, a.bf16,
-                            y + tok * a.ldy + row);
+        if (has)
+            finish_row<false>(z, f, su + (size_t)e * rows + row, ad, a.v, id, tok, row, rows,
+                              a.bf16, y + tok * a.ldy + row);
     }
 }
 
@@ -647,12 +674,13 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
                 z[3][i] = whole ? b - d : d;
             }
             const float ft = f * xs[tok];
+            const int id = out.v ? out.ad.ids[tok] : -1;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const int row = 32 * w + 8 * p;
                 if (rb * 128 + row < rows)
-                    finish_row(z[w], ft, su + row, out.ad, out.v, tok, rb * 128 + row, rows,
-                               out.bf16, out.y + tok * out.ldy + rb * 128 + row);
+                    finish_row<false>(z[w], ft, su + row, out.ad, out.v, id, tok, rb * 128 + row,
+                                      rows, out.bf16, out.y + tok * out.ldy + rb * 128 + row);
             }
         }
         return;
@@ -675,19 +703,22 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
 }
 
 // ---- y ----
-// A wave per row of y and 512 of its columns, eight a lane.  Latency bounds it:
-// 4 us from the first load to the last store at 24 x 4096, 7 at 333 x 4096.
-__global__ void __launch_bounds__(256)
+// A wave per row of y and 512 of its columns, eight a lane, in a workgroup of its
+// own: the waves of the smaller calls then spread over the compute units (32 x
+// 4096 with adapters: 9.4 us with four waves a workgroup, 7.5 with one, 6 with 16
+// ranks' loads at once).  Latency
+// bounds it: 4 us from the first load to the last store at 24 x 4096, 6.5 at
+// 333 x 4096.
+__global__ void __launch_bounds__(64)
 finish_kernel(const float *__restrict__ part, int split, int64_t n, int rows, int had,
               const float *__restrict__ scale, const float *__restrict__ su,
               const int32_t *__restrict__ offsets, int groups, AdapterArgs ad,
               const uint16_t *__restrict__ v, bool bf16, uint16_t *__restrict__ y, int64_t ldy) {
     const int lane = threadIdx.x & 63, blocks = (rows + 511) / 512;
-    const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t tok = wave / blocks;
-    if (tok >= n) return;
-    const int row = (int)(wave - tok * blocks) * 512 + lane * 8;
+    const int64_t tok = blockIdx.x / blocks;
+    const int row = (int)(blockIdx.x - tok * blocks) * 512 + lane * 8;
     const bool in = row < rows;
+    const int id = v ? ad.ids[tok] : -1;
     int e = 0;
     if (offsets) {
         e = group_of_row(offsets, groups, tok);
@@ -719,8 +750,9 @@ finish_kernel(const float *__restrict__ part, int split, int64_t n, int rows, in
         }
     }
     hadamard8(z, had);
-    if (in) finish_row(z, scale[e] / (float)had, su + (size_t)e * rows + row, ad, v, tok, row,
-                       rows, bf16, y + tok * ldy + row);
+    if (in)
+        finish_row<true>(z, scale[e] / (float)had, su + (size_t)e * rows + row, ad, v, id, tok, row,
+                         rows, bf16, y + tok * ldy + row);
 }
 
 template <int LV, int K>
@@ -843,9 +875,9 @@ hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const
 hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const float *part, int split,
                          int64_t n, bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
                          int64_t ldy, hipStream_t stream) {
-    const unsigned grid = (unsigned)((n * ((w.rows + 511) / 512) + 3) / 4);
+    const unsigned grid = (unsigned)(n * ((w.rows + 511) / 512));
     const AdapterArgs args = ad ? *ad : AdapterArgs{};
-    hipLaunchKernelGGL(finish_kernel, dim3(grid), dim3(256), 0, stream, part, split, n, w.rows,
+    hipLaunchKernelGGL(finish_kernel, dim3(grid), dim3(64), 0, stream, part, split, n, w.rows,
                        w.had, w.scale, w.su, offsets, w.groups, args, v, bf16,
                        static_cast<uint16_t *>(y), ldy);
     return hipGetLastError();
