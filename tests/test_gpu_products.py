@@ -285,6 +285,16 @@ def test_the_other_direction_in_tiles_meets_the_dense_form(T, ctx_of, n, per, K,
             check(y[cut[e]:cut[e + 1]], xe @ m.T, spread_of(xe, m), inner_of(False, FP), "%d" % e)
 
 
+@pytest.mark.parametrize("n", [600, 1536, 1537])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_long_contractions_of_many_rows(T, ctx, n, transpose):
+    w = random_weight(2624, 192, 2, 64, n) if transpose else random_weight(192, 2624, 2, 64, n)
+    m = dense(w).T if transpose else dense(w)
+    x, x64 = rows_of(n, 2624, BF, n + 1)
+    y = ctx.linear(x, on_gpu(T, w), transpose=transpose)
+    check(y, x64 @ m.T, spread_of(x64, m), inner_of(False, BF))
+
+
 def test_zero_rows_and_zero_input(T, ctx):
     w = random_weight(128, 256, 2, 128, 151)
     g = on_gpu(T, w)

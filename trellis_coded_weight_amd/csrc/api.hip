@@ -861,15 +861,25 @@ bool rows_aligned(const void *p, int64_t ld) {
 // and dense, us: 4 rows 17 and 58, 200 rows 35 and 56, 400 rows 44 and 55;
 // 4096 x 12288, K = 3: 100 rows 40 and 69, 300 rows 101 and 86; 16 of
 // 1408 x 2048, K = 2: 100 rows each 46 and 52, 400 rows 93 and 85.
+//
+// Tiles also serve more rows where the matrix product's tiles would fill less than
+// half of the compute units for a long contraction, which the tiles' kernel
+// splits, us: 1,350 rows, 512 columns from 7,296: 44 against 80; 900 rows, 1,024
+// from 4,096: 33 against 48; 789 rows, 832 from 2,880: 30 against 38.  Not past
+// some 1,500 rows, whose x' and sums cost more (4,000 rows, 512 from 8,192: 85
+// against 75), nor for short contractions (800 rows, 1,024 from 1,024: 23 against
+// 17).
 enum Form { kFewRows, kTiles, kDense };
 
-Form form_of(const exl3::WeightArgs &w, bool transpose, int64_t n) {
+Form form_of(const exl3::WeightArgs &w, bool transpose, int64_t n, int n_cu) {
     const bool tiles = w.lv_kind != exl3::kLevelsTable &&
                        reinterpret_cast<uintptr_t>(w.packed) % 16 == 0;
-    if (transpose) return tiles && n <= (int64_t)256 * w.groups ? kTiles : kDense;
-    if (n <= (int64_t)16 * w.groups) return kFewRows;
-    if (tiles && n <= (int64_t)512 * w.groups) return kTiles;
-    return n <= (int64_t)64 * w.groups ? kFewRows : kDense;
+    const int m = transpose ? w.cols : w.rows, k = transpose ? w.rows : w.cols;
+    const int64_t products = ((n + 127) / 128 + w.groups - 1) * ((m + 127) / 128);
+    const int64_t most = k >= 2560 && products <= n_cu / 2 ? 1536 : transpose ? 256 : 512;
+    if (!transpose && n <= (int64_t)16 * w.groups) return kFewRows;
+    if (tiles && n <= most * w.groups) return kTiles;
+    return !transpose && n <= (int64_t)64 * w.groups ? kFewRows : kDense;
 }
 
 // y = x W^T or x W, with v b^T of the adapters when ad is given (ad_b: their
@@ -907,7 +917,7 @@ exl3::WeightArgs directed(const Product &p) {
 int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
     const exl3::WeightArgs w = directed(p);
     const size_t n = (size_t)p.n;
-    p.form = form_of(*p.w, p.transpose, p.n);
+    p.form = form_of(*p.w, p.transpose, p.n, ctx->n_cu);
     if (p.form != kDense) {
         if (p.form == kFewRows) {
             // a wave has 256 columns; a workgroup up to four tiles of rows, as many as
