@@ -424,10 +424,11 @@ typedef struct {
  *   y      [n][out] of the same type, rows ldy elements apart; out = the other
  *          side.  x and y share no element.
  * Products are summed in binary32 and rounded once to the type of y.  Up to 512
- * rows (not transposed) are multiplied by the levels themselves, with the
- * transformed activations in binary16 under a power-of-two scale of each row
- * (each 256 columns of it); more rows, and the other direction, by W rounded to
- * the type of x.  A row of x with a NaN or an infinity gives a row of y without
+ * rows a group (256 transposed, 1,536 where a long contraction has few results)
+ * are multiplied by the levels themselves, with the transformed activations in
+ * binary16 under a power-of-two scale of each row (each 256 columns of it); more
+ * rows, and transposed products by the general decoder, by W rounded to the type
+ * of x.  A row of x with a NaN or an infinity gives a row of y without
  * finite values; other rows are not affected.  Results do not depend on
  * scheduling.  n may be 0; at most 2^24 rows.
  * Asynchronous.  The context's workspace grows on demand: to capture the call

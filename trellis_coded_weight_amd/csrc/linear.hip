@@ -1,4 +1,6 @@
-// Products of few rows with coded weights, y = x W^T, on gfx950.
+// Products of few and of medium numbers of rows with coded weights, y = x W^T,
+// and of the latter y = x W with both sides' transforms and factors exchanged, on
+// gfx950.
 //
 // W = diag(su) H_l (scale C) H_r diag(sv) with C the codes' levels, so
 //   y = scale / had * su (H_l (C x')),   x' = H_r (sv x)
