@@ -114,6 +114,8 @@ struct exl3_ctx {
     bool has_order = false;
     // the procedural codebook the level table holds, or -1 for a caller's table
     int cb_kind = EXL3_CB_MUL1;
+    // a power of two that takes the largest level of a caller's table into [2, 4)
+    float cb_norm = 1.0f;
     // workspace of the products with coded weights; outgrown ones are kept, as
     // a captured graph may hold their addresses
     char *d_work = nullptr;
@@ -783,7 +785,7 @@ int check_weight(exl3_ctx *ctx, const exl3_weight *w, exl3::WeightArgs *out) {
     out->cols = w->cols;
     out->K = w->K;
     out->had = w->had_block;
-    out->lv = exl3::Levels{0, 0, ctx->d_levels, tile_order_inv(ctx), w->K};
+    out->lv = exl3::Levels{0, 0, ctx->d_levels, tile_order_inv(ctx), w->K, ctx->cb_norm};
     out->lv_kind = exl3::kLevelsTable;
     if (!ctx->has_order && w->K <= 4) {
         if (ctx->cb_kind == EXL3_CB_MUL1) out->lv_kind = exl3::kLevelsMul1;
@@ -1171,11 +1173,13 @@ int exl3_set_codebook(exl3_ctx *ctx, const uint16_t *levels_fp16_host) {
         return rc;
     if ((rc = set_device(ctx)) != EXL3_OK) return rc;
     std::vector<uint16_t> lv(65536);
+    uint32_t largest = 0;
     if (levels_fp16_host) {
         for (int i = 0; i < 65536; ++i) {
             if ((levels_fp16_host[i] & 0x7C00u) == 0x7C00u)
                 return fail(ctx, EXL3_EINVAL, "level %d is NaN or Inf", i);
             lv[(size_t)i] = levels_fp16_host[i];
+            largest = std::max<uint32_t>(largest, levels_fp16_host[i] & 0x7FFFu);
         }
     } else {
         exl3::build_mul1_levels(lv.data());
@@ -1184,6 +1188,13 @@ int exl3_set_codebook(exl3_ctx *ctx, const uint16_t *levels_fp16_host) {
                                  hipMemcpyHostToDevice, ctx->stream));
     EXL3_HIP(ctx, hipStreamSynchronize(ctx->stream));
     ctx->cb_kind = levels_fp16_host ? -1 : (int)EXL3_CB_MUL1;
+    // binary16 magnitudes: exponent field 16 is [2, 4); below field 1 the leading bit counts
+    ctx->cb_norm = 1.0f;
+    if (largest) {
+        const int field = (int)(largest >> 10);
+        const int e = field ? field - 15 : std::ilogb((double)largest) - 24;
+        ctx->cb_norm = std::ldexp(1.0f, 1 - e);
+    }
     return EXL3_OK;
 }
 
@@ -1202,6 +1213,7 @@ int exl3_set_codebook_kind(exl3_ctx *ctx, int kind) {
                                  hipMemcpyHostToDevice, ctx->stream));
     EXL3_HIP(ctx, hipStreamSynchronize(ctx->stream));
     ctx->cb_kind = kind;
+    ctx->cb_norm = 1.0f;
     return EXL3_OK;
 }
 

@@ -61,6 +61,8 @@ struct Levels {
     const uint16_t *table;   // kLevelsTable: 65,536 binary16 values
     const uint8_t *inv;      // element -> position within a tile, or null (kLevelsTable only)
     int K;                   // bits a weight (kLevelsTable only; otherwise a template argument)
+    float norm;              // a power of two that takes the table's largest level below 4, the
+                             // procedural codebooks' range (kLevelsTable only)
 };
 
 // The levels of two states as two binary16 values.

@@ -22,7 +22,9 @@ __device__ __forceinline__ uint32_t parity16(uint32_t v) { return __popc(v) & 1u
 //      column as binary16: for bfloat16 weights rounded to it (2^-12 of each,
 //      an eighth of what the final rounding takes), for binary16 weights in two
 //      parts, the rounded value and the rest, so that the weights are rounded
-//      once.
+//      once.  The codebooks' levels are below 4 and their sums below 2^9; a
+//      caller's table may hold any binary16 value, and its sums take the power of
+//      two that brings its largest level there (Levels::norm, exact both ways).
 //   3. The wave transforms 16 columns over the rows.  Of a row's index in H_HB
 //      the lowest five bits meet the matrix instruction's 32 k's; the sums over
 //      the remaining index are butterflies of the results.
@@ -87,7 +89,8 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
     u32x4 h32[2];
     h32[0] = (g & 1) ? low[1] : low[0];
     h32[1] = h32[0] ^ ((g >> 1) ? 0x80008000u : 0u);
-    const float f = scale[e] / (float)HB;
+    const float norm = LV == kLevelsTable ? lv.norm : 1.0f;
+    const float f = scale[e] / ((float)HB * norm);
     const float *su_b = su + (size_t)e * rows + (size_t)br * HB;
     float su_t[TR ? 1 : NT];
     if (!TR)
@@ -116,6 +119,7 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
     // column 16 t + r, rows 16 wv + 4 g .. + 3
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+        if (LV == kLevelsTable) sum[t] *= norm;
         f16x2 a, b;
         a[0] = (_Float16)sum[t][0];
         a[1] = (_Float16)sum[t][1];
