@@ -402,7 +402,8 @@ int exl3_quantize_matrix_ldlq(exl3_ctx *ctx, const void *w, int w_dtype, int row
  *   packed  uint16 [groups][rows/16][cols/16][16*K], 4-byte aligned
  *   scale   float [groups]
  *   su, sv  float [groups][rows], float [groups][cols]: any finite values (the
- *           signs, or folded as by exl3_channel_normalize)
+ *           signs, or folded as by exl3_channel_normalize) whose products with
+ *           the scale, the levels and the activations stay within binary32
  * K in 1..8 (5..8, a table set by exl3_set_codebook and a within-tile order
  * other than the natural one take a slower general decoder); had_block 64 or
  * 128; rows and cols positive multiples of had_block, at most 2^20; groups 1 ..
@@ -428,7 +429,8 @@ typedef struct {
  * are multiplied by the levels themselves, with the transformed activations in
  * binary16 under a power-of-two scale of each row (each 256 columns of it); more
  * rows, and transposed products by the general decoder, by W rounded to the type
- * of x.  A row of x with a NaN or an infinity gives a row of y without
+ * of x (binary16: apart from powers of two, one of each channel of the result and
+ * one of the largest on the other side, so that W is not held to its range).  A row of x with a NaN or an infinity gives a row of y without
  * finite values; other rows are not affected.  Results do not depend on
  * scheduling.  n may be 0; at most 2^24 rows.
  * Asynchronous.  The context's workspace grows on demand: to capture the call

@@ -50,3 +50,59 @@ def test_level_tables_of_any_size(T, kind, dtype, n, transpose):
         c.set_codebook(torch.from_numpy(table))
         y = c.linear(x, on_gpu(T, w), transpose=transpose)
         check(y, x64 @ m.T, spread_of(x64, m), inner_of(False, dtype))
+
+
+# rows of a group up to which the levels are used themselves, and one more
+THRESHOLD = [(512, False), (513, False), (256, True), (257, True)]
+
+
+@pytest.mark.parametrize("n,transpose", THRESHOLD)
+@pytest.mark.parametrize("size,std", [(1e-8, 500.0), (1e-5, 50.0), (1e5, 1e-3)])
+def test_binary16_weights_of_any_size(T, ctx, size, std, n, transpose):
+    w = random_weight(128, 192, 2, 64, 411)
+    w["su"] = (w["su"] * (size / 0.02)).astype(np.float32)
+    m = dense(w)
+    m = m.T if transpose else m
+    x, x64 = rows_of(n, m.shape[1], FP, 412, std)
+    y = ctx.linear(x, on_gpu(T, w), transpose=transpose)
+    check(y, x64 @ m.T, spread_of(x64, m), inner_of(False, FP))
+
+
+@pytest.mark.parametrize("n,transpose", THRESHOLD)
+def test_binary16_channels_of_many_sizes(T, ctx, n, transpose):
+    """Channels over 28 powers of two, and input channels over six.  Of a transposed product the
+    input has large values where its channels are small."""
+    r = np.random.Generator(np.random.PCG64(421))
+    w = random_weight(128, 192, 3, 64, 422, dead=False)
+    power = r.uniform(-20, -6, 128) if transpose else r.uniform(-26, 2, 128)
+    w["su"] = (np.sign(w["su"]) * 2.0 ** power).astype(np.float32)
+    w["sv"] = (w["sv"] * 2.0 ** r.uniform(-3, 3, 192)).astype(np.float32)
+    m, inner = (dense(w).T, w["su"]) if transpose else (dense(w), w["sv"])
+    inner = inner.astype(np.float64)
+    z = r.standard_normal((n, m.shape[1])) * (2.0 ** (-8 - power) if transpose else 64.0)
+    x = torch.from_numpy(z).to(FP)
+    x64 = x.double().numpy()
+    y = ctx.linear(x.to(DEV), on_gpu(T, w), transpose=transpose)
+    # the transforms spread what the factors leave
+    check(y, x64 @ m.T, spread_of(x64 * inner, m / inner), inner_of(False, FP))
+
+
+@pytest.mark.parametrize("per,transpose", [(513, False), (257, True)])
+def test_binary16_groups_of_different_sizes(T, per, transpose):
+    """Groups whose weights lie 40 powers of two apart, in batches of two of the dense form."""
+    sizes = [1e-7, 1e5, 1.0, 1e-4, 1e2]
+    w = random_weight(128, 192, 2, 64, 431, groups=5)
+    w["su"] = (w["su"] * (np.array(sizes)[:, None] / 0.02)).astype(np.float32)
+    n = 5 * per
+    std = np.repeat([300.0, 1e-3, 1.0, 30.0, 0.1], per)[:, None]
+    r = np.random.Generator(np.random.PCG64(432))
+    x = torch.from_numpy(r.standard_normal((n, 128 if transpose else 192)) * std).to(FP)
+    x64 = x.double().numpy()
+    cut = torch.arange(6, dtype=torch.int32, device=DEV) * per
+    with T.Context(0, scratch_bytes=2 * 128 * 192 * 2) as c:
+        y = c.grouped_linear(x.to(DEV), on_gpu(T, w), cut, transpose=transpose)
+        for e in range(5):
+            m = dense(w, group=e)
+            m = m.T if transpose else m
+            at = slice(e * per, e * per + per)
+            check(y[at], x64[at] @ m.T, spread_of(x64[at], m), inner_of(False, FP), "group %d" % e)

@@ -902,7 +902,7 @@ struct Product {
     // set by plan_product
     Form form;
     int split, run, per, batch;
-    size_t xh_at, xs_at, part_at, dense_at, xpack_at;
+    size_t xh_at, xs_at, part_at, dense_at, xpack_at, inner_at;
     bool pack, own_x, finish;
 };
 
@@ -960,6 +960,7 @@ int plan_product(exl3_ctx *ctx, Product &p, Carve &c) {
     p.dense_at = c.take(one * p.batch);
     p.pack = !rows_aligned(p.x, p.ldx);
     p.xpack_at = p.pack ? c.take(n * w.cols * 2) : 0;
+    p.inner_at = p.bf16 ? 0 : c.take((size_t)w.groups * sizeof(int32_t));
     return EXL3_OK;
 }
 
@@ -1005,12 +1006,16 @@ int run_product(exl3_ctx *ctx, const Product &p) {
         x = xp;
         ldx = k;
     }
+    int32_t *inner = reinterpret_cast<int32_t *>(ws + p.inner_at);
+    if (!p.bf16) EXL3_HIP(ctx, exl3::launch_inner(*p.w, p.transpose, inner, ctx->stream));
+    const exl3::DenseScale ds{w.scale, w.su, inner,
+                              (float)w.had * (w.lv_kind == exl3::kLevelsTable ? w.lv.norm : 1.0f)};
     for (int g0 = 0; g0 < w.groups; g0 += p.batch) {
         const int ng = std::min(p.batch, w.groups - g0);
-        EXL3_HIP(ctx, exl3::launch_dense(*p.w, p.offsets, p.n, g0, ng, p.transpose, p.bf16, dense,
-                                         p.y, p.ldy, ctx->stream));
-        EXL3_HIP(ctx, exl3::launch_gemm(x, ldx, dense, p.n, m, k, p.offsets, g0, ng, p.bf16, p.ad,
-                                        p.ad_b, v, p.y, p.ldy, ctx->n_cu, ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_dense(*p.w, p.offsets, p.n, g0, ng, p.transpose, p.bf16, inner,
+                                         dense, p.y, p.ldy, ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_gemm(x, ldx, dense, ds, p.n, m, k, p.offsets, g0, ng, p.bf16,
+                                        p.ad, p.ad_b, v, p.y, p.ldy, ctx->n_cu, ctx->stream));
     }
     return EXL3_OK;
 }

@@ -445,15 +445,28 @@ hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const floa
 
 // The dense weights in the activations' type: [groups][rows][cols], or
 // [groups][cols][rows] when transposed; groups g0 .. g0 + ng - 1.  With offsets
-// and g0 = 0 also sets the rows of y that no group holds to zero.
+// and g0 = 0 also sets the rows of y that no group holds to zero.  Binary16
+// weights are divided by powers of two (DenseScale) from inner, launch_inner's.
 hipError_t launch_dense(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
-                        bool transposed, bool bf16, uint16_t *dense, void *y, int64_t ldy,
-                        hipStream_t stream);
+                        bool transposed, bool bf16, const int32_t *inner, uint16_t *dense, void *y,
+                        int64_t ldy, hipStream_t stream);
+
+// inner[groups]: the exponent of the largest of each group's factors on the side
+// that is contracted (sv, or su when transposed).
+hipError_t launch_inner(const WeightArgs &w, bool transposed, int32_t *inner, hipStream_t stream);
+
+// What binary16 dense weights were divided by, row by row: 2 to the sum of the
+// exponents of scale[g] / div, of out[g][row] and of inner[g] + 1.
+struct DenseScale {
+    const float *scale, *out;
+    const int32_t *inner;
+    float div;
+};
 
 // y[n][m] = x[n][k] dense[g][m][k]^T for the rows of groups g0 .. g0 + ng - 1,
-// plus the adapters' products v b^T (b: [count][m][rank]).
-hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_t n, int m, int k,
-                       const int32_t *offsets, int g0, int ng, bool bf16,
+// plus the adapters' products v b^T (b: [count][m][rank]).  ds: read for binary16.
+hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, const DenseScale &ds,
+                       int64_t n, int m, int k, const int32_t *offsets, int g0, int ng, bool bf16,
                        const AdapterArgs *ad, const void *b, const uint16_t *v, void *y,
                        int64_t ldy, int n_cu, hipStream_t stream);
 

@@ -29,7 +29,12 @@ __device__ __forceinline__ uint32_t parity16(uint32_t v) { return __popc(v) & 1u
 //      the lowest five bits meet the matrix instruction's 32 k's; the sums over
 //      the remaining index are butterflies of the results.
 // Then the scale, su and sv in binary32 and one rounding to the activations'
-// type.  Row-major and transposed output differ in the order of step 3's
+// type.  Binary16 has too few exponents for any su and sv: its weights are stored
+// without the powers of two of their scale and of their result's channel, and
+// divided by that of the largest factor on the contracted side, below 2^15 and,
+// where the levels are spread evenly, some 2^4; the product's results get them back
+// (gemm_kernel).  What is below 2^-18 of a channel's spread alone is rounded to
+// fewer bits.  Row-major and transposed output differ in the order of step 3's
 // operands: either way a lane holds four consecutive elements of the output.
 // 4096 x 4096, K = 2: 13.3 to 15 us, 2.5 TB/s written; the chain of decoding,
 // products and two passes through shared memory in each workgroup bounds it more
@@ -39,8 +44,8 @@ __global__ void __launch_bounds__(HB * 4, 4)
 dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols, int Kr,
              const float *__restrict__ scale, const float *__restrict__ su,
              const float *__restrict__ sv, const int32_t *__restrict__ offsets, int64_t n, int g0,
-             uint16_t *__restrict__ dense, uint16_t *__restrict__ y, int64_t ldy,
-             int groups) {
+             const int32_t *__restrict__ inner, uint16_t *__restrict__ dense,
+             uint16_t *__restrict__ y, int64_t ldy, int groups) {
     constexpr int kPitch = HB * 2 + 16;          // bytes a column of the block takes in LDS
     constexpr int kParts = BF ? 1 : 2, NT = HB / 16, NP = HB / 32;
     __shared__ __align__(16) char mid[kParts][HB * kPitch];
@@ -90,12 +95,20 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
     h32[0] = (g & 1) ? low[1] : low[0];
     h32[1] = h32[0] ^ ((g >> 1) ? 0x80008000u : 0u);
     const float norm = LV == kLevelsTable ? lv.norm : 1.0f;
-    const float f = scale[e] / ((float)HB * norm);
+    float f = scale[e] / ((float)HB * norm);
+    int down = 0;                                // powers of two taken off the contracted side
+    if (!BF) {
+        f = __builtin_amdgcn_frexp_mantf(f);
+        down = -(inner[e] + 1);
+    }
+    // the factors of the result's side, and of the contracted one
+    auto outer_factor = [&](float s) { return f * (BF ? s : __builtin_amdgcn_frexp_mantf(s)); };
+    auto inner_factor = [&](float s) { return BF ? s : __builtin_ldexpf(s, down); };
     const float *su_b = su + (size_t)e * rows + (size_t)br * HB;
     float su_t[TR ? 1 : NT];
     if (!TR)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) su_t[t] = f * su_b[16 * t + r];
+        for (int t = 0; t < NT; ++t) su_t[t] = outer_factor(su_b[16 * t + r]);
     uint16_t *out = dense + (size_t)blockIdx.y * rows * cols;
 
     f32x4 sum[NT];
@@ -171,7 +184,7 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
     float sv_r = 0.0f;
     f32x4 sv_4 = {0.0f, 0.0f, 0.0f, 0.0f};
     if (TR)
-        sv_r = f * sv_b[r];
+        sv_r = outer_factor(sv_b[r]);
     else
         sv_4 = *reinterpret_cast<const f32x4u *>(sv_b + 4 * g);
     __syncthreads();                         // the halves have been read
@@ -181,10 +194,10 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
         if (TR) {
             const f32x4 s4 = *reinterpret_cast<const f32x4u *>(su_b + 16 * t + 4 * g);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] *= sv_r * s4[i];
+            for (int i = 0; i < 4; ++i) v[i] *= sv_r * inner_factor(s4[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] *= su_t[t] * sv_4[i];
+            for (int i = 0; i < 4; ++i) v[i] *= su_t[t] * inner_factor(sv_4[i]);
         }
         char *at = TR ? mid[0] + (16 * wv + r) * kPitch + (16 * t + 4 * g) * 2
                       : mid[0] + (16 * t + r) * kPitch + (16 * wv + 4 * g) * 2;
@@ -203,6 +216,31 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
         *reinterpret_cast<u32x4 *>(o0 + row * pitch + c * 8) =
             *reinterpret_cast<const u32x4 *>(mid[0] + row * kPitch + c * 16);
     }
+}
+
+// The exponent of the largest of each group's k factors (a workgroup a group).
+__global__ void __launch_bounds__(512)
+inner_kernel(const float *__restrict__ factors, int k, int32_t *__restrict__ inner) {
+    __shared__ uint32_t wave_big[8];
+    const float *at = factors + (size_t)blockIdx.x * k;
+    uint32_t big = 0;                            // magnitudes compare as integers
+    for (int c = threadIdx.x * 4; c < k; c += 2048) {
+        const f32x4 v = *reinterpret_cast<const f32x4u *>(at + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t m = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
+            big = m > big ? m : big;
+        }
+    }
+    for (int m = 1; m < 64; m <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)big, m);
+        big = o > big ? o : big;
+    }
+    if ((threadIdx.x & 63) == 0) wave_big[threadIdx.x >> 6] = big;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int i = 1; i < 8; ++i) big = wave_big[i] > big ? wave_big[i] : big;
+    inner[blockIdx.x] = __builtin_amdgcn_frexp_expf(__builtin_bit_cast(float, big));
 }
 
 // ---- matrix product ----
@@ -224,8 +262,8 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
 // the reads it waits for, once a slice.
 template <int BM, int BN, int WM, int WN, bool BF, bool AD>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
-gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w, int64_t n,
-            int m, int k, const int32_t *__restrict__ offsets, int g0, int ng, int m_tiles,
+gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w,
+            DenseScale ds, int64_t n, int m, int k, const int32_t *__restrict__ offsets, int g0, int ng, int m_tiles,
             int total, AdapterArgs ad, const uint16_t *__restrict__ ad_b,
             const uint16_t *__restrict__ v, uint16_t *__restrict__ y, int64_t ldy) {
     constexpr int kThreads = 64 * WM * WN, SM = BM / WM, SN = BN / WN, TM = SM / 16, TN = SN / 16;
@@ -351,6 +389,23 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
     }
     const int m0 = mt * BM + wm * SM;
     const int64_t t0 = row0 + wn * SN;
+    if (!BF) {
+        // the powers of two that the weights were divided by
+        const int eg = g0 + e;
+        const int all = __builtin_amdgcn_frexp_expf(ds.scale[eg] / ds.div) + ds.inner[eg] + 1;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int mr = m0 + 16 * i + 4 * g;  // past the edge: repeats, not stored
+            const f32x4 s = *reinterpret_cast<const f32x4u *>(ds.out + (size_t)eg * m +
+                                                              (mr < m ? mr : m - 4));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int up = all + __builtin_amdgcn_frexp_expf(s[c]);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j][c] = __builtin_ldexpf(acc[i][j][c], up);
+            }
+        }
+    }
     if (AD) {
         // v b^T of each adapter that some row of the wave has, in ascending
         // order; its result is added where the row's adapter is this one, so
@@ -454,13 +509,13 @@ pack_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int k,
 
 template <int LV, int K, int HB>
 hipError_t dense_t(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
-                   bool transposed, bool bf16, uint16_t *dense, uint16_t *y, int64_t ldy,
-                   hipStream_t stream) {
+                   bool transposed, bool bf16, const int32_t *inner, uint16_t *dense,
+                   uint16_t *y, int64_t ldy, hipStream_t stream) {
     const dim3 grid((unsigned)(w.rows / HB * (w.cols / HB)), (unsigned)ng);
 #define EXL3_DENSE(BF, TR)                                                                     \
     hipLaunchKernelGGL((dense_kernel<LV, K, HB, BF, TR>), grid, dim3(HB * 4), 0, stream,       \
                        w.packed, w.lv, w.rows, w.cols, w.K, w.scale, w.su, w.sv, offsets, n, g0, \
-                       dense, y, ldy, w.groups)
+                       inner, dense, y, ldy, w.groups)
     if (bf16 && transposed)
         EXL3_DENSE(true, true);
     else if (bf16)
@@ -475,21 +530,23 @@ hipError_t dense_t(const WeightArgs &w, const int32_t *offsets, int64_t n, int g
 
 template <int LV, int K>
 hipError_t dense_h(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
-                   bool transposed, bool bf16, uint16_t *dense, uint16_t *y, int64_t ldy,
-                   hipStream_t stream) {
-    return w.had == 128
-               ? dense_t<LV, K, 128>(w, offsets, n, g0, ng, transposed, bf16, dense, y, ldy, stream)
-               : dense_t<LV, K, 64>(w, offsets, n, g0, ng, transposed, bf16, dense, y, ldy, stream);
+                   bool transposed, bool bf16, const int32_t *inner, uint16_t *dense,
+                   uint16_t *y, int64_t ldy, hipStream_t stream) {
+    return w.had == 128 ? dense_t<LV, K, 128>(w, offsets, n, g0, ng, transposed, bf16, inner, dense,
+                                              y, ldy, stream)
+                        : dense_t<LV, K, 64>(w, offsets, n, g0, ng, transposed, bf16, inner, dense,
+                                             y, ldy, stream);
 }
 
 }  // namespace
 
 hipError_t launch_dense(const WeightArgs &w, const int32_t *offsets, int64_t n, int g0, int ng,
-                        bool transposed, bool bf16, uint16_t *dense, void *yv, int64_t ldy,
-                        hipStream_t stream) {
+                        bool transposed, bool bf16, const int32_t *inner, uint16_t *dense, void *yv,
+                        int64_t ldy, hipStream_t stream) {
     uint16_t *y = static_cast<uint16_t *>(yv);
 #define EXL3_DENSE_K(LV, KK) \
-    case KK: return dense_h<LV, KK>(w, offsets, n, g0, ng, transposed, bf16, dense, y, ldy, stream)
+    case KK:                     \
+        return dense_h<LV, KK>(w, offsets, n, g0, ng, transposed, bf16, inner, dense, y, ldy, stream)
     if (w.lv_kind == kLevelsMul1)
         switch (w.K) {
             EXL3_DENSE_K(kLevelsMul1, 1);
@@ -505,11 +562,18 @@ hipError_t launch_dense(const WeightArgs &w, const int32_t *offsets, int64_t n, 
             EXL3_DENSE_K(kLevelsHalves, 4);
         }
 #undef EXL3_DENSE_K
-    return dense_h<kLevelsTable, 0>(w, offsets, n, g0, ng, transposed, bf16, dense, y, ldy, stream);
+    return dense_h<kLevelsTable, 0>(w, offsets, n, g0, ng, transposed, bf16, inner, dense, y, ldy,
+                                    stream);
 }
 
-hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_t n, int m, int k,
-                       const int32_t *offsets, int g0, int ng, bool bf16,
+hipError_t launch_inner(const WeightArgs &w, bool transposed, int32_t *inner, hipStream_t stream) {
+    hipLaunchKernelGGL(inner_kernel, dim3((unsigned)w.groups), dim3(512), 0, stream,
+                       transposed ? w.su : w.sv, transposed ? w.rows : w.cols, inner);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, const DenseScale &ds,
+                       int64_t n, int m, int k, const int32_t *offsets, int g0, int ng, bool bf16,
                        const AdapterArgs *ad, const void *b, const uint16_t *v, void *y,
                        int64_t ldy, int n_cu, hipStream_t stream) {
     const AdapterArgs args = ad ? *ad : AdapterArgs{};
@@ -517,8 +581,8 @@ hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, int64_
     uint16_t *yy = static_cast<uint16_t *>(y);
 #define EXL3_GEMM_T(BM, BN, WM, WN, BF, AD)                                                      \
     hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, BF, AD>), dim3((unsigned)total),             \
-                       dim3(64 * WM * WN), 0, stream, xx, ldx, dense, n, m, k, offsets, g0, ng,  \
-                       m_tiles, total, args, bb, v, yy, ldy)
+                       dim3(64 * WM * WN), 0, stream, xx, ldx, dense, ds, n, m, k, offsets, g0,  \
+                       ng, m_tiles, total, args, bb, v, yy, ldy)
 #define EXL3_GEMM(BM, BN, WM, WN)                                                                \
     do {                                                                                         \
         const int m_tiles = (m + BM - 1) / BM;                                                   \
