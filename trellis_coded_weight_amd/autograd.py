@@ -3,6 +3,10 @@
 The coded matrix is frozen: gradients go to the activations and to the adapters' matrices.
 Activations may have any leading dimensions, [..., cols]; the row arguments (ids, offsets)
 count rows in their flattened order.
+
+A weight's levels and within-tile order are its context's: a backward pass needs those of its
+forward pass and raises if the context has others by then (weights of different codebooks take a
+context each).
 """
 from __future__ import annotations
 
@@ -15,10 +19,16 @@ def _rows(x: torch.Tensor) -> torch.Tensor:
     return x.reshape(-1, x.shape[-1])
 
 
+def _same_decoder(context: Context, decoder) -> None:
+    if context._decoder() != decoder:
+        raise RuntimeError("the context's codebook or within-tile order has changed since the "
+                           "forward pass: set it back, or use a context for each codebook")
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, context, weight, offsets):
-        ctx.args = context, weight
+        ctx.args = context, weight, context._decoder()
         ctx.save_for_backward(offsets)
         if offsets is None:
             return context.linear(x, weight)
@@ -27,7 +37,8 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        context, weight = ctx.args
+        context, weight, decoder = ctx.args
+        _same_decoder(context, decoder)
         (offsets,) = ctx.saved_tensors
         if offsets is None:
             dx = context.linear(dy, weight, transpose=True)
@@ -39,14 +50,15 @@ class _Linear(torch.autograd.Function):
 class _AdapterLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, A, B, context, weight, alpha, ids):
-        ctx.args = context, weight
+        ctx.args = context, weight, context._decoder()
         ctx.save_for_backward(x, A, B, alpha, ids)
         return context.adapter_linear(x, weight, Adapters(A, B, alpha), ids)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        context, weight = ctx.args
+        context, weight, decoder = ctx.args
+        _same_decoder(context, decoder)
         x, A, B, alpha, ids = ctx.saved_tensors
         want_x, want_a, want_b = ctx.needs_input_grad[:3]
         dx, dA, dB = context.adapter_linear_backward(

@@ -291,6 +291,8 @@ class Context:
         if rc != EXL3_OK:
             raise Exl3Error(rc, "context creation failed")
         self.handle = h
+        # what the level table and the within-tile order were set to
+        self._levels, self._order = "mul1", None
 
     def close(self):
         if getattr(self, "handle", None):
@@ -341,28 +343,40 @@ class Context:
         """levels_fp16: host tensor of 65536 float16 values (None restores mul1)."""
         self._sync_stream()
         if levels_fp16 is None:
-            return self._check(self.lib.exl3_set_codebook(self.handle, None))
+            self._check(self.lib.exl3_set_codebook(self.handle, None))
+            self._levels = "mul1"
+            return
         lv = levels_fp16.detach().cpu().contiguous().view(torch.int16)
         if lv.numel() != 65536:
             raise ValueError("need 65536 levels")
         self._check(self.lib.exl3_set_codebook(self.handle, ctypes.c_void_p(lv.data_ptr())))
+        self._levels = lv.numpy().tobytes()
 
     def set_codebook_kind(self, name: str):
         """Select a procedural codebook by name: "mul1", "mcg" or "3inst"."""
         self._sync_stream()
         self._check(self.lib.exl3_set_codebook_kind(self.handle, CODEBOOK_KINDS[name]))
+        self._levels = name
 
     def set_tile_order(self, order):
         """Within-tile order of tile-major arrays: position t of a tile holds its
         element order[t] (16 * row + col); None restores the natural order."""
         self._sync_stream()
         if order is None:
-            return self._check(self.lib.exl3_set_tile_order(self.handle, None))
+            self._check(self.lib.exl3_set_tile_order(self.handle, None))
+            self._order = None
+            return
         o = torch.as_tensor(order, dtype=torch.int64).cpu()
         if o.numel() != 256 or int(o.min()) < 0 or int(o.max()) > 255:
             raise ValueError("a within-tile order has 256 entries in 0..255")
         buf = o.to(torch.uint8).contiguous()
         self._check(self.lib.exl3_set_tile_order(self.handle, ctypes.c_void_p(buf.data_ptr())))
+        order = buf.numpy().tobytes()
+        self._order = None if order == bytes(range(256)) else order
+
+    def _decoder(self):
+        """What codes mean to this context now, for comparison with a later time."""
+        return self._levels, self._order
 
     def get_codebook(self) -> torch.Tensor:
         out = torch.empty(65536, dtype=torch.int16)
