@@ -82,3 +82,16 @@ def test_levels_set_again_are_the_same_levels(T):
         y.backward(dy)
         assert x.grad is not None
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("op", ["linear", "grouped", "adapters"])
+@pytest.mark.parametrize("name", ["packed", "scale", "su", "sv"])
+def test_a_weight_changed_in_place_is_refused(T, op, name):
+    """As torch refuses any tensor that a backward pass needs and that has changed since."""
+    w, we, ad, ids, cut, x, dy = _setup(T, op)
+    with T.Context(0) as c:
+        y = _call(T, c, op, x, w, we, ad, ids, cut)
+        getattr(we if op == "grouped" else w, name).neg_()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward(dy)
+        torch.cuda.synchronize()

@@ -19,6 +19,11 @@ def _rows(x: torch.Tensor) -> torch.Tensor:
     return x.reshape(-1, x.shape[-1])
 
 
+def _kept(weight: CodedWeight):
+    """The weight's tensors, saved so that torch sees if they change before the backward pass."""
+    return weight.packed, weight.scale, weight.su, weight.sv
+
+
 def _same_decoder(context: Context, decoder) -> None:
     if context._decoder() != decoder:
         raise RuntimeError("the context's codebook or within-tile order has changed since the "
@@ -29,7 +34,7 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, context, weight, offsets):
         ctx.args = context, weight, context._decoder()
-        ctx.save_for_backward(offsets)
+        ctx.save_for_backward(offsets, *_kept(weight))
         if offsets is None:
             return context.linear(x, weight)
         return context.grouped_linear(x, weight, offsets)
@@ -39,7 +44,7 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, dy):
         context, weight, decoder = ctx.args
         _same_decoder(context, decoder)
-        (offsets,) = ctx.saved_tensors
+        offsets = ctx.saved_tensors[0]
         if offsets is None:
             dx = context.linear(dy, weight, transpose=True)
         else:
@@ -51,7 +56,7 @@ class _AdapterLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, A, B, context, weight, alpha, ids):
         ctx.args = context, weight, context._decoder()
-        ctx.save_for_backward(x, A, B, alpha, ids)
+        ctx.save_for_backward(x, A, B, alpha, ids, *_kept(weight))
         return context.adapter_linear(x, weight, Adapters(A, B, alpha), ids)
 
     @staticmethod
@@ -59,7 +64,7 @@ class _AdapterLinear(torch.autograd.Function):
     def backward(ctx, dy):
         context, weight, decoder = ctx.args
         _same_decoder(context, decoder)
-        x, A, B, alpha, ids = ctx.saved_tensors
+        x, A, B, alpha, ids = ctx.saved_tensors[:5]
         want_x, want_a, want_b = ctx.needs_input_grad[:3]
         dx, dA, dB = context.adapter_linear_backward(
             dy, x, weight, Adapters(A, B, alpha), ids, want_dx=want_x,
