@@ -95,3 +95,16 @@ def test_a_weight_changed_in_place_is_refused(T, op, name):
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.backward(dy)
         torch.cuda.synchronize()
+
+
+def test_alpha_has_no_gradient(T):
+    """Refused, where a silent None would leave it untrained."""
+    w, we, ad, ids, cut, x, dy = _setup(T, "adapters")
+    with T.Context(0) as c:
+        alpha = ad.alpha.clone().requires_grad_()
+        with pytest.raises(ValueError, match="alpha"):
+            T.coded_adapter_linear(c, x, w, ad.A, ad.B, alpha, ids)
+        with torch.no_grad():
+            y = T.coded_adapter_linear(c, x, w, ad.A, ad.B, alpha, ids)
+        assert torch.equal(y, T.coded_adapter_linear(c, x, w, ad.A, ad.B, alpha.detach(), ids))
+        torch.cuda.synchronize()

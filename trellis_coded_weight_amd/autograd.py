@@ -87,6 +87,8 @@ def coded_grouped_linear(context: Context, x: torch.Tensor, weight: CodedWeight,
 def coded_adapter_linear(context: Context, x: torch.Tensor, weight: CodedWeight, A: torch.Tensor,
                          B: torch.Tensor, alpha: torch.Tensor, ids: torch.Tensor) -> torch.Tensor:
     """x [..., cols] -> x W^T + alpha_a (x A_a^T) B_a^T; ids int32, the adapter of each row or
-    -1.  Differentiable in x, A and B."""
+    -1.  Differentiable in x, A and B; alpha has no gradient and may not require one."""
+    if torch.is_grad_enabled() and alpha.requires_grad:
+        raise ValueError("alpha requires a gradient, which is not computed: pass alpha.detach()")
     y = _AdapterLinear.apply(_rows(x), A, B, context, weight, alpha, ids.reshape(-1))
     return y.reshape(x.shape[:-1] + (weight.rows,))
