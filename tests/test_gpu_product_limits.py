@@ -50,3 +50,30 @@ def test_many_adapters(T, ctx):
     rest = torch.ones(count, dtype=torch.bool, device=DEV)
     rest[idt.long()] = False
     assert (dA[rest] == 0).all() and (dB[rest] == 0).all()
+
+
+# ---- workspace ----
+def test_a_gradient_of_the_activations_alone_needs_little_workspace(T):
+    """dx takes the two small products and W, nothing for the matrices' gradients: their sums
+    alone would be 4 parts of 32 adapters, 268 MB for each matrix."""
+    rows = cols = 8192
+    g = torch.zeros(rows // 16, cols // 16, 32, dtype=torch.int16, device=DEV)
+    w = T.CodedWeight(g, 2, 1.0, torch.ones(rows, device=DEV), torch.ones(cols, device=DEV))
+    A = torch.zeros(32, 64, cols, dtype=BF, device=DEV)
+    B = torch.zeros(32, rows, 64, dtype=BF, device=DEV)
+    ad = T.Adapters(A, B, torch.ones(32, device=DEV))
+    n = 512
+    x, dy = torch.zeros(n, cols, dtype=BF, device=DEV), torch.zeros(n, rows, dtype=BF, device=DEV)
+    ids = torch.zeros(n, dtype=torch.int32, device=DEV)
+    with T.Context(0) as c:
+        c.linear(dy[:1], w)                                 # what any call brings along
+        keep = torch.empty(n, cols, dtype=BF, device=DEV)   # dx comes from torch's pool
+        del keep
+        torch.cuda.synchronize()
+        free = torch.cuda.mem_get_info()[0]
+        dx, dA, dB = c.adapter_linear_backward(dy, x, w, ad, ids, want_adapters=False)
+        torch.cuda.synchronize()
+        took = free - torch.cuda.mem_get_info()[0]
+        assert dA is None and dB is None and (dx == 0).all()
+        # W 134 MB, A and B transposed 34 MB each
+        assert took < 260e6, took

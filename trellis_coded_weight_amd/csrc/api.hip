@@ -2025,15 +2025,17 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
     p.ldy = lddx;
     p.ad = &aa;
     Carve c;
-    p.v_at = c.take((size_t)n * aa.rank_pad * 2);
+    // room for what the wanted gradients need only
+    auto take = [&c](bool wanted, size_t bytes) { return wanted ? c.take(bytes) : 0; };
     const size_t pitch = ((size_t)n + 31) / 32 * 32, ranks = (size_t)aa.rank_pad;
-    const size_t v_at = c.take((size_t)n * ranks * 2);
-    const size_t ut_at = c.take(pitch * ranks * 2), vt_at = c.take(pitch * ranks * 2);
-    const size_t bt_at = c.take(m * w->rows * 2), at_at = c.take(m * w->cols * 2);
+    p.v_at = take(needs_u, (size_t)n * ranks * 2);
+    const size_t v_at = take(db, (size_t)n * ranks * 2);
+    const size_t ut_at = take(da, pitch * ranks * 2), vt_at = take(db, pitch * ranks * 2);
+    const size_t bt_at = take(needs_u, m * w->rows * 2), at_at = take(wants_dx, m * w->cols * 2);
     const int splits = exl3::adapter_grad_splits(n, aa.count);
-    const size_t pa_at = c.take(splits * m * w->cols * sizeof(float));
-    const size_t pb_at = c.take(splits * m * w->rows * sizeof(float));
-    const size_t used_at = c.take((size_t)splits * aa.count);
+    const size_t pa_at = take(da, splits * m * w->cols * sizeof(float));
+    const size_t pb_at = take(db, splits * m * w->rows * sizeof(float));
+    const size_t used_at = take(da || db, (size_t)splits * aa.count);
     if (wants_dx && (rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
     char *ws = ctx->d_work;
