@@ -77,3 +77,21 @@ def test_a_gradient_of_the_activations_alone_needs_little_workspace(T):
         assert dA is None and dB is None and (dx == 0).all()
         # W 134 MB, A and B transposed 34 MB each
         assert took < 260e6, took
+
+
+# ---- offsets that no program should pass ----
+def test_offsets_that_claim_rows_over_and_over(T, ctx):
+    """Every other group claims all rows, 2^31 tiles and more between them: rows are unspecified,
+    but nothing is written beside them."""
+    groups, n = 65535, 1 << 22
+    packed = torch.zeros(groups * 4 * 20 * 16 + 4, dtype=torch.int16, device=DEV)
+    w = T.CodedWeight(packed[4:].view(groups, 4, 20, 16), 1, torch.ones(groups, device=DEV),
+                      torch.ones(groups, 64, device=DEV), torch.ones(groups, 320, device=DEV),
+                      had_block=64)
+    at = torch.zeros(groups + 1, dtype=torch.int32, device=DEV)
+    at[1::2] = n
+    x = torch.zeros(n, 64, dtype=BF, device=DEV)
+    flat = torch.full((n * 320 + 2048,), 3.0, dtype=BF, device=DEV)
+    ctx.grouped_linear(x, w, at, transpose=True, out=flat[1024:-1024].view(n, 320))
+    torch.cuda.synchronize()
+    assert (flat[:1024] == 3.0).all() and (flat[-1024:] == 3.0).all()

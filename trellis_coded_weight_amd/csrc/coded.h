@@ -343,14 +343,17 @@ __device__ __forceinline__ int tiles_of_group(const int32_t *offsets, int e, boo
     return b > a ? (int)((b - a + per - 1) / per) : 0;
 }
 
+// At most `most`, the grid's: offsets that claim rows over and over could count more
+// than an integer holds (each of 65,535 groups up to 2^24 / per).
 __device__ __forceinline__ int count_tiles(const int32_t *offsets, int g0, int ng, int64_t n,
-                                           int per) {
+                                           int per, int most) {
     const int lane = threadIdx.x & 63;
-    int sum = 0;
+    int64_t sum = 0;
     for (int j = lane; j < ng + lane; j += 64) sum += tiles_of_group(offsets, g0 + j, j < ng, n, per);
+    int some = sum < most ? (int)sum : most;     // 64 of them: most is below 2^25
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
-    return sum;
+    for (int s = 1; s < 64; s <<= 1) some += __shfl_xor(some, s);
+    return some < most ? some : most;
 }
 
 // The group that holds tile nt, which becomes the tile's number within it.

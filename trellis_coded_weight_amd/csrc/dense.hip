@@ -277,8 +277,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
     const int r = lane & 15, g = lane >> 4, wm = wv % WM, wn = wv / WM;
     // each die takes a run of tiles
     if (offsets) {
-        const int tiles = count_tiles(offsets, g0, ng, n, BN) * m_tiles;
-        total = tiles < total ? tiles : total;
+        total = count_tiles(offsets, g0, ng, n, BN, total / m_tiles) * m_tiles;
         if ((int)blockIdx.x >= total) return;    // fewer tiles than the grid allows for
     }
     int id = tile_of_die(blockIdx.x, total);

@@ -460,8 +460,8 @@ coded_tiles_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int
     // each die takes a run of tiles: row blocks of W one after the other for the
     // same rows of x'
     if (offsets) {
-        const int tiles = count_tiles(offsets, 0, groups, n, kRows) * row_blocks * split;
-        total = tiles < total ? tiles : total;
+        const int each = row_blocks * split;
+        total = count_tiles(offsets, 0, groups, n, kRows, total / each) * each;
         if ((int)blockIdx.x >= total) return;    // fewer tiles than the grid allows for
     }
     const int id = tile_of_die(blockIdx.x, total), rb = id % row_blocks;
