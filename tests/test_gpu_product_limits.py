@@ -95,3 +95,21 @@ def test_offsets_that_claim_rows_over_and_over(T, ctx):
     ctx.grouped_linear(x, w, at, transpose=True, out=flat[1024:-1024].view(n, 320))
     torch.cuda.synchronize()
     assert (flat[:1024] == 3.0).all() and (flat[-1024:] == 3.0).all()
+
+
+# ---- the most rows ----
+def test_the_most_rows(T, ctx):
+    """2^24 rows: the kernels with a workgroup a row have more lanes than one launch takes."""
+    groups, n = 32768, 1 << 24
+    w = random_weight(64, 64, 1, 64, 661, groups=4)
+    big = {k: (np.concatenate([v] * (groups // 4)) if isinstance(v, np.ndarray) else v)
+           for k, v in w.items()}
+    g = on_gpu(T, big)
+    x, x64 = rows_of(2048, 64, BF, 662)
+    at = torch.arange(groups + 1, dtype=torch.int32, device=DEV) * (n // groups)
+    y = ctx.grouped_linear(x.repeat(n // 2048, 1), g, at)
+    first = y[:2048]
+    for e in range(4):
+        m, xe = dense(w, group=e), x64[512 * e:512 * e + 512]
+        check(first[512 * e:512 * e + 512], xe @ m.T, spread_of(xe, m), inner_of(True, BF))
+    assert (y.view(n // 2048, 2048, 64) == first).all()

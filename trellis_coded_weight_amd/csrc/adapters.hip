@@ -272,11 +272,11 @@ adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t
 // parts of the above.
 template <bool BF>
 __global__ void __launch_bounds__(256)
-adapter_sum_kernel(GradArgs g0, GradArgs g1, int splits, int count, int rank,
+adapter_sum_kernel(GradArgs g0, GradArgs g1, int splits, int count, int rank, size_t first,
                    const uint8_t *__restrict__ used) {
     const GradArgs p = blockIdx.y ? g1 : g0;
     const size_t all = (size_t)count * rank * p.k;
-    const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const size_t i = first + ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= all) return;
     const int id = (int)(i / ((size_t)rank * p.k));
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -374,14 +374,20 @@ hipError_t launch_adapter_grad(const AdapterArgs &ad, const GradArgs *p, int pro
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     const int k = q[0].k > q[1].k ? q[0].k : q[1].k;
-    const unsigned groups = (unsigned)(((size_t)ad.count * ad.rank * k / 4 + 255) / 256);
-    if (bf16)
-        hipLaunchKernelGGL((adapter_sum_kernel<true>), dim3(groups, (unsigned)products), dim3(256),
-                           0, stream, q[0], q[1], splits, ad.count, ad.rank, used);
-    else
-        hipLaunchKernelGGL((adapter_sum_kernel<false>), dim3(groups, (unsigned)products),
-                           dim3(256), 0, stream, q[0], q[1], splits, ad.count, ad.rank, used);
-    return hipGetLastError();
+    const int64_t all = ((int64_t)ad.count * ad.rank * k / 4 + 255) / 256, each = rows_a_launch(256);
+    for (int64_t g = 0; g < all; g += each) {
+        const dim3 blocks_here((unsigned)(all - g < each ? all - g : each), (unsigned)products);
+        const size_t first = (size_t)g * 1024;
+        if (bf16)
+            hipLaunchKernelGGL((adapter_sum_kernel<true>), blocks_here, dim3(256), 0, stream, q[0],
+                               q[1], splits, ad.count, ad.rank, first, used);
+        else
+            hipLaunchKernelGGL((adapter_sum_kernel<false>), blocks_here, dim3(256), 0, stream,
+                               q[0], q[1], splits, ad.count, ad.rank, first, used);
+        err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace exl3

@@ -404,6 +404,13 @@ struct AdapterArgs {
     int count, rank, rank_pad;
 };
 
+// A launch takes fewer than 2^32 lanes along a grid's side: rows (or pieces) a
+// launch, for kernels of `lanes` lanes each.
+inline int64_t rows_a_launch(int64_t lanes) {
+    const int64_t most = (((int64_t)1 << 31) / lanes);
+    return most < 1 ? 1 : most;
+}
+
 // x' = H_r (sv x) as binary16 [n][cols] with a scale [n] (a power of two).
 hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void *x, int64_t ldx,
                          int64_t n, bool bf16, uint16_t *xh, float *xs, hipStream_t stream);

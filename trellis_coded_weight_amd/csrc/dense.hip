@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(256)
 pack_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int k,
                  uint16_t *__restrict__ out) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n * (k / 8)) return;
+    if (i >= n * (k / 8)) return;                // the rows of one launch
     const int64_t row = i / (k / 8);
     const int c = (int)(i - row * (k / 8)) * 8;
     *reinterpret_cast<u32x4 *>(out + row * k + c) =
@@ -626,10 +626,16 @@ hipError_t launch_gemm(const void *x, int64_t ldx, const uint16_t *dense, const 
 
 hipError_t launch_pack_rows(const void *x, int64_t ldx, int64_t n, int k, uint16_t *out,
                             hipStream_t stream) {
-    const unsigned grid = (unsigned)((n * (k / 8) + 255) / 256);
-    hipLaunchKernelGGL(pack_rows_kernel, dim3(grid), dim3(256), 0, stream,
-                       static_cast<const uint16_t *>(x), ldx, n, k, out);
-    return hipGetLastError();
+    const int64_t per = rows_a_launch(k / 8);
+    for (int64_t r0 = 0; r0 < n; r0 += per) {
+        const int64_t rows = n - r0 < per ? n - r0 : per;
+        const unsigned grid = (unsigned)((rows * (k / 8) + 255) / 256);
+        hipLaunchKernelGGL(pack_rows_kernel, dim3(grid), dim3(256), 0, stream,
+                           static_cast<const uint16_t *>(x) + r0 * ldx, ldx, rows, k, out + r0 * k);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace exl3

@@ -30,9 +30,9 @@ template <bool BF, int THREADS>
 __global__ void __launch_bounds__(THREADS)
 rotate_kernel(const uint16_t *__restrict__ x, int64_t ldx, int cols, int had,
               const float *__restrict__ sv, const int32_t *__restrict__ offsets, int groups,
-              uint16_t *__restrict__ xh, float *__restrict__ xs) {
+              int64_t row0, uint16_t *__restrict__ xh, float *__restrict__ xs) {
     __shared__ float wave_big[THREADS / 64];
-    const int64_t row = blockIdx.x;
+    const int64_t row = row0 + blockIdx.x;
     if (offsets) {
         const int e = group_of_row(offsets, groups, row);
         sv += (size_t)(e < groups ? e : groups - 1) * cols;
@@ -715,10 +715,12 @@ __global__ void __launch_bounds__(64)
 finish_kernel(const float *__restrict__ part, int split, int64_t n, int rows, int had,
               const float *__restrict__ scale, const float *__restrict__ su,
               const int32_t *__restrict__ offsets, int groups, AdapterArgs ad,
-              const uint16_t *__restrict__ v, bool bf16, uint16_t *__restrict__ y, int64_t ldy) {
+              const uint16_t *__restrict__ v, bool bf16, int64_t tok0, uint16_t *__restrict__ y,
+              int64_t ldy) {
     const int lane = threadIdx.x & 63, blocks = (rows + 511) / 512;
-    const int64_t tok = blockIdx.x / blocks;
-    const int row = (int)(blockIdx.x - tok * blocks) * 512 + lane * 8;
+    const int here = blockIdx.x / blocks;
+    const int64_t tok = tok0 + here;
+    const int row = (int)(blockIdx.x - here * blocks) * 512 + lane * 8;
     const bool in = row < rows;
     const int id = v ? ad.ids[tok] : -1;
     int e = 0;
@@ -782,20 +784,26 @@ hipError_t coded_rows_t(const WeightArgs &w, const int32_t *offsets, const RowsA
 hipError_t launch_rotate(const WeightArgs &w, const int32_t *offsets, const void *x, int64_t ldx,
                          int64_t n, bool bf16, uint16_t *xh, float *xs, hipStream_t stream) {
     const uint16_t *xx = static_cast<const uint16_t *>(x);
-#define EXL3_ROTATE(BF, THREADS)                                                               \
-    hipLaunchKernelGGL((rotate_kernel<BF, THREADS>), dim3((unsigned)n), dim3(THREADS), 0, stream, \
-                       xx, ldx, w.cols, w.had, w.sv, offsets, w.groups, xh, xs)
-    // a round a row while that takes at most 512 lanes
-    if (bf16 && w.cols <= 2048)
-        EXL3_ROTATE(true, 256);
-    else if (bf16)
-        EXL3_ROTATE(true, 512);
-    else if (w.cols <= 2048)
-        EXL3_ROTATE(false, 256);
-    else
-        EXL3_ROTATE(false, 512);
+#define EXL3_ROTATE(BF, THREADS)                                                              \
+    hipLaunchKernelGGL((rotate_kernel<BF, THREADS>), dim3(rows), dim3(THREADS), 0, stream, xx, \
+                       ldx, w.cols, w.had, w.sv, offsets, w.groups, r0, xh, xs)
+    const int64_t per = rows_a_launch(512);
+    for (int64_t r0 = 0; r0 < n; r0 += per) {
+        const unsigned rows = (unsigned)(n - r0 < per ? n - r0 : per);
+        // a round a row while that takes at most 512 lanes
+        if (bf16 && w.cols <= 2048)
+            EXL3_ROTATE(true, 256);
+        else if (bf16)
+            EXL3_ROTATE(true, 512);
+        else if (w.cols <= 2048)
+            EXL3_ROTATE(false, 256);
+        else
+            EXL3_ROTATE(false, 512);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
 #undef EXL3_ROTATE
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 hipError_t launch_coded_rows(const WeightArgs &w, const int32_t *offsets, const RowsArgs &a,
@@ -877,12 +885,18 @@ hipError_t launch_coded_tiles(const WeightArgs &w, const int32_t *offsets, const
 hipError_t launch_finish(const WeightArgs &w, const int32_t *offsets, const float *part, int split,
                          int64_t n, bool bf16, const AdapterArgs *ad, const uint16_t *v, void *y,
                          int64_t ldy, hipStream_t stream) {
-    const unsigned grid = (unsigned)(n * ((w.rows + 511) / 512));
+    const int blocks = (w.rows + 511) / 512;
     const AdapterArgs args = ad ? *ad : AdapterArgs{};
-    hipLaunchKernelGGL(finish_kernel, dim3(grid), dim3(64), 0, stream, part, split, n, w.rows,
-                       w.had, w.scale, w.su, offsets, w.groups, args, v, bf16,
-                       static_cast<uint16_t *>(y), ldy);
-    return hipGetLastError();
+    const int64_t per = rows_a_launch(64 * blocks);
+    for (int64_t t0 = 0; t0 < n; t0 += per) {
+        const unsigned grid = (unsigned)(n - t0 < per ? n - t0 : per) * (unsigned)blocks;
+        hipLaunchKernelGGL(finish_kernel, dim3(grid), dim3(64), 0, stream, part, split, n, w.rows,
+                           w.had, w.scale, w.su, offsets, w.groups, args, v, bf16, t0,
+                           static_cast<uint16_t *>(y), ldy);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace exl3
