@@ -316,6 +316,21 @@ void close_timed(exl3_ctx *ctx, int id) {
     if (id >= 0) (void)hipEventRecord(ctx->timed[(size_t)id].stop, ctx->timed[(size_t)id].stream);
 }
 
+// The record of a call that may fail on the way: closed with rc == EXL3_OK, taken
+// out otherwise, as its events may never have been recorded.  It has to be the
+// last one.
+int end_timed(exl3_ctx *ctx, int id, int rc) {
+    if (id < 0) return rc;
+    if (rc == EXL3_OK) {
+        close_timed(ctx, id);
+        return rc;
+    }
+    (void)hipEventDestroy(ctx->timed.back().start);
+    (void)hipEventDestroy(ctx->timed.back().stop);
+    ctx->timed.pop_back();
+    return rc;
+}
+
 int ensure_small(exl3_ctx *ctx, size_t n) {
     if (n <= ctx->small_cap && ctx->d_end && ctx->d_X && ctx->d_cost) return EXL3_OK;
     if (ctx->d_end || ctx->d_X || ctx->d_cost) {
@@ -1050,9 +1065,71 @@ int linear_any(exl3_ctx *ctx, const exl3_weight *w, const int32_t *offsets, int 
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
     const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT,
                               (int64_t)w->groups * (w->rows / 16) * (w->cols / 16));
-    rc = run_product(ctx, p);
-    close_timed(ctx, id);
-    return rc;
+    return end_timed(ctx, id, run_product(ctx, p));
+}
+
+int run_adapters(exl3_ctx *ctx, const Product &p, const exl3::AdapterArgs &aa) {
+    const exl3::ShrinkArgs sh{static_cast<const uint16_t *>(aa.a),
+                              static_cast<const uint16_t *>(p.x), p.ldx, p.w->cols,
+                              reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at), nullptr, 0};
+    EXL3_HIP(ctx, exl3::launch_shrink(aa, &sh, 1, p.n, p.bf16, ctx->stream));
+    return run_product(ctx, p);
+}
+
+// Where the backward pass's operands lie in the workspace.
+struct BackwardPlan {
+    bool wants_dx, needs_u;
+    size_t pitch, v_at, ut_at, vt_at, bt_at, at_at, pa_at, pb_at, used_at;
+    int splits;
+};
+
+int run_backward(exl3_ctx *ctx, Product &p, const exl3::AdapterArgs &aa, const BackwardPlan &b,
+                 const void *x, int64_t ldx, void *da, void *db) {
+    const exl3::WeightArgs &w = *p.w;
+    const int64_t n = p.n, lddy = p.ldx;
+    char *ws = ctx->d_work;
+    auto at16 = [ws](size_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
+    const uint16_t *a16 = static_cast<const uint16_t *>(aa.a);
+    const uint16_t *b16 = static_cast<const uint16_t *>(aa.b);
+    const uint16_t *x16 = static_cast<const uint16_t *>(x);
+    const uint16_t *dy16 = static_cast<const uint16_t *>(p.x);
+    if (n > 0) {
+        // u = alpha dy B (its matrix transposed), v = alpha x A^T
+        exl3::TransposeArgs tr[2];
+        exl3::ShrinkArgs sh[2];
+        int nt = 0, ns = 0;
+        if (b.needs_u) {
+            tr[nt++] = exl3::TransposeArgs{b16, at16(b.bt_at), w.rows, aa.rank};
+            sh[ns++] = exl3::ShrinkArgs{at16(b.bt_at), dy16, lddy, w.rows, at16(p.v_at),
+                                        da ? at16(b.ut_at) : nullptr, (int64_t)b.pitch};
+        }
+        if (b.wants_dx) tr[nt++] = exl3::TransposeArgs{a16, at16(b.at_at), aa.rank, w.cols};
+        if (db)
+            sh[ns++] = exl3::ShrinkArgs{a16, x16, ldx, w.cols, at16(b.v_at), at16(b.vt_at),
+                                        (int64_t)b.pitch};
+        if (nt) EXL3_HIP(ctx, exl3::launch_transpose16(tr, nt, aa.count, ctx->stream));
+        if (ns) EXL3_HIP(ctx, exl3::launch_shrink(aa, sh, ns, n, p.bf16, ctx->stream));
+    }
+    if (b.wants_dx) {
+        p.ad_b = ws + b.at_at;
+        const int rc = run_product(ctx, p);
+        if (rc != EXL3_OK) return rc;
+    }
+    exl3::GradArgs gr[2];
+    int ng = 0;
+    if (da)
+        gr[ng++] = exl3::GradArgs{at16(b.ut_at), x16, (int64_t)b.pitch, ldx, w.cols, false,
+                                  reinterpret_cast<float *>(ws + b.pa_at),
+                                  static_cast<uint16_t *>(da)};
+    if (db)
+        gr[ng++] = exl3::GradArgs{at16(b.vt_at), dy16, (int64_t)b.pitch, lddy, w.rows, true,
+                                  reinterpret_cast<float *>(ws + b.pb_at),
+                                  static_cast<uint16_t *>(db)};
+    if (ng)
+        EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, gr, ng, n, p.bf16, b.splits,
+                                                reinterpret_cast<uint8_t *>(ws + b.used_at),
+                                                ctx->stream));
+    return EXL3_OK;
 }
 
 }  // namespace
@@ -1979,13 +2056,7 @@ int exl3_adapter_linear(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters
     if ((rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
     const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
-    const exl3::ShrinkArgs sh{static_cast<const uint16_t *>(aa.a),
-                              static_cast<const uint16_t *>(x), ldx, w->cols,
-                              reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at), nullptr, 0};
-    EXL3_HIP(ctx, exl3::launch_shrink(aa, &sh, 1, n, p.bf16, ctx->stream));
-    rc = run_product(ctx, p);
-    close_timed(ctx, id);
-    return rc;
+    return end_timed(ctx, id, run_adapters(ctx, p, aa));
 }
 
 int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters *ad,
@@ -2012,76 +2083,38 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
          ((da || db) && rows_overlap(x, ldx, w->cols, dx, lddx, w->cols, n))))
         return fail(ctx, EXL3_EINVAL, "dx overlaps dy or x");
     if ((rc = set_device(ctx)) != EXL3_OK) return rc;
-    const bool bf16 = dtype == EXL3_BF16, wants_dx = dx && n > 0;
-    const bool needs_u = wants_dx || da;
+    BackwardPlan b{};
+    b.wants_dx = dx && n > 0;
+    b.needs_u = b.wants_dx || da;
     Product p{};
     p.w = &wa;
     p.transpose = true;
     p.x = dy;
     p.ldx = lddy;
     p.n = n;
-    p.bf16 = bf16;
+    p.bf16 = dtype == EXL3_BF16;
     p.y = dx;
     p.ldy = lddx;
     p.ad = &aa;
     Carve c;
     // room for what the wanted gradients need only
     auto take = [&c](bool wanted, size_t bytes) { return wanted ? c.take(bytes) : 0; };
-    const size_t pitch = ((size_t)n + 31) / 32 * 32, ranks = (size_t)aa.rank_pad;
-    p.v_at = take(needs_u, (size_t)n * ranks * 2);
-    const size_t v_at = take(db, (size_t)n * ranks * 2);
-    const size_t ut_at = take(da, pitch * ranks * 2), vt_at = take(db, pitch * ranks * 2);
-    const size_t bt_at = take(needs_u, m * w->rows * 2), at_at = take(wants_dx, m * w->cols * 2);
-    const int splits = exl3::adapter_grad_splits(n, aa.count);
-    const size_t pa_at = take(da, splits * m * w->cols * sizeof(float));
-    const size_t pb_at = take(db, splits * m * w->rows * sizeof(float));
-    const size_t used_at = take(da || db, (size_t)splits * aa.count);
-    if (wants_dx && (rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
+    const size_t ranks = (size_t)aa.rank_pad;
+    b.pitch = ((size_t)n + 31) / 32 * 32;
+    p.v_at = take(b.needs_u, (size_t)n * ranks * 2);
+    b.v_at = take(db, (size_t)n * ranks * 2);
+    b.ut_at = take(da, b.pitch * ranks * 2);
+    b.vt_at = take(db, b.pitch * ranks * 2);
+    b.bt_at = take(b.needs_u, m * w->rows * 2);
+    b.at_at = take(b.wants_dx, m * w->cols * 2);
+    b.splits = exl3::adapter_grad_splits(n, aa.count);
+    b.pa_at = take(da, b.splits * m * w->cols * sizeof(float));
+    b.pb_at = take(db, b.splits * m * w->rows * sizeof(float));
+    b.used_at = take(da || db, (size_t)b.splits * aa.count);
+    if (b.wants_dx && (rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
-    char *ws = ctx->d_work;
-    auto at16 = [ws](size_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
     const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
-    const uint16_t *a16 = static_cast<const uint16_t *>(aa.a);
-    const uint16_t *b16 = static_cast<const uint16_t *>(aa.b);
-    const uint16_t *x16 = static_cast<const uint16_t *>(x);
-    const uint16_t *dy16 = static_cast<const uint16_t *>(dy);
-    if (n > 0) {
-        // u = alpha dy B (its matrix transposed), v = alpha x A^T
-        exl3::TransposeArgs tr[2];
-        exl3::ShrinkArgs sh[2];
-        int nt = 0, ns = 0;
-        if (needs_u) {
-            tr[nt++] = exl3::TransposeArgs{b16, at16(bt_at), w->rows, aa.rank};
-            sh[ns++] = exl3::ShrinkArgs{at16(bt_at), dy16, lddy, w->rows, at16(p.v_at),
-                                        da ? at16(ut_at) : nullptr, (int64_t)pitch};
-        }
-        if (wants_dx) tr[nt++] = exl3::TransposeArgs{a16, at16(at_at), aa.rank, w->cols};
-        if (db)
-            sh[ns++] = exl3::ShrinkArgs{a16, x16, ldx, w->cols, at16(v_at), at16(vt_at),
-                                        (int64_t)pitch};
-        if (nt) EXL3_HIP(ctx, exl3::launch_transpose16(tr, nt, aa.count, ctx->stream));
-        if (ns) EXL3_HIP(ctx, exl3::launch_shrink(aa, sh, ns, n, bf16, ctx->stream));
-    }
-    if (wants_dx) {
-        p.ad_b = ws + at_at;
-        if ((rc = run_product(ctx, p)) != EXL3_OK) return rc;
-    }
-    exl3::GradArgs gr[2];
-    int ng = 0;
-    if (da)
-        gr[ng++] = exl3::GradArgs{at16(ut_at), x16, (int64_t)pitch, ldx, w->cols, false,
-                                  reinterpret_cast<float *>(ws + pa_at),
-                                  static_cast<uint16_t *>(da)};
-    if (db)
-        gr[ng++] = exl3::GradArgs{at16(vt_at), dy16, (int64_t)pitch, lddy, w->rows, true,
-                                  reinterpret_cast<float *>(ws + pb_at),
-                                  static_cast<uint16_t *>(db)};
-    if (ng)
-        EXL3_HIP(ctx, exl3::launch_adapter_grad(aa, gr, ng, n, bf16, splits,
-                                                reinterpret_cast<uint8_t *>(ws + used_at),
-                                                ctx->stream));
-    close_timed(ctx, id);
-    return EXL3_OK;
+    return end_timed(ctx, id, run_backward(ctx, p, aa, b, x, ldx, da, db));
 }
 
 }  // extern "C"
