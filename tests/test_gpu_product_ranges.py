@@ -87,6 +87,20 @@ def test_binary16_channels_of_many_sizes(T, ctx, n, transpose):
     check(y, x64 @ m.T, spread_of(x64 * inner, m / inner), inner_of(False, FP))
 
 
+@pytest.mark.parametrize("at", [0, 1, 2, 3, 126, 127])
+@pytest.mark.parametrize("n,transpose", [(513, False), (257, True)])
+def test_binary16_one_large_factor(T, ctx, n, transpose, at):
+    """One factor of the contracted side far above the others, wherever it stands."""
+    w = random_weight(128, 128, 2, 64, 426, dead=False)
+    name = "su" if transpose else "sv"
+    w[name][at] *= 2.0 ** 14
+    m, inner = (dense(w).T, w["su"]) if transpose else (dense(w), w["sv"])
+    inner = inner.astype(np.float64)
+    x, x64 = rows_of(n, 128, FP, 427, 0.05)
+    y = ctx.linear(x, on_gpu(T, w), transpose=transpose)
+    check(y, x64 @ m.T, spread_of(x64 * inner, m / inner), inner_of(False, FP))
+
+
 @pytest.mark.parametrize("per,transpose", [(513, False), (257, True)])
 def test_binary16_groups_of_different_sizes(T, per, transpose):
     """Groups whose weights lie 40 powers of two apart, in batches of two of the dense form."""

@@ -228,7 +228,9 @@ inner_kernel(const float *__restrict__ factors, int k, int32_t *__restrict__ inn
         const f32x4 v = *reinterpret_cast<const f32x4u *>(at + c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t m = __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu;
+            const float one = v[i];              // (of a vector's element itself a bit cast is
+                                                 // that of the first)
+            const uint32_t m = __builtin_bit_cast(uint32_t, one) & 0x7FFFFFFFu;
             big = m > big ? m : big;
         }
     }
