@@ -476,8 +476,9 @@ typedef struct {
  * requests at once, each with its adapter.
  *   ids    int32 [n], device: the row's adapter, or -1 for none (any value
  *          outside 0..count-1 is none)
- * W has groups = 1.  alpha (x A^T) is rounded to the activations' type; an
- * adapter's values reach no row of another.  Otherwise as exl3_linear.
+ * W has groups = 1.  alpha (x A^T) is rounded to the activations' type (binary16:
+ * over a power of two of each row, so that its range is not met); an adapter's
+ * values reach no row of another.  Otherwise as exl3_linear.
  */
 int exl3_adapter_linear(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters *ad,
                         const int32_t *ids, const void *x, int64_t ldx, int64_t n, int dtype,
@@ -489,6 +490,8 @@ int exl3_adapter_linear(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters
  *   da_a = sum over the rows t of adapter a of alpha_a (dy_t B_a)^T x_t
  *   db_a = sum over the rows t of adapter a of dy_t^T (alpha_a x_t A_a^T)
  *   dx   [n][cols], rows lddx apart, or null;  da, db  as a and b, or null
+ * alpha (dy B) is rounded as alpha (x A^T) is; for da and db in binary16 the power
+ * of two is that of the rows of one adapter among 16 neighbours.
  * Written whole (zero for adapters without rows), in the activations' type; the
  * sums over rows are binary32, in an order that does not depend on scheduling.
  * x is read for da and db only.  Errors: as exl3_linear.

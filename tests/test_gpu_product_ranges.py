@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
-from product_reference import check, dense, inner_of, random_weight, spread_of
-from test_gpu_products import BF, DEV, FP, on_gpu, rows_of
+from product_reference import HALF, check, dense, inner_of, random_weight, spread_of
+from test_gpu_products import (BF, DEV, FP, adapter_forward, adapters_of, ids_of, on_gpu,
+                               rows_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +121,70 @@ def test_binary16_groups_of_different_sizes(T, per, transpose):
             m = m.T if transpose else m
             at = slice(e * per, e * per + per)
             check(y[at], x64[at] @ m.T, spread_of(x64[at], m), inner_of(False, FP), "group %d" % e)
+
+
+def check_subnormal(got, want, spread, inner, name):
+    """check() for results that may lie in binary16's subnormal range, where a rounding is off by
+    half a step of 2^-24 whatever the value: of every value, as there, and so of the whole."""
+    off = np.abs(got.detach().double().cpu().numpy() - want)
+    u, half_step = HALF[FP], 2.0 ** -25
+    assert np.isfinite(off).all(), name
+    bound = u * np.abs(want) * 1.001 + (8 / np.sqrt(3) * inner[0] + 2.0 ** -20) * spread + half_step
+    assert (off <= bound).all(), "%s: %.3g times its bound" % (name, (off / bound).max())
+    norm = np.linalg.norm(np.broadcast_to(spread, want.shape))
+    assert np.linalg.norm(off) <= u * np.linalg.norm(want) + (inner[0] + 2.0 ** -20) * norm + \
+        half_step * np.sqrt(want.size), name
+
+
+# x, A, B and dy: alpha dy B far below binary16's normal range; alpha x A^T past its largest value
+@pytest.mark.parametrize("n", [3, 40, 600])
+@pytest.mark.parametrize("sx,sa,sb,sd", [(30.0, 1 / 16, 1e-3, 1e-5), (100.0, 60.0, 1e-4, 1e-4)])
+def test_binary16_adapters_of_any_size(T, ctx, sx, sa, sb, sd, n):
+    rows, cols, count, rank = 256, 256, 3, 12
+    r = np.random.Generator(np.random.PCG64(441))
+    w = random_weight(rows, cols, 2, 128, 442)
+    A = torch.from_numpy(r.standard_normal((count, rank, cols)) * sa).to(FP)
+    B = torch.from_numpy(r.standard_normal((count, rows, rank)) * sb).to(FP)
+    al = torch.from_numpy((0.5 + r.random(count)).astype(np.float32))
+    x, x64 = rows_of(n, cols, FP, 443, sx)
+    dy, d64 = rows_of(n, rows, FP, 444, sd)
+    ids = ids_of(n, count, 445)
+    ad = T.Adapters(A.to(DEV), B.to(DEV), al.to(DEV))
+    idt, g, m = torch.from_numpy(ids).to(DEV), on_gpu(T, w), dense(w)
+    A, B, al = A.double().numpy(), B.double().numpy(), al.double().numpy()
+    part, s = adapter_forward(x64, A, B, al, ids)
+    y = ctx.adapter_linear(x, g, ad, idt)
+    check_subnormal(y, x64 @ m.T + part, spread_of(x64, m) + s, inner_of(False, FP), "y")
+    dx, dA, dB = ctx.adapter_linear_backward(dy, x, g, ad, idt)
+    part, s = adapter_forward(d64, B.transpose(0, 2, 1), A.transpose(0, 2, 1), al, ids)
+    check_subnormal(dx, d64 @ m + part, spread_of(d64, m.T) + s, inner_of(False, FP), "dx")
+    for a in range(count):
+        at = np.flatnonzero(ids == a)
+        v, u = al[a] * (x64[at] @ A[a].T), al[a] * (d64[at] @ B[a])
+        half = (HALF[FP], FP)
+        check_subnormal(dA[a], u.T @ x64[at], np.sqrt((u ** 2).T @ x64[at] ** 2), half, "dA")
+        check_subnormal(dB[a], d64[at].T @ v, np.sqrt((d64[at] ** 2).T @ v ** 2), half, "dB")
+
+
+def test_binary16_rows_of_one_adapter_of_many_sizes(T, ctx):
+    """Rows of one adapter, neighbours and far apart, over 20 powers of two: each row's part of y
+    and dx is right by itself, the gradients' sums by the largest rows."""
+    n, rows, cols, rank = 200, 128, 128, 8
+    r = np.random.Generator(np.random.PCG64(451))
+    w = random_weight(rows, cols, 2, 64, 452)
+    ad, A, B, al = adapters_of(T, rows, cols, 1, rank, FP, 453)
+    size = 2.0 ** r.uniform(-14, 6, n)[:, None]
+    x = torch.from_numpy(r.standard_normal((n, cols)) * size).to(FP)
+    dy = torch.from_numpy(r.standard_normal((n, rows)) * r.permutation(size)).to(FP)
+    ids = np.zeros(n, np.int32)
+    m, x64, d64 = dense(w), x.double().numpy(), dy.double().numpy()
+    g, idt = on_gpu(T, w), torch.zeros(n, dtype=torch.int32, device=DEV)
+    part, s = adapter_forward(x64, A, B, al, ids)
+    check_subnormal(ctx.adapter_linear(x.to(DEV), g, ad, idt), x64 @ m.T + part,
+                    spread_of(x64, m) + s, inner_of(False, FP), "y")
+    dx, dA, dB = ctx.adapter_linear_backward(dy.to(DEV), x.to(DEV), g, ad, idt)
+    part, s = adapter_forward(d64, B.transpose(0, 2, 1), A.transpose(0, 2, 1), al, ids)
+    check_subnormal(dx, d64 @ m + part, spread_of(d64, m.T) + s, inner_of(False, FP), "dx")
+    v, u = al[0] * (x64 @ A[0].T), al[0] * (d64 @ B[0])
+    check_subnormal(dA[0], u.T @ x64, np.sqrt((u ** 2).T @ x64 ** 2), (HALF[FP], FP), "dA")
+    check_subnormal(dB[0], d64.T @ v, np.sqrt((d64 ** 2).T @ v ** 2), (HALF[FP], FP), "dB")

@@ -2,8 +2,11 @@
 // narrow matrices.  A row t of the activations has the adapter a = ids[t] (or
 // none), and v_t = alpha_a A_a x_t enters the projection's kernels as one
 // more, short, contraction (B_a v_t).  v is rounded to the activations' type,
-// as the operand of that product: 2^-9 (bfloat16) or 2^-12 (binary16) of the
-// adapter's part of the result, which is rounded to the same type.
+// as the operand of that product: at most 2^-8 (bfloat16) or 2^-11 (binary16) of
+// each value, the adapter's part of a result that is rounded to the same type.
+// Binary16's range would cut gradients of common sizes (dy of 1e-5 and B of 1e-3
+// give u = alpha B^T dy near its least step), so there each row is stored over a
+// power of two that takes its largest value into [2^13, 2^14).
 #include "coded.h"
 
 namespace exl3 {
@@ -33,6 +36,7 @@ __global__ void __launch_bounds__(512)
 shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
     constexpr int kWaves = 8;
     __shared__ f32x4 sums[kWaves][RT][64];
+    __shared__ uint32_t row_big[RT][16];
     const ShrinkArgs p = blockIdx.z ? p1 : p0;
     const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 15, g = lane >> 4, k = p.k;
@@ -93,17 +97,59 @@ shrink_kernel(AdapterArgs ad, ShrinkArgs p0, ShrinkArgs p1, int64_t n) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) sums[wv][t][lane] = acc[t];
         __syncthreads();
+        f32x4 z;
         if (wv < RT) {                           // a wave a tile of ranks
-            f32x4 z = sums[0][wv][lane];
+            z = sums[0][wv][lane];
 #pragma unroll
             for (int w = 1; w < kWaves; ++w) z += sums[w][wv][lane];
+            z = ad.alpha[id] * z;
+            if (!BF) {
+                // the row's largest finite magnitude (as an integer; the others go
+                // their own way)
+                uint32_t big = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float zi = z[i];       // (a bit cast of z[i] itself is z[0]'s)
+                    const uint32_t m = __builtin_bit_cast(uint32_t, zi) & 0x7FFFFFFFu;
+                    big = id_r == id && m < 0x7F800000u && m > big ? m : big;
+                }
+#pragma unroll
+                for (int s = 16; s < 64; s <<= 1) {
+                    const uint32_t o = (uint32_t)__shfl_xor((int)big, s);
+                    big = o > big ? o : big;
+                }
+                if (lane < 16) row_big[wv][lane] = big;
+            }
+        }
+        if (!BF) __syncthreads();
+        if (wv < RT) {
+            PowerOfTwo one{1.0f, 1.0f, 1.0f, false}, all = one;      // of the row, and of 16
+            if (!BF) {
+                uint32_t big = row_big[0][r];
+#pragma unroll
+                for (int t = 1; t < RT; ++t) big = row_big[t][r] > big ? row_big[t][r] : big;
+                one = scale_for(big);
+#pragma unroll
+                for (int s = 1; s < 16; s <<= 1) {
+                    const uint32_t o = (uint32_t)__shfl_xor((int)big, s);
+                    big = o > big ? o : big;
+                }
+                all = scale_for(big);
+            }
+            auto pair = [&](const PowerOfTwo &p2, int i) {
+                return BF ? Act<BF>::store2(z[i], z[i + 1])
+                          : Act<BF>::store2(z[i] * p2.up * p2.up2, z[i + 1] * p2.up * p2.up2);
+            };
             const int c = 16 * wv + 4 * g;
             if (id_r == id && c < ad.rank_pad) {
-                const float al = ad.alpha[id];
-                const uint32_t lo = Act<BF>::store2(al * z[0], al * z[1]);
-                const uint32_t hi = Act<BF>::store2(al * z[2], al * z[3]);
-                *reinterpret_cast<uint2 *>(p.v + tok * ad.rank_pad + c) = uint2{lo, hi};
+                *reinterpret_cast<uint2 *>(p.v + tok * ad.rank_pad + c) =
+                    uint2{pair(one, 0), pair(one, 2)};
+                if (!BF && c == 0) {
+                    if (p.vs) p.vs[tok] = one.scale;
+                    if (p.ts) p.ts[tok] = all.scale;
+                }
                 if (p.vt) {
+                    const uint32_t lo = pair(all, 0), hi = pair(all, 2);
                     uint16_t *o = p.vt + (size_t)c * p.ldvt + tok;
                     o[0] = (uint16_t)lo;
                     o[p.ldvt] = (uint16_t)(lo >> 16);
@@ -145,7 +191,9 @@ transpose16_kernel(TransposeArgs t0, TransposeArgs t1) {
 // chosen and not multiplied, so that whatever they hold stays out; blocks of
 // 32 rows without the adapter are passed over.  The rows are split in parts,
 // those that have the adapter are summed in order afterwards: the result does
-// not depend on scheduling.  2,048 rows, four adapters of rank 16, 4096 x 4096:
+// not depend on scheduling.  In binary16 the two halves of a block have each a
+// power of two of their own for u: the lesser half is brought to the other's, and
+// the block's products are added under that.  2,048 rows, four adapters of rank 16, 4096 x 4096:
 // 17.5 us for both matrices, x and dy read once, eight bytes a lane and load, which
 // bounds it (34 MB, 1.9 TB/s).
 // grid: blocks of 256 columns of the first product, then of the second;
@@ -176,9 +224,15 @@ adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t
         uint2 x[8];
         u32x4 u[RT];
         uint32_t has;
+        float half[2];                           // the halves' powers of two (binary16)
     };
     auto fetch = [&](Step &s, int64_t b, uint32_t has) {
         s.has = has;
+        if (!BF) {
+            const uint32_t lo = has & 0xFFFFu, hi = has >> 16;
+            s.half[0] = lo ? p.us[b + __ffs(lo) - 1] : 0.0f;
+            s.half[1] = hi ? p.us[b + 16 + __ffs(hi) - 1] : 0.0f;
+        }
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             s.x[t] = uint2{0u, 0u};
@@ -213,11 +267,28 @@ adapter_grad_kernel(AdapterArgs ad, GradArgs g0, GradArgs g1, int64_t n, int64_t
             b[2][c] = __builtin_amdgcn_perm(by, ay, 0x05040100u);
             b[3][c] = __builtin_amdgcn_perm(by, ay, 0x07060302u);
         }
+        if (BF) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const u32x4 u = s.u[t] & keep;
+            for (int t = 0; t < RT; ++t) {
+                const u32x4 u = s.u[t] & keep;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[t][c] = Act<BF>::mfma(u, b[c], acc[t][c]);
+                for (int c = 0; c < 4; ++c) acc[t][c] = Act<BF>::mfma(u, b[c], acc[t][c]);
+            }
+        } else {
+            const float up = s.half[0] > s.half[1] ? s.half[0] : s.half[1];
+            const _Float16 by = (_Float16)((g < 2 ? s.half[0] : s.half[1]) / up);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const u32x4 u = __builtin_bit_cast(
+                    u32x4, __builtin_bit_cast(f16x8, s.u[t] & keep) * by);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const f32x4 z = Act<BF>::mfma(u, b[c], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[t][c][i] = __builtin_fmaf(z[i], up, acc[t][c][i]);
+                }
+            }
         }
     };
     bool any = false;

@@ -913,7 +913,7 @@ struct Product {
     int64_t ldy;
     const exl3::AdapterArgs *ad;
     const void *ad_b;
-    size_t v_at;               // of v in the workspace
+    size_t v_at, vs_at;        // of v and its scales (binary16) in the workspace
     // set by plan_product
     Form form;
     int split, run, per, batch;
@@ -985,6 +985,7 @@ int run_product(exl3_ctx *ctx, const Product &p) {
     if (p.ad) {
         ad_args = *p.ad;
         ad_args.b = p.ad_b;
+        ad_args.vs = p.bf16 ? nullptr : reinterpret_cast<const float *>(ctx->d_work + p.vs_at);
     }
     const exl3::AdapterArgs *ad = p.ad ? &ad_args : nullptr;
     char *ws = ctx->d_work;
@@ -1030,7 +1031,7 @@ int run_product(exl3_ctx *ctx, const Product &p) {
         EXL3_HIP(ctx, exl3::launch_dense(*p.w, p.offsets, p.n, g0, ng, p.transpose, p.bf16, inner,
                                          dense, p.y, p.ldy, ctx->stream));
         EXL3_HIP(ctx, exl3::launch_gemm(x, ldx, dense, ds, p.n, m, k, p.offsets, g0, ng, p.bf16,
-                                        p.ad, p.ad_b, v, p.y, p.ldy, ctx->n_cu, ctx->stream));
+                                        ad, p.ad_b, v, p.y, p.ldy, ctx->n_cu, ctx->stream));
     }
     return EXL3_OK;
 }
@@ -1071,7 +1072,9 @@ int linear_any(exl3_ctx *ctx, const exl3_weight *w, const int32_t *offsets, int 
 int run_adapters(exl3_ctx *ctx, const Product &p, const exl3::AdapterArgs &aa) {
     const exl3::ShrinkArgs sh{static_cast<const uint16_t *>(aa.a),
                               static_cast<const uint16_t *>(p.x), p.ldx, p.w->cols,
-                              reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at), nullptr, 0};
+                              reinterpret_cast<uint16_t *>(ctx->d_work + p.v_at), nullptr, 0,
+                              p.bf16 ? nullptr : reinterpret_cast<float *>(ctx->d_work + p.vs_at),
+                              nullptr};
     EXL3_HIP(ctx, exl3::launch_shrink(aa, &sh, 1, p.n, p.bf16, ctx->stream));
     return run_product(ctx, p);
 }
@@ -1079,7 +1082,7 @@ int run_adapters(exl3_ctx *ctx, const Product &p, const exl3::AdapterArgs &aa) {
 // Where the backward pass's operands lie in the workspace.
 struct BackwardPlan {
     bool wants_dx, needs_u;
-    size_t pitch, v_at, ut_at, vt_at, bt_at, at_at, pa_at, pb_at, used_at;
+    size_t pitch, v_at, ut_at, vt_at, uts_at, vts_at, bt_at, at_at, pa_at, pb_at, used_at;
     int splits;
 };
 
@@ -1089,6 +1092,9 @@ int run_backward(exl3_ctx *ctx, Product &p, const exl3::AdapterArgs &aa, const B
     const int64_t n = p.n, lddy = p.ldx;
     char *ws = ctx->d_work;
     auto at16 = [ws](size_t at) { return reinterpret_cast<uint16_t *>(ws + at); };
+    auto scales = [ws, &p](bool wanted, size_t at) {
+        return wanted && !p.bf16 ? reinterpret_cast<float *>(ws + at) : nullptr;
+    };
     const uint16_t *a16 = static_cast<const uint16_t *>(aa.a);
     const uint16_t *b16 = static_cast<const uint16_t *>(aa.b);
     const uint16_t *x16 = static_cast<const uint16_t *>(x);
@@ -1101,12 +1107,13 @@ int run_backward(exl3_ctx *ctx, Product &p, const exl3::AdapterArgs &aa, const B
         if (b.needs_u) {
             tr[nt++] = exl3::TransposeArgs{b16, at16(b.bt_at), w.rows, aa.rank};
             sh[ns++] = exl3::ShrinkArgs{at16(b.bt_at), dy16, lddy, w.rows, at16(p.v_at),
-                                        da ? at16(b.ut_at) : nullptr, (int64_t)b.pitch};
+                                        da ? at16(b.ut_at) : nullptr, (int64_t)b.pitch,
+                                        scales(true, p.vs_at), scales(da, b.uts_at)};
         }
         if (b.wants_dx) tr[nt++] = exl3::TransposeArgs{a16, at16(b.at_at), aa.rank, w.cols};
         if (db)
             sh[ns++] = exl3::ShrinkArgs{a16, x16, ldx, w.cols, at16(b.v_at), at16(b.vt_at),
-                                        (int64_t)b.pitch};
+                                        (int64_t)b.pitch, nullptr, scales(true, b.vts_at)};
         if (nt) EXL3_HIP(ctx, exl3::launch_transpose16(tr, nt, aa.count, ctx->stream));
         if (ns) EXL3_HIP(ctx, exl3::launch_shrink(aa, sh, ns, n, p.bf16, ctx->stream));
     }
@@ -1118,11 +1125,13 @@ int run_backward(exl3_ctx *ctx, Product &p, const exl3::AdapterArgs &aa, const B
     exl3::GradArgs gr[2];
     int ng = 0;
     if (da)
-        gr[ng++] = exl3::GradArgs{at16(b.ut_at), x16, (int64_t)b.pitch, ldx, w.cols, false,
+        gr[ng++] = exl3::GradArgs{at16(b.ut_at), x16, scales(true, b.uts_at), (int64_t)b.pitch, ldx,
+                                  w.cols, false,
                                   reinterpret_cast<float *>(ws + b.pa_at),
                                   static_cast<uint16_t *>(da)};
     if (db)
-        gr[ng++] = exl3::GradArgs{at16(b.vt_at), dy16, (int64_t)b.pitch, lddy, w.rows, true,
+        gr[ng++] = exl3::GradArgs{at16(b.vt_at), dy16, scales(true, b.vts_at), (int64_t)b.pitch, lddy,
+                                  w.rows, true,
                                   reinterpret_cast<float *>(ws + b.pb_at),
                                   static_cast<uint16_t *>(db)};
     if (ng)
@@ -2053,6 +2062,7 @@ int exl3_adapter_linear(exl3_ctx *ctx, const exl3_weight *w, const exl3_adapters
     p.ad_b = aa.b;
     Carve c;
     p.v_at = c.take((size_t)n * aa.rank_pad * 2);
+    p.vs_at = p.bf16 ? 0 : c.take((size_t)n * sizeof(float));
     if ((rc = plan_product(ctx, p, c)) != EXL3_OK) return rc;
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
     const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
@@ -2105,6 +2115,9 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
     b.v_at = take(db, (size_t)n * ranks * 2);
     b.ut_at = take(da, b.pitch * ranks * 2);
     b.vt_at = take(db, b.pitch * ranks * 2);
+    p.vs_at = take(b.needs_u && !p.bf16, (size_t)n * sizeof(float));
+    b.uts_at = take(da && !p.bf16, (size_t)n * sizeof(float));
+    b.vts_at = take(db && !p.bf16, (size_t)n * sizeof(float));
     b.bt_at = take(b.needs_u, m * w->rows * 2);
     b.at_at = take(b.wants_dx, m * w->cols * 2);
     b.splits = exl3::adapter_grad_splits(n, aa.count);

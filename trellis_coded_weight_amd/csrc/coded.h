@@ -402,6 +402,7 @@ struct AdapterArgs {
     const float *alpha;
     const int32_t *ids;       // [n]
     int count, rank, rank_pad;
+    const float *vs;          // [n]: what v's rows are multiplied by (binary16), or null
 };
 
 // A launch takes fewer than 2^32 lanes along a grid's side: rows (or pieces) a
@@ -486,14 +487,17 @@ hipError_t launch_pack_rows(const void *x, int64_t ldx, int64_t n, int k, uint16
 
 // v[n][rank_pad] = alpha_a x a_a^T in the activations' type, zero past the rank
 // and for rows without an adapter; a: [count][rank][k].  vt, if not null, also
-// gets v transposed, [rank_pad][ldvt] (rows with an adapter only).  One launch
-// takes up to two such products.
+// gets v transposed, [rank_pad][ldvt] (rows with an adapter only).  In binary16
+// a row of v is stored over a power of two vs[t], and of vt over ts[t], which rows
+// of one adapter among 16 share (rows with an adapter only; vs may be null, and
+// both are for bfloat16).  One launch takes up to two such products.
 struct ShrinkArgs {
     const uint16_t *a, *x;
     int64_t ldx;
     int k;
     uint16_t *v, *vt;
     int64_t ldvt;
+    float *vs, *ts;
 };
 hipError_t launch_shrink(const AdapterArgs &ad, const ShrinkArgs *p, int products, int64_t n,
                          bool bf16, hipStream_t stream);
@@ -509,9 +513,11 @@ hipError_t launch_transpose16(const TransposeArgs *t, int arrays, int count, hip
 // out[a][i][j] = sum over the rows t of adapter a of u[t][i] q[t][j], i < rank;
 // written as [count][rank][k], or [count][k][rank] when transposed.  ut: u
 // transposed, rows 16-byte aligned and ldut >= n rounded up to 32 apart.  part:
-// float [splits][count][rank][k].  Up to two products of equal n and splits.
+// float [splits][count][rank][k].  us: launch_shrink's ts (binary16).  Up to two
+// products of equal n and splits.
 struct GradArgs {
     const uint16_t *ut, *q;
+    const float *us;
     int64_t ldut, ldq;
     int k;
     bool transposed;

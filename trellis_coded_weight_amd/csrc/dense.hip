@@ -437,6 +437,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
                 // the rank
                 const int valid = ad.rank - kk - 8 * g;
                 u32x4 keep, av[TM], bv[TN];
+                float vs[TN];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     keep[c] = valid >= 2 * c + 2 ? 0xFFFFFFFFu : valid == 2 * c + 1 ? 0xFFFFu : 0u;
@@ -459,6 +460,7 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
                     int64_t tok = t0 + 16 * j + r;
                     tok = tok < hi ? tok : hi - 1;
                     bv[j] = *reinterpret_cast<const u32x4 *>(v + tok * ad.rank_pad + kk + 8 * g);
+                    vs[j] = BF ? 1.0f : ad.vs[tok];
                 }
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
@@ -467,7 +469,8 @@ gemm_kernel(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restr
                         f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
                         z = Act<BF>::mfma(av[i] & keep, bv[j], z);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[i][j][c] += idj[j] == next ? z[c] : 0.0f;
+                        for (int c = 0; c < 4; ++c)
+                            acc[i][j][c] += idj[j] == next ? (BF ? z[c] : z[c] * vs[j]) : 0.0f;
                     }
             }
         }

@@ -126,6 +126,7 @@ __device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *
             const uint16_t *b = static_cast<const uint16_t *>(ad.b) +
                                 ((size_t)id * rows + row) * ad.rank;
             const uint16_t *vt = v + tok * ad.rank_pad;
+            const float vs = ad.vs ? ad.vs[tok] : 1.0f;
             int k = 0;
             for (; AHEAD && k + 16 <= ad.rank; k += 16) {
                 u32x4 vk[2], bk[8][2];
@@ -142,7 +143,7 @@ __device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const float vf =
-                            act_load(bf16, (uint16_t)(vk[h][c >> 1] >> (16 * (c & 1))));
+                            act_load(bf16, (uint16_t)(vk[h][c >> 1] >> (16 * (c & 1)))) * vs;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             z[i] += vf * act_load(bf16, (uint16_t)(bk[i][h][c >> 1] >>
@@ -154,7 +155,7 @@ __device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *
                 float vf[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    vf[c] = act_load(bf16, (uint16_t)(vk[c >> 1] >> (16 * (c & 1))));
+                    vf[c] = act_load(bf16, (uint16_t)(vk[c >> 1] >> (16 * (c & 1)))) * vs;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint16_t *bi = b + (size_t)i * ad.rank + k;
