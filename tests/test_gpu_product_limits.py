@@ -23,6 +23,115 @@ def ctx(T):
     c.close()
 
 
+def unaligned(T, w):
+    """The weight with words that start on 8 bytes, which the tiles' kernel does not take."""
+    g = on_gpu(T, w)
+    flat = torch.zeros(g.packed.numel() + 4, dtype=torch.int16, device=DEV)
+    flat[4:] = g.packed.reshape(-1)
+    h = T.CodedWeight(flat[4:].view(g.packed.shape), w["K"], g.scale, g.su, g.sv,
+                      had_block=w["had"])
+    assert h.packed.data_ptr() % 16 == 8
+    return h
+
+
+def cut_of(sizes, first=0):
+    cut = first + np.concatenate([[0], np.cumsum(sizes)])
+    return cut, torch.from_numpy(cut.astype(np.int32)).to(DEV)
+
+
+def check_groups(y, x64, w, cut, transpose, dtype):
+    for e in range(len(cut) - 1):
+        if cut[e + 1] > cut[e]:
+            m = dense(w, group=e)
+            m = m.T if transpose else m
+            xe = x64[cut[e]:cut[e + 1]]
+            check(y[cut[e]:cut[e + 1]], xe @ m.T, spread_of(xe, m), inner_of(False, dtype),
+                  "group %d" % e)
+
+
+# ---- dense weights of groups ----
+# more than 64 rows a group on average, so that also x W^T takes the dense form
+@pytest.mark.parametrize("K,dtype", [(2, BF), (2, FP), (3, BF), (5, FP), (8, BF)])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("batch", [1, 2, 3])
+def test_dense_groups_in_batches(T, K, dtype, transpose, batch):
+    """As many groups at a time as the scratch bound holds: empty groups at the batches' ends,
+    rows before the first group and after the last."""
+    sizes = [130, 0, 0, 301, 64, 0, 70]
+    w = random_weight(128, 192, K, 64, 601 + K, groups=7)
+    cut, at = cut_of(sizes, 5)
+    n = int(cut[-1]) + 9
+    x, x64 = rows_of(n, 128 if transpose else 192, dtype, 602)
+    with T.Context(0, scratch_bytes=batch * 128 * 192 * 2) as c:
+        y = torch.full((n, 192 if transpose else 128), 7.0, dtype=dtype, device=DEV)
+        c.grouped_linear(x, unaligned(T, w), at, transpose=transpose, out=y)
+        assert (y[:5] == 0).all() and (y[int(cut[-1]):] == 0).all()
+        check_groups(y, x64, w, cut, transpose, dtype)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("K", [5, 6, 7, 8])
+@pytest.mark.parametrize("per", [3, 12, 40, 90])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_general_decoder_of_groups(T, ctx, K, per, transpose):
+    w = random_weight(192, 128, K, 64, 611 + K, groups=3)
+    cut, at = cut_of([per, 0, per + 1], 2)
+    n = int(cut[-1]) + 3
+    x, x64 = rows_of(n, 192 if transpose else 128, FP, 612)
+    y = ctx.grouped_linear(x, on_gpu(T, w), at, transpose=transpose)
+    assert (y[:2] == 0).all() and (y[int(cut[-1]):] == 0).all()
+    check_groups(y, x64, w, cut, transpose, FP)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_one_launch_with_rows_of_no_group(T, ctx, dtype):
+    """Few enough rows that the first kernel writes y itself, the rows of no group included."""
+    w = random_weight(128, 256, 2, 128, 621, groups=3)
+    cut, at = cut_of([2, 0, 4], 3)
+    x, x64 = rows_of(12, 256, dtype, 622)
+    for repeat in range(2):
+        y = torch.full((12, 128), 7.0, dtype=dtype, device=DEV)
+        ctx.grouped_linear(x, on_gpu(T, w), at, out=y)
+        assert (y[:3] == 0).all() and (y[9:] == 0).all()
+        check_groups(y, x64, w, cut, False, dtype)
+
+
+# ---- long rows ----
+@pytest.mark.parametrize("cols,had", [(4096 + 128, 128), (16384 + 64, 64), (16384 + 4096 + 128, 128)])
+@pytest.mark.parametrize("n", [2, 9, 40])
+def test_long_rows(T, ctx, cols, had, n):
+    """Rows of x that a workgroup transforms in several rounds, and past 16,384 columns twice."""
+    w = random_weight(128, cols, 2, had, 631)
+    m = dense(w)
+    x, x64 = rows_of(n, cols, BF, 632)
+    check(ctx.linear(x, on_gpu(T, w)), x64 @ m.T, spread_of(x64, m), inner_of(True, BF))
+    w = random_weight(cols, 128, 2, had, 633)
+    m = dense(w).T
+    x, x64 = rows_of(n, cols, FP, 634)
+    y = ctx.linear(x, on_gpu(T, w), transpose=True)
+    check(y, x64 @ m.T, spread_of(x64, m), inner_of(True, FP))
+
+
+# ---- the decoded forms by their own bound ----
+@pytest.mark.parametrize("n,rows,cols,K,had,codebook", [
+    (1, 256, 1152, 1, 128, "mul1"), (15, 384, 2176, 4, 128, "mcg"), (17, 640, 256, 3, 128, "3inst"),
+    (40, 192, 320, 2, 64, "mul1"), (65, 128, 1152, 3, 128, "mul1"), (300, 640, 576, 2, 64, "mcg"),
+    (512, 128, 256, 4, 128, "mul1")])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_decoded_forms_round_the_activations_only(T, n, rows, cols, K, had, codebook, dtype):
+    w = random_weight(rows, cols, K, had, 641 + n)
+    m = dense(w, codebook)
+    x, x64 = rows_of(n, cols, dtype, 642)
+    with T.Context(0) as c:
+        c.set_codebook_kind(codebook)
+        check(c.linear(x, on_gpu(T, w)), x64 @ m.T, spread_of(x64, m), inner_of(True, dtype))
+        if n <= 256:
+            x, x64 = rows_of(n, rows, dtype, 643)
+            y = c.linear(x, on_gpu(T, w), transpose=True)
+            check(y, x64 @ m, spread_of(x64, m.T), inner_of(True, dtype))
+        torch.cuda.synchronize()
+
+
 # ---- many adapters ----
 def test_many_adapters(T, ctx):
     """Past half of the largest count, most of them without rows."""
