@@ -99,7 +99,9 @@ const char *exl3_last_error(const exl3_ctx *ctx);
  * Change the stream later calls enqueue on (the caller still owns it).  The new
  * stream is made to wait (through an event, without blocking the host) for the
  * work already enqueued on the old one, since that work may still use the
- * context's buffers.  Errors: EXL3_EINVAL, EXL3_EHIP.
+ * context's buffers.  A stream that is capturing cannot wait for work outside its
+ * capture: it is taken if the old stream is idle, and refused otherwise
+ * (EXL3_EINVAL; the capture goes on).  Errors: EXL3_EINVAL, EXL3_EHIP.
  */
 int exl3_ctx_set_stream(exl3_ctx *ctx, void *hip_stream);
 
@@ -434,8 +436,8 @@ typedef struct {
  * finite values; other rows are not affected.  Results do not depend on
  * scheduling.  n may be 0; at most 2^24 rows.
  * Asynchronous.  The context's workspace grows on demand: to capture the call
- * in a graph, make a call with the same arguments on the same stream first
- * (a growth during capture is refused with EXL3_ENOMEM).  Workspaces are kept
+ * in a graph, make a call with the same arguments first and wait for it (a
+ * growth during capture is refused with EXL3_ENOMEM).  Workspaces are kept
  * until the context is destroyed, so a captured graph stays valid until then;
  * its replays use the context's workspace and are ordered against the context's
  * other calls by the caller.

@@ -1217,6 +1217,29 @@ int exl3_ctx_set_stream(exl3_ctx *ctx, void *hip_stream) {
     // buffers: the new stream waits for it (no host synchronization)
     int rc;
     if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    // a stream that is capturing cannot wait for an event from outside the capture
+    // (the attempt would break the capture off): there is nothing to wait for if the
+    // old stream is idle
+    auto capturing = [](hipStream_t q) {
+        hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+        if (hipStreamIsCapturing(q, &st) != hipSuccess) (void)hipGetLastError();
+        return st == hipStreamCaptureStatusActive;
+    };
+    if (capturing(s) && !capturing(ctx->stream)) {
+        // (asking would break off a capture of the thread in the stricter modes)
+        hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+        EXL3_HIP(ctx, hipThreadExchangeStreamCaptureMode(&mode));
+        const hipError_t idle = hipStreamQuery(ctx->stream);
+        (void)hipThreadExchangeStreamCaptureMode(&mode);
+        if (idle != hipSuccess) {
+            (void)hipGetLastError();
+            return fail(ctx, EXL3_EINVAL,
+                        "the new stream is capturing and the old one has work left: wait for it "
+                        "before the capture begins");
+        }
+        ctx->stream = s;
+        return EXL3_OK;
+    }
     if (!ctx->ev_switch)
         EXL3_HIP(ctx, hipEventCreateWithFlags(&ctx->ev_switch, hipEventDisableTiming));
     EXL3_HIP(ctx, hipEventRecord(ctx->ev_switch, ctx->stream));
