@@ -19,7 +19,7 @@ __device__ __forceinline__ uint32_t parity16(uint32_t v) { return __popc(v) & 1u
 //      them by H_64 over their columns: entry (c, n) is (-1)^popcount(c & n).
 //      For HB = 128 the halves' sum and difference follow.
 //   2. The result, sums of HB levels, passes through shared memory column by
-//      column as binary16: for bfloat16 weights rounded to it (2^-12 of each,
+//      column as binary16: for bfloat16 weights rounded to it (at most 2^-11 of each,
 //      an eighth of what the final rounding takes), for binary16 weights in two
 //      parts, the rounded value and the rest, so that the weights are rounded
 //      once.  The codebooks' levels are below 4 and their sums below 2^9; a
@@ -219,6 +219,8 @@ dense_kernel(const uint32_t *__restrict__ packed, Levels lv, int rows, int cols,
 }
 
 // The exponent of the largest of each group's k factors (a workgroup a group).
+// Latency bounds it: 3 us for 4,096 factors; found in every workgroup of
+// dense_kernel instead, beside its other loads, it lengthened that by as much.
 __global__ void __launch_bounds__(512)
 inner_kernel(const float *__restrict__ factors, int k, int32_t *__restrict__ inner) {
     __shared__ uint32_t wave_big[8];

@@ -5,9 +5,10 @@
 // W = diag(su) H_l (scale C) H_r diag(sv) with C the codes' levels, so
 //   y = scale / had * su (H_l (C x')),   x' = H_r (sv x)
 // (H here without its factor 1 / sqrt(had), which enters twice).  x' comes from
-// rotate_kernel, C x' from the codes in coded_rows_kernel, which also takes the
-// left transform and the factors, or for more rows in coded_tiles_kernel, after
-// which finish_kernel takes them.
+// rotate_kernel, C x' from the codes in coded_rows_kernel or, for more rows, in
+// coded_tiles_kernel.  The left transform and the factors are finish_kernel's; the
+// smallest calls take them in coded_rows_kernel, and those whose columns are not
+// split in coded_tiles_kernel.
 #include "coded.h"
 
 namespace exl3 {
@@ -20,8 +21,8 @@ namespace {
 // are transformed a second time).  x' is held in binary16, whose products with
 // the levels (binary16 themselves) the matrix instruction sums in binary32.  The
 // row's scale is the power of two that takes its largest magnitude into
-// [2^13, 2^14): rounding then costs 2^-12 of each value down to 2^-27 of the
-// largest, whatever the range of the activations (bfloat16's is far wider than
+// [2^13, 2^14): rounding then costs at most 2^-11 of each value down to 2^-27 of
+// the largest, whatever the range of the activations (bfloat16's is far wider than
 // binary16's).  A row with a NaN or an infinity becomes NaN throughout.  8,200
 // rows of 2,048 columns: 16 us, 4.2 TB/s of both sides, near a copy's 4.7.
 constexpr int kKeep = 4;
@@ -199,8 +200,10 @@ __device__ __forceinline__ void finish_row(float (&z)[8], float f, const float *
 // workgroup stores its sums past its die's cache, waits until they are there,
 // and counts itself, and the last of a block reads all sums, in the order of the
 // splits, and finishes the rows of y.  One launch in place of three: 8.3 us
-// for one row and 1024 x 4096 (three took 15.3); with more workgroups than compute
-// units the late finish costs more than the launches.
+// for one row and 1024 x 4096 (three took 15.3).  With more workgroups than compute
+// units a launch of its own costs less than one tile a workgroup, its stores past the
+// die's cache and the late finish do: 12288 x 4096, K = 4, in one launch 23.7 us, in
+// two 15.6; 64 rows of 64 experts of 1408 x 2048 51 and 33.
 constexpr int kUnit = 256, kOwn = 8;
 constexpr int kOwnPitch = kUnit * 2 + 16;        // bytes of a row of a wave's own x'
 
