@@ -442,7 +442,8 @@ typedef struct {
  * its replays use the context's workspace and are ordered against the context's
  * other calls by the caller.
  * Errors: EXL3_EINVAL, EXL3_EUNSUPPORTED, EXL3_ENOMEM (also when one dense
- * matrix does not fit the context's scratch bound), EXL3_EHIP.
+ * matrix does not fit the context's scratch bound, which limits the dense weights
+ * written at a time and nothing else of the workspace), EXL3_EHIP.
  */
 int exl3_linear(exl3_ctx *ctx, const exl3_weight *w, int transpose, const void *x, int64_t ldx,
                 int64_t n, int dtype, void *y, int64_t ldy);
