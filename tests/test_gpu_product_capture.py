@@ -14,17 +14,21 @@ def T():
     return T
 
 
+@pytest.mark.parametrize("first", ["side", "default"])
 @pytest.mark.parametrize("n", [2, 40, 600])
-def test_a_capture_on_torchs_own_stream(T, n):
+def test_a_capture_on_torchs_own_stream(T, n, first):
     """Warmed up on one stream, captured on the one that torch takes, used on the first again."""
     w = on_gpu(T, random_weight(256, 384, 2, 128, 701))
     x, _ = rows_of(n, 384, BF, 702)
     with T.Context(0) as c, T.Context(0) as other:
-        side = torch.cuda.Stream()
-        side.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(side):
+        if first == "side":
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                c.linear(x, w)
+            torch.cuda.current_stream().wait_stream(side)
+        else:
             c.linear(x, w)
-        torch.cuda.current_stream().wait_stream(side)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             y = c.linear(x, w)
