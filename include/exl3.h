@@ -504,6 +504,116 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
                                  int64_t ldx, int64_t n, int dtype, void *dx, int64_t lddx,
                                  void *da, void *db);
 
+/*
+ * ---- 8-bit blocks ----
+ *
+ * Codes in 8-bit floating point (e4m3 without infinities, largest value 448) with
+ * a binary32 scale for each block: 128 consecutive elements of a row of
+ * activations, 128 x 128 elements of a matrix; a block at an edge is smaller.  A
+ * code stands for scale * e4m3.  Written here, a block of largest magnitude a has
+ * the scale max(a / 448, 2^-126), its codes are value / scale (rounded to binary32)
+ * rounded to nearest, ties to even; a block that holds an infinity or a NaN has the
+ * scale and all codes NaN.
+ */
+
+/* Rows of activations, `width` elements each.
+ *   q      [n][ldq] codes, 16-byte aligned; ldq a multiple of 128, at least width.
+ *          Bytes from width to the next multiple of 128 belong to the last block:
+ *          written as zeros, and read, where they must be zero.
+ *   scale  float [blocks][lds], blocks = width / 128 rounded up: the scale of row
+ *          t's block b is scale[b * lds + t]; lds at least n */
+typedef struct {
+    uint8_t *q;
+    float *scale;
+    int64_t ldq, lds;
+} exl3_block_rows;
+
+/* A matrix W [rows][cols] of codes, or one after the other for `groups` (experts).
+ *   q      [groups][rows][ldq] codes, 16-byte aligned; ldq a multiple of 128, at
+ *          least cols.  Bytes from cols to the next multiple of 128 are read and
+ *          must not be NaN (0x7F, 0xFF).
+ *   scale  float [groups][rows / 128][cols / 128], both rounded up
+ * rows and cols 1 .. 2^20, groups 1 .. 65535. */
+typedef struct {
+    const uint8_t *q;
+    const float *scale;
+    int groups, rows, cols;
+    int64_t ldq;
+} exl3_block_weight;
+
+/* Rows of x [n][cols] (EXL3_BF16 or EXL3_F16, rows ldx elements apart) as blocks.
+ * Asynchronous; allocates nothing.  Errors: EXL3_EINVAL, EXL3_EHIP. */
+int exl3_block_quantize(exl3_ctx *ctx, const void *x, int64_t ldx, int64_t n, int cols, int dtype,
+                        const exl3_block_rows *out);
+
+/* A matrix w [rows][cols] (EXL3_F32, EXL3_BF16 or EXL3_F16, rows ldw elements apart)
+ * as blocks of 128 x 128: q [rows][ldq] and scale as in exl3_block_weight, bytes past
+ * cols up to the next multiple of 128 zero.  Asynchronous; allocates nothing. */
+int exl3_block_quantize_weight(exl3_ctx *ctx, const void *w, int64_t ldw, int rows, int cols,
+                               int dtype, uint8_t *q, int64_t ldq, float *scale);
+
+/*
+ * Root-mean-square norm of s = x + residual (or of x):
+ *   y_t = s_t / sqrt(mean(s_t^2) + eps) * gain
+ * computed in binary32 from the unrounded s (in binary64 where a row's squares leave
+ * binary32's range).
+ *   x, residual  [n][cols] of `dtype` (EXL3_BF16 or EXL3_F16), rows ldx and ldr
+ *                elements apart; residual may be null
+ *   gain         [cols], of type gain_dtype: EXL3_F32, or dtype
+ *   y            [n][cols] of `dtype`, rows ldy apart; or null, with
+ *   blocks       y as blocks instead (null with y)
+ *   sum          s rounded to `dtype`, rows ldsum apart, or null; with a residual only
+ * y and sum may each be x or residual itself (one address and one pitch), but share
+ * no element with either otherwise, nor with one another.  eps >= 0 and finite; a row
+ * of zeros at eps = 0 gives NaN, as the formula does.  cols 1 .. 2^20, n 0 .. 2^24.
+ * Asynchronous; allocates nothing.  Errors: EXL3_EINVAL, EXL3_EHIP.
+ */
+int exl3_rms_norm(exl3_ctx *ctx, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                  const void *gain, int gain_dtype, float eps, int64_t n, int cols, int dtype,
+                  void *y, int64_t ldy, const exl3_block_rows *blocks, void *sum, int64_t ldsum);
+
+/*
+ * Its gradients from dy, the gradient of y (blocks pass it straight through), and ds,
+ * the gradient of the sum, or null:
+ *   dx_t  = ds_t + r_t (dy_t gain - u_t mean(dy_t gain u_t)),  u_t = s_t r_t,
+ *           r_t = 1 / sqrt(mean(s_t^2) + eps): the gradient of x and of the residual
+ *   dgain = sum over t of dy_t u_t
+ *   s      [n][cols]: what was normalised (the stored sum, or x)
+ *   dx     [n][cols] of `dtype`, or null; it may be dy or ds itself
+ *   dgain  [cols] of gain's type, or null; its sums are binary32, in an order that does
+ *          not depend on scheduling
+ * Asynchronous; the context's workspace grows on demand as in exl3_linear.
+ */
+int exl3_rms_norm_backward(exl3_ctx *ctx, const void *dy, int64_t lddy, const void *ds,
+                           int64_t ldds, const void *s, int64_t lds, const void *gain,
+                           int gain_dtype, float eps, int64_t n, int cols, int dtype, void *dx,
+                           int64_t lddx, void *dgain);
+
+/*
+ * y = x W^T (transpose == 0), or y = x W (transpose != 0: the input gradient of the
+ * former) with W in 8-bit blocks, groups = 1.
+ *   x        [n][in] of `dtype` (EXL3_BF16 or EXL3_F16), rows ldx elements apart,
+ *            written as blocks in the call; in = cols, or rows when transposed
+ *   xblocks  x as blocks instead of x (which is then null); exactly one of both
+ *   y        [n][out] of `dtype`, rows ldy elements apart; shares no element with x
+ * The products of a block are summed by the matrix units in binary32, the blocks'
+ * sums times their two scales in binary32, and the result is rounded once.  A row of x
+ * that holds NaN or an infinity gives a row of NaN; other rows are not affected.  Results do not
+ * depend on scheduling.  n may be 0; at most 2^24 rows.
+ * Asynchronous; capture, workspace and errors as in exl3_linear.
+ */
+int exl3_block_linear(exl3_ctx *ctx, const exl3_block_weight *w, int transpose, const void *x,
+                      int64_t ldx, const exl3_block_rows *xblocks, int64_t n, int dtype, void *y,
+                      int64_t ldy);
+
+/* The same with a matrix per group (expert): rows offsets[e] .. offsets[e+1]-1 of x are
+ * multiplied by matrix e.  offsets as in exl3_grouped_linear: rows of no group give
+ * rows of zeros. */
+int exl3_block_grouped_linear(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *offsets,
+                              int transpose, const void *x, int64_t ldx,
+                              const exl3_block_rows *xblocks, int64_t n, int dtype, void *y,
+                              int64_t ldy);
+
 /* Kernel kinds for exl3_ctx_read_timing. */
 enum {
     EXL3_KERNEL_FWD1 = 0,        /* forward pass 1 (rotated input, free start) */
@@ -519,9 +629,13 @@ enum {
                                     on the context's stream) */
     EXL3_KERNEL_CHANNEL = 7,     /* out-channel normalization (tile count 0) */
     EXL3_KERNEL_DECODE = 8,      /* exl3_decode_tiles */
-    EXL3_KERNEL_PRODUCT = 9      /* products with coded weights (one record a
+    EXL3_KERNEL_PRODUCT = 9,     /* products with coded weights (one record a
                                     call, its launches together; tiles: the
                                     weights' tiles) */
+    EXL3_KERNEL_BLOCK = 10,      /* products in 8-bit blocks (one record a call;
+                                    tiles: the weights' blocks) */
+    EXL3_KERNEL_NORM = 11        /* norm, its backward pass and the writing of
+                                    blocks (one record a call; tile count 0) */
 };
 
 /*

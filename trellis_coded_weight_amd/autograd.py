@@ -1,4 +1,4 @@
-"""Products with coded weights as differentiable functions.
+"""Products with coded weights, products in 8-bit blocks and the norm as differentiable functions.
 
 The coded matrix is frozen: gradients go to the activations and to the adapters' matrices.
 Activations may have any leading dimensions, [..., cols]; the row arguments (ids, offsets)
@@ -10,9 +10,11 @@ context each).
 """
 from __future__ import annotations
 
+from typing import Optional
+
 import torch
 
-from .binding import Adapters, CodedWeight, Context
+from .binding import Adapters, BlockWeight, CodedWeight, Context
 
 
 def _rows(x: torch.Tensor) -> torch.Tensor:
@@ -92,3 +94,76 @@ def coded_adapter_linear(context: Context, x: torch.Tensor, weight: CodedWeight,
         raise ValueError("alpha requires a gradient, which is not computed: pass alpha.detach()")
     y = _AdapterLinear.apply(_rows(x), A, B, context, weight, alpha, ids.reshape(-1))
     return y.reshape(x.shape[:-1] + (weight.rows,))
+
+
+class _BlockLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, context, weight, offsets):
+        ctx.args = context, weight
+        ctx.save_for_backward(offsets, weight.q, weight.scale)
+        if offsets is None:
+            return context.block_linear(x, weight)
+        return context.block_grouped_linear(x, weight, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        context, weight = ctx.args
+        offsets = ctx.saved_tensors[0]
+        if offsets is None:
+            dx = context.block_linear(dy, weight, transpose=True)
+        else:
+            dx = context.block_grouped_linear(dy, weight, offsets, transpose=True)
+        return dx, None, None, None
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gain, residual, context, eps):
+        ctx.set_materialize_grads(False)
+        ctx.args = context, eps
+        if residual is None:
+            ctx.save_for_backward(x, gain)
+            return context.rms_norm(x, gain, eps)
+        y, total = context.rms_norm(x, gain, eps, residual=residual)
+        ctx.save_for_backward(total, gain)
+        return y, total
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, ds=None):
+        context, eps = ctx.args
+        s, gain = ctx.saved_tensors
+        want_x, want_gain, want_residual = ctx.needs_input_grad[:3]
+        dx = dgain = None
+        if dy is None:
+            dx = ds
+            dgain = torch.zeros_like(gain) if want_gain else None
+        else:
+            dx, dgain = context.rms_norm_backward(dy, s, gain, eps, ds=ds,
+                                                  want_dx=want_x or want_residual,
+                                                  want_dgain=want_gain)
+        return (dx if want_x else None, dgain, dx if want_residual else None, None, None)
+
+
+def block_linear(context: Context, x: torch.Tensor, weight: BlockWeight) -> torch.Tensor:
+    """x [..., cols] -> x W^T [..., rows] with W, and x within the call, in 8-bit blocks.  The
+    gradient of x is dy W with dy in 8-bit blocks; x's own rounding is passed straight through."""
+    y = _BlockLinear.apply(_rows(x), context, weight, None)
+    return y.reshape(x.shape[:-1] + (weight.rows,))
+
+
+def block_grouped_linear(context: Context, x: torch.Tensor, weight: BlockWeight,
+                         offsets: torch.Tensor) -> torch.Tensor:
+    """x [n, cols], sorted by group (expert) -> [n, rows]; offsets int32 [groups + 1]."""
+    return _BlockLinear.apply(x, context, weight, offsets)
+
+
+def rms_norm(context: Context, x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None):
+    """Root-mean-square norm of s = x + residual over the last dimension, times gain: y, or
+    (y, s) with a residual.  Differentiable in x, gain and the residual."""
+    if residual is None:
+        return _RmsNorm.apply(_rows(x), gain, None, context, eps).reshape(x.shape)
+    y, total = _RmsNorm.apply(_rows(x), gain, _rows(residual), context, eps)
+    return y.reshape(x.shape), total.reshape(x.shape)

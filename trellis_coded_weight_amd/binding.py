@@ -37,10 +37,12 @@ EXPORTED = [
     "exl3_quantize_matrix_ldlq", "exl3_quantize_matrix_grid", "exl3_quantize_matrix_f16", "exl3_scratch_per_tile",
     "exl3_ctx_set_timing", "exl3_ctx_read_timing",
     "exl3_linear", "exl3_grouped_linear", "exl3_adapter_linear", "exl3_adapter_linear_backward",
+    "exl3_block_quantize", "exl3_block_quantize_weight", "exl3_rms_norm", "exl3_rms_norm_backward",
+    "exl3_block_linear", "exl3_block_grouped_linear",
 ]
 CODEBOOK_KINDS = {"mul1": 0, "mcg": 1, "3inst": 2}
 KERNEL_KINDS = {"fwd1": 0, "fwd2": 1, "tb1": 2, "tb2": 3, "regularize": 4, "fwd_side": 5,
-                "fwd_cost": 6, "channel": 7, "decode": 8, "product": 9}
+                "fwd_cost": 6, "channel": 7, "decode": 8, "product": 9, "block": 10, "norm": 11}
 
 
 class Exl3Error(RuntimeError):
@@ -70,6 +72,16 @@ class _Weight(ctypes.Structure):
 class _Adapters(ctypes.Structure):
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("alpha", ctypes.c_void_p),
                 ("count", ctypes.c_int), ("rank", ctypes.c_int)]
+
+
+class _BlockRows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+                ("lds", ctypes.c_int64)]
+
+
+class _BlockWeight(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("groups", ctypes.c_int),
+                ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("ldq", ctypes.c_int64)]
 
 
 GRID_PAGES = (0.1, 1.9, 0.1, 2, 0.075, 0.025, 0.01)
@@ -159,6 +171,21 @@ def load_library():
     lib.exl3_adapter_linear_backward.restype = i32
     lib.exl3_adapter_linear_backward.argtypes = [vp, wp, ap, vp, vp, i64, vp, i64, i64, i32, vp,
                                                  i64, vp, vp]
+    bp, wb = ctypes.POINTER(_BlockRows), ctypes.POINTER(_BlockWeight)
+    lib.exl3_block_quantize.restype = i32
+    lib.exl3_block_quantize.argtypes = [vp, vp, i64, i64, i32, i32, bp]
+    lib.exl3_block_quantize_weight.restype = i32
+    lib.exl3_block_quantize_weight.argtypes = [vp, vp, i64, i32, i32, i32, vp, i64, vp]
+    lib.exl3_rms_norm.restype = i32
+    lib.exl3_rms_norm.argtypes = [vp, vp, i64, vp, i64, vp, i32, f32, i64, i32, i32, vp, i64, bp,
+                                  vp, i64]
+    lib.exl3_rms_norm_backward.restype = i32
+    lib.exl3_rms_norm_backward.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i32, f32, i64, i32,
+                                           i32, vp, i64, vp]
+    lib.exl3_block_linear.restype = i32
+    lib.exl3_block_linear.argtypes = [vp, wb, i32, vp, i64, bp, i64, i32, vp, i64]
+    lib.exl3_block_grouped_linear.restype = i32
+    lib.exl3_block_grouped_linear.argtypes = [vp, wb, vp, i32, vp, i64, bp, i64, i32, vp, i64]
     _lib = lib
     return lib
 
@@ -246,7 +273,129 @@ class Adapters:
         self._ref = ctypes.byref(self._c)
 
 
+BLOCK = 128                        # elements along a row that share a scale in 8-bit blocks
+_E4M3 = torch.float8_e4m3fn
+
+
+def _blocks(width: int) -> int:
+    return -(-width // BLOCK)
+
+
+class BlockRows:
+    """Rows of activations in 8-bit blocks: a code (e4m3) for each element and a scale for every
+    128 consecutive ones of a row; a code stands for scale * q.
+
+    q      float8_e4m3fn [n, cols]
+    scale  float32 [n, cols/128 rounded up]
+
+    Both attributes are views of the storage that products read: rows padded with zeros to whole
+    blocks, scales of one block of consecutive rows side by side.  Tensors that lie so already
+    (cols a multiple of 128, scale transposed) are kept, others copied."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor):
+        if not isinstance(q, torch.Tensor) or q.dim() != 2 or q.shape[1] < 1:
+            raise ValueError("q must be a tensor [n, cols]")
+        _need_e4m3(q, "q")
+        n, cols = q.shape
+        if not isinstance(scale, torch.Tensor) or scale.device != q.device:
+            raise ValueError("scale must be a tensor on q's device")
+        if scale.dtype != torch.float32 or tuple(scale.shape) != (n, _blocks(cols)):
+            raise ValueError("scale must be float32 %s, got %s %s" %
+                             ((n, _blocks(cols)), scale.dtype, tuple(scale.shape)))
+        if (cols % BLOCK or q.stride(1) != 1 or q.data_ptr() % 16 or
+                (n > 1 and (q.stride(0) < cols or q.stride(0) % BLOCK))):
+            q = _pad_codes(q)
+        ldq = q.stride(0) if n > 1 else BLOCK * _blocks(cols)
+        by_block = scale.t()
+        if (n > 1 and by_block.stride(1) != 1) or (by_block.shape[0] > 1 and
+                                                   by_block.stride(0) < n):
+            by_block = by_block.contiguous()
+        lds = by_block.stride(0) if by_block.shape[0] > 1 else max(n, 1)
+        self._set(q[:, :cols], by_block.t(), ldq, lds)
+
+    def _set(self, q, scale, ldq, lds):
+        self.q, self.scale, self.device = q, scale, q.device
+        self.n, self.cols = q.shape
+        self._c = _BlockRows(q.data_ptr(), scale.data_ptr(), ldq, lds)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def _empty(cls, n: int, cols: int, device) -> "BlockRows":
+        rows = cls.__new__(cls)
+        q = torch.empty(n, BLOCK * _blocks(cols), dtype=_E4M3, device=device)
+        scale = torch.empty(_blocks(cols), n, dtype=torch.float32, device=device)
+        rows._set(q[:, :cols], scale.t(), q.shape[1], max(n, 1))
+        return rows
+
+    def dequantize(self) -> torch.Tensor:
+        """The values [n, cols] in float32."""
+        return self.q.float() * self.scale.repeat_interleave(BLOCK, dim=1)[:, :self.cols]
+
+
+class BlockWeight:
+    """A matrix in 8-bit blocks, or one per group (expert): a code (e4m3) for each element and a
+    scale for every 128 x 128.
+
+    q      float8_e4m3fn [rows, cols], or [groups, rows, cols]
+    scale  float32 [rows/128, cols/128] rounded up, or [groups, ...]
+
+    Contiguous tensors with cols a multiple of 128 are kept, others copied once (q padded with
+    zeros to whole blocks); in-place changes to kept tensors show in later products."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor):
+        if not isinstance(q, torch.Tensor) or q.dim() not in (2, 3) or not q.numel():
+            raise ValueError("q must be a tensor [rows, cols] or [groups, rows, cols]")
+        _need_e4m3(q, "q")
+        lead = tuple(q.shape[:-2])
+        rows, cols = q.shape[-2:]
+        _need(scale.contiguous() if isinstance(scale, torch.Tensor) else scale, torch.float32,
+              lead + (_blocks(rows), _blocks(cols)), "scale")
+        if scale.device != q.device:
+            raise ValueError("scale must be on q's device")
+        if cols % BLOCK or not q.is_contiguous() or q.data_ptr() % 16:
+            q = _pad_codes(q)
+        scale = scale.contiguous()
+        self._set(q, scale, cols)
+
+    def _set(self, q, scale, cols):
+        self.grouped = q.dim() == 3
+        self.q, self.scale, self.device = q[..., :cols], scale, q.device
+        self.groups, self.rows, self.cols = q.shape[0] if self.grouped else 1, q.shape[-2], cols
+        self._c = _BlockWeight(q.data_ptr(), scale.data_ptr(), self.groups, self.rows, cols,
+                               q.shape[-1])
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def _of(cls, q, scale, cols) -> "BlockWeight":
+        """From codes in whole blocks of columns and their scales, both contiguous."""
+        weight = cls.__new__(cls)
+        weight._set(q, scale, cols)
+        return weight
+
+    def dequantize(self) -> torch.Tensor:
+        """The matrices in float32."""
+        s = self.scale.repeat_interleave(BLOCK, dim=-1).repeat_interleave(BLOCK, dim=-2)
+        return self.q.float() * s[..., :self.rows, :self.cols]
+
+
+def _need_e4m3(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.dtype != _E4M3:
+        raise ValueError("%s must be %s, got %s" % (name, _E4M3, t.dtype))
+
+
+def _pad_codes(q):
+    """q [..., cols] in whole blocks of columns, zeros behind the last."""
+    wide = torch.zeros(q.shape[:-1] + (BLOCK * _blocks(q.shape[-1]),), dtype=torch.uint8,
+                       device=q.device)
+    wide[..., :q.shape[-1]] = q.view(torch.uint8) if q.stride(-1) == 1 else \
+        q.contiguous().view(torch.uint8)
+    return wide.view(_E4M3)
+
+
 _ACT = {torch.bfloat16: EXL3_BF16, torch.float16: EXL3_F16}
+_FLOAT = {torch.float32: EXL3_F32, **_ACT}
 
 
 def _act_rows(t: torch.Tensor, width: int, name: str):
@@ -563,6 +712,184 @@ class Context:
             None if dx is None else dx.data_ptr(), weight.cols,
             None if dA is None else dA.data_ptr(), None if dB is None else dB.data_ptr()))
         return dx, dA, dB
+
+    # -- 8-bit blocks --
+    def block_quantize(self, x: torch.Tensor) -> BlockRows:
+        """x [n, cols] bfloat16 or float16, rows of any pitch, as 8-bit blocks."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be a tensor [n, cols]")
+        x, ldx = _act_rows(x, x.shape[1], "x")
+        out = BlockRows._empty(x.shape[0], x.shape[1], x.device)
+        self._sync_stream()
+        self._check(self.lib.exl3_block_quantize(self.handle, x.data_ptr(), ldx, x.shape[0],
+                                                 x.shape[1], _ACT[x.dtype], out._ref))
+        return out
+
+    def block_quantize_weight(self, w: torch.Tensor) -> BlockWeight:
+        """w [rows, cols] float32, bfloat16 or float16 as 8-bit blocks of 128 x 128; [groups, rows,
+        cols]: matrix by matrix."""
+        if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3) or not w.numel():
+            raise ValueError("w must be a tensor [rows, cols] or [groups, rows, cols]")
+        if not w.is_cuda:
+            raise ValueError("w must be a device tensor")
+        if w.dtype not in _FLOAT:
+            raise ValueError("w must be float32, bfloat16 or float16, got %s" % w.dtype)
+        rows, cols = w.shape[-2:]
+        lead = tuple(w.shape[:-2])
+        q = torch.empty(lead + (rows, BLOCK * _blocks(cols)), dtype=_E4M3, device=w.device)
+        scale = torch.empty(lead + (_blocks(rows), _blocks(cols)), dtype=torch.float32,
+                            device=w.device)
+        self._sync_stream()
+        for g in range(w.shape[0] if lead else 1):
+            one = w[g] if lead else w
+            if one.stride(1) != 1 or (rows > 1 and one.stride(0) < cols):
+                one = one.contiguous()
+            self._check(self.lib.exl3_block_quantize_weight(
+                self.handle, one.data_ptr(), one.stride(0) if rows > 1 else cols, rows, cols,
+                _FLOAT[w.dtype], (q[g] if lead else q).data_ptr(), q.shape[-1],
+                (scale[g] if lead else scale).data_ptr()))
+        return BlockWeight._of(q, scale, cols)
+
+    def block_weight(self, weight: CodedWeight) -> BlockWeight:
+        """A coded matrix (or one per group) decoded and written as 8-bit blocks: twice the bytes of
+        K = 4, and products at the 8-bit rate.  Reads the scales on the host."""
+        n = weight.rows // 16 * (weight.cols // 16)
+        parts = []
+        for g, scale in enumerate(weight.scale.tolist()):
+            def of(t):
+                return t[g] if weight.grouped else t
+            tiles = self.decode_tiles(of(weight.packed).reshape(n, 16 * weight.K), weight.K, scale)
+            parts.append(self.block_quantize_weight(
+                self.unregularize(tiles, weight.rows, weight.cols, of(weight.su), of(weight.sv),
+                                  weight.had_block)))
+        if not weight.grouped:
+            return parts[0]
+        return BlockWeight(torch.stack([p.q for p in parts]), torch.stack([p.scale for p in parts]))
+
+    def _gain(self, gain, x):
+        if not isinstance(gain, torch.Tensor) or gain.dtype not in (x.dtype, torch.float32):
+            raise ValueError("gain must be a %s or float32 tensor" % x.dtype)
+        _need(gain, gain.dtype, (x.shape[1],), "gain")
+        return _FLOAT[gain.dtype]
+
+    def rms_norm(self, x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None, blocks: bool = False,
+                 out: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None):
+        """Root-mean-square norm of s = x + residual: s / sqrt(mean(s^2) + eps) * gain over the
+        columns of x [n, cols] (bfloat16 or float16, rows of any pitch), as a tensor of the same
+        type or, with blocks, as BlockRows.  gain [cols], of x's type or float32.
+        Without a residual returns y, with one (y, s); s is rounded to x's type after the norm has
+        used it.  out, sum_out: tensors to write; each may be x or residual itself."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be a tensor [n, cols]")
+        x, ldx = _act_rows(x, x.shape[1], "x")
+        n, cols = x.shape
+        gain_dtype = self._gain(gain, x)
+        ldr = ldsum = ldy = 0
+        total = None
+        if residual is not None:
+            residual, ldr = _act_rows(residual, cols, "residual")
+            if residual.shape != x.shape or residual.dtype != x.dtype:
+                raise ValueError("residual must be %s %s" % (x.dtype, tuple(x.shape)))
+            total, ldsum = _out_rows(sum_out, n, cols, x, "sum_out")
+        elif sum_out is not None:
+            raise ValueError("sum_out without a residual")
+        if blocks:
+            if out is not None:
+                raise ValueError("out with blocks")
+            y = BlockRows._empty(n, cols, x.device)
+        else:
+            y, ldy = _out_rows(out, n, cols, x, "out")
+        self._sync_stream()
+        self._check(self.lib.exl3_rms_norm(
+            self.handle, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
+            gain.data_ptr(), gain_dtype, float(eps), n, cols, _ACT[x.dtype],
+            None if blocks else y.data_ptr(), ldy, y._ref if blocks else None,
+            None if total is None else total.data_ptr(), ldsum))
+        return y if residual is None else (y, total)
+
+    def rms_norm_backward(self, dy: torch.Tensor, s: torch.Tensor, gain: torch.Tensor,
+                          eps: float = 1e-6, ds: Optional[torch.Tensor] = None,
+                          want_dx: bool = True, want_dgain: bool = True):
+        """Gradients (dx, dgain) of rms_norm at s, what was normalised (its second result, or x),
+        for dy and, where the sum is used further, its gradient ds.  dx is the gradient of x and
+        of the residual alike; dgain is of gain's type.  None for what is not wanted."""
+        if not isinstance(s, torch.Tensor) or s.dim() != 2:
+            raise ValueError("s must be a tensor [n, cols]")
+        s, lds = _act_rows(s, s.shape[1], "s")
+        n, cols = s.shape
+        dy, lddy = _act_rows(dy, cols, "dy")
+        gain_dtype = self._gain(gain, s)
+        ldds = 0
+        if ds is not None:
+            ds, ldds = _act_rows(ds, cols, "ds")
+        for t, name in ((dy, "dy"), (ds, "ds")):
+            if t is not None and (t.shape != s.shape or t.dtype != s.dtype):
+                raise ValueError("%s must be %s %s" % (name, s.dtype, tuple(s.shape)))
+        dx = torch.empty(n, cols, dtype=s.dtype, device=s.device) if want_dx else None
+        dgain = torch.empty_like(gain) if want_dgain else None
+        self._sync_stream()
+        self._check(self.lib.exl3_rms_norm_backward(
+            self.handle, dy.data_ptr(), lddy, None if ds is None else ds.data_ptr(), ldds,
+            s.data_ptr(), lds, gain.data_ptr(), gain_dtype, float(eps), n, cols, _ACT[s.dtype],
+            None if dx is None else dx.data_ptr(), cols,
+            None if dgain is None else dgain.data_ptr()))
+        return dx, dgain
+
+    def _block_input(self, x, width, out, dtype):
+        """(x or None, its pitch, blocks or None, n, type of the result)."""
+        if isinstance(x, BlockRows):
+            if x.cols != width:
+                raise ValueError("x must have %d columns, got %d" % (width, x.cols))
+            if dtype is None:
+                dtype = out.dtype if isinstance(out, torch.Tensor) else torch.bfloat16
+            if dtype not in _ACT:
+                raise ValueError("dtype must be bfloat16 or float16, got %s" % dtype)
+            return None, 0, x, x.n, dtype
+        x, ldx = _act_rows(x, width, "x")
+        if dtype is not None and dtype != x.dtype:
+            raise ValueError("dtype must be that of x, %s" % x.dtype)
+        return x, ldx, None, x.shape[0], x.dtype
+
+    def block_linear(self, x, weight: BlockWeight, transpose: bool = False,
+                     out: Optional[torch.Tensor] = None, dtype=None) -> torch.Tensor:
+        """x [n, cols] -> x W^T [n, rows]; transpose: x [n, rows] -> x W [n, cols] (the input
+        gradient of the former).  x: bfloat16 or float16, rows of any pitch, which the call writes
+        as 8-bit blocks first; or BlockRows, with dtype the type of the result (that of out, or
+        bfloat16)."""
+        if weight.grouped and weight.groups != 1:
+            raise ValueError("a weight of %d groups: use block_grouped_linear" % weight.groups)
+        return self._block_product(x, weight, None, transpose, out, dtype)
+
+    def block_grouped_linear(self, x, weight: BlockWeight, offsets: torch.Tensor,
+                             transpose: bool = False, out: Optional[torch.Tensor] = None,
+                             dtype=None) -> torch.Tensor:
+        """block_linear with a matrix per group (expert): rows offsets[e] .. offsets[e + 1] - 1 of
+        x are multiplied by matrix e; offsets int32 [groups + 1] on the device.  Rows of no group
+        give zeros."""
+        _need(offsets, torch.int32, (weight.groups + 1,), "offsets")
+        return self._block_product(x, weight, offsets, transpose, out, dtype)
+
+    def _block_product(self, x, weight, offsets, transpose, out, dtype):
+        wide, tall = (weight.rows, weight.cols) if transpose else (weight.cols, weight.rows)
+        x, ldx, blocks, n, dtype = self._block_input(x, wide, out, dtype)
+        device = blocks.device if x is None else x.device
+        if out is None:
+            y, ldy = torch.empty(n, tall, dtype=dtype, device=device), tall
+        else:
+            y, ldy = _out_rows(out, n, tall, torch.empty(0, dtype=dtype, device=device), "out")
+        ptr = None if x is None else x.data_ptr()
+        ref = None if blocks is None else blocks._ref
+        self._sync_stream()
+        if offsets is None:
+            rc = self.lib.exl3_block_linear(self.handle, weight._ref, int(transpose), ptr, ldx, ref,
+                                            n, _ACT[dtype], y.data_ptr(), ldy)
+        else:
+            rc = self.lib.exl3_block_grouped_linear(
+                self.handle, weight._ref, offsets.data_ptr(), int(transpose), ptr, ldx, ref, n,
+                _ACT[dtype], y.data_ptr(), ldy)
+        self._check(rc)
+        return y
 
     def quantize_matrix(self, w: torch.Tensor, K: int, su: torch.Tensor, sv: torch.Tensor,
                         had_block: int = 128,

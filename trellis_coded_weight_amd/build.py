@@ -18,7 +18,8 @@ LIB = os.path.join(OUT_DIR, "libexl3_gfx950.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.hip", "viterbi_fwd.hip", "viterbi_fwd_f16.hip", "traceback.hip", "regularize.hip",
-           "channel.hip", "ldlq.hip", "linear.hip", "dense.hip", "adapters.hip", "codebook.cpp"]
+           "channel.hip", "ldlq.hip", "linear.hip", "dense.hip", "adapters.hip",
+           "norm.hip", "blocks.hip", "codebook.cpp"]
 # Matrix instructions on vector registers throughout: where a kernel has more than
 # 256 registers a lane, the compiler otherwise moves accumulators to and from the
 # accumulation registers in the product's inner loop.

@@ -13,6 +13,7 @@
 #include "exl3.h"
 #include "exl3_internal.h"
 #include "coded.h"
+#include "blocks.h"
 
 #include <algorithm>
 #include <cmath>
@@ -2151,6 +2152,381 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
     const int id = open_timed(ctx, EXL3_KERNEL_PRODUCT, (int64_t)(w->rows / 16) * (w->cols / 16));
     return end_timed(ctx, id, run_backward(ctx, p, aa, b, x, ldx, da, db));
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- 8-bit blocks ----
+
+// Whether two ranges of bytes share one.
+bool spans_meet(const void *p, size_t np, const void *q, size_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return np && nq && a < b + nq && b < a + np;
+}
+
+// The bytes a matrix of n rows spans.
+size_t rows_span(int64_t ld, int64_t n, int width) {
+    return n ? ((size_t)(n - 1) * (size_t)ld + (size_t)width) * 2 : 0;
+}
+
+int check_side(exl3_ctx *ctx, int64_t v, const char *name) {
+    if (v < 1 || v > kMaxSide)
+        return fail(ctx, EXL3_EINVAL, "%s = %lld (1..%d)", name, (long long)v, kMaxSide);
+    return EXL3_OK;
+}
+
+int check_blocks(exl3_ctx *ctx, const exl3_block_rows *b, int64_t n, int width, const char *name,
+                 exl3::BlockRowsArgs *out) {
+    if (!b) return fail(ctx, EXL3_EINVAL, "null %s", name);
+    *out = exl3::BlockRowsArgs{b->q, b->scale, b->ldq, b->lds};
+    if (n == 0) return EXL3_OK;
+    const int blocks = exl3::blocks_of(width);
+    if (!b->q || !b->scale) return fail(ctx, EXL3_EINVAL, "%s: null q or scale", name);
+    if (b->ldq < width || b->ldq % exl3::kBlock || b->ldq > ((int64_t)1 << 40))
+        return fail(ctx, EXL3_EINVAL, "%s: rows of %d codes %lld apart (a multiple of %d)", name,
+                    width, (long long)b->ldq, exl3::kBlock);
+    if (b->lds < n || b->lds > ((int64_t)1 << 40))
+        return fail(ctx, EXL3_EINVAL, "%s: scales of %lld rows %lld apart", name, (long long)n,
+                    (long long)b->lds);
+    if (reinterpret_cast<uintptr_t>(b->q) % 16 || reinterpret_cast<uintptr_t>(b->scale) % 4)
+        return fail(ctx, EXL3_EINVAL, "%s: q (%p) is not 16-byte or scale (%p) not 4-byte aligned",
+                    name, static_cast<void *>(b->q), static_cast<void *>(b->scale));
+    int rc;
+    if ((rc = check_span(ctx, b->q, (size_t)(n - 1) * (size_t)b->ldq + (size_t)blocks * exl3::kBlock,
+                         "codes")) != EXL3_OK)
+        return rc;
+    return check_span(ctx, b->scale,
+                      ((size_t)(blocks - 1) * (size_t)b->lds + (size_t)n) * sizeof(float), "scales");
+}
+
+// The bytes that the codes and the scales of checked rows span.
+size_t codes_span(const exl3::BlockRowsArgs &b, int64_t n, int width) {
+    return n ? (size_t)(n - 1) * (size_t)b.ld + (size_t)exl3::blocks_of(width) * exl3::kBlock : 0;
+}
+size_t scales_span(const exl3::BlockRowsArgs &b, int64_t n, int width) {
+    return n ? ((size_t)(exl3::blocks_of(width) - 1) * (size_t)b.lds + (size_t)n) * sizeof(float)
+             : 0;
+}
+
+// Blocks as an output share nothing with `p` (np bytes) nor with one another.
+int check_apart(exl3_ctx *ctx, const exl3::BlockRowsArgs &b, int64_t n, int width, const void *p,
+                size_t np, const char *name) {
+    const size_t nq = codes_span(b, n, width), ns = scales_span(b, n, width);
+    if (spans_meet(b.q, nq, p, np) || spans_meet(b.scale, ns, p, np))
+        return fail(ctx, EXL3_EINVAL, "the blocks overlap %s", name);
+    if (spans_meet(b.q, nq, b.scale, ns))
+        return fail(ctx, EXL3_EINVAL, "the blocks' codes and scales overlap");
+    return EXL3_OK;
+}
+
+int check_gain(exl3_ctx *ctx, const void *gain, int gain_dtype, int dtype, int cols,
+               const char *name) {
+    if (gain_dtype != EXL3_F32 && gain_dtype != dtype)
+        return fail(ctx, EXL3_EINVAL, "gain dtype %d is neither EXL3_F32 nor the rows' (%d)",
+                    gain_dtype, dtype);
+    const size_t size = gain_dtype == EXL3_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(gain) % size)
+        return fail(ctx, EXL3_EINVAL, "%s (%p) is not aligned to its elements", name, gain);
+    return check_span(ctx, gain, (size_t)cols * size, name);
+}
+
+int check_norm(exl3_ctx *ctx, int64_t n, int cols, int dtype, float eps, const void *gain,
+               int gain_dtype) {
+    int rc;
+    if ((rc = check_product(ctx, n, dtype)) != EXL3_OK ||
+        (rc = check_side(ctx, cols, "cols")) != EXL3_OK)
+        return rc;
+    if (!(eps >= 0.0f) || !std::isfinite(eps))
+        return fail(ctx, EXL3_EINVAL, "eps = %g is negative or not finite", (double)eps);
+    if (!gain) return fail(ctx, EXL3_EINVAL, "null gain");
+    return check_gain(ctx, gain, gain_dtype, dtype, cols, "gain");
+}
+
+// An output may be the input itself, row for row, but overlap it in no other way.
+bool same_or_apart(const void *out, int64_t ldo, const void *in, int64_t ldi, int width, int64_t n) {
+    if (!out || !in || n == 0) return true;
+    return (out == in && (ldo == ldi || n == 1)) || !rows_overlap(out, ldo, width, in, ldi, width, n);
+}
+
+int check_block_weight(exl3_ctx *ctx, const exl3_block_weight *w, exl3::BlockWeightArgs *out) {
+    if (!w) return fail(ctx, EXL3_EINVAL, "null weight");
+    if (!w->q || !w->scale) return fail(ctx, EXL3_EINVAL, "null q or scale");
+    int rc;
+    if ((rc = check_side(ctx, w->rows, "rows")) != EXL3_OK ||
+        (rc = check_side(ctx, w->cols, "cols")) != EXL3_OK)
+        return rc;
+    if (w->groups < 1 || w->groups > kMaxGroups)
+        return fail(ctx, EXL3_EINVAL, "groups = %d (1..%d)", w->groups, kMaxGroups);
+    if (w->ldq < w->cols || w->ldq % exl3::kBlock || w->ldq > 2 * kMaxSide)
+        return fail(ctx, EXL3_EINVAL, "rows of %d codes %lld apart (a multiple of %d, at most %d)",
+                    w->cols, (long long)w->ldq, exl3::kBlock, 2 * kMaxSide);
+    if (reinterpret_cast<uintptr_t>(w->q) % 16 || reinterpret_cast<uintptr_t>(w->scale) % 4)
+        return fail(ctx, EXL3_EINVAL, "q (%p) is not 16-byte or scale (%p) not 4-byte aligned",
+                    static_cast<const void *>(w->q), static_cast<const void *>(w->scale));
+    const size_t g = (size_t)w->groups;
+    if ((rc = check_span(ctx, w->q, g * w->rows * (size_t)w->ldq, "q")) != EXL3_OK ||
+        (rc = check_span(ctx, w->scale,
+                         g * exl3::blocks_of(w->rows) * exl3::blocks_of(w->cols) * sizeof(float),
+                         "scale")) != EXL3_OK)
+        return rc;
+    *out = exl3::BlockWeightArgs{w->q, w->scale, w->groups, w->rows, w->cols, w->ldq};
+    return EXL3_OK;
+}
+
+int run_block_product(exl3_ctx *ctx, const exl3::BlockWeightArgs &w,
+                      const exl3::BlockProductArgs &a, const void *x, int64_t ldx, int in,
+                      bool bf16) {
+    if (x)
+        EXL3_HIP(ctx, exl3::launch_block_quantize(x, ldx, a.n, in, bf16, a.x, ctx->n_cu,
+                                                  ctx->stream));
+    EXL3_HIP(ctx, exl3::launch_block_gemm(w, a, bf16, ctx->n_cu, ctx->stream));
+    return EXL3_OK;
+}
+
+int block_linear_any(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *offsets,
+                     int transpose, const void *x, int64_t ldx, const exl3_block_rows *xb, int64_t n,
+                     int dtype, void *y, int64_t ldy) {
+    int rc;
+    exl3::BlockWeightArgs wa;
+    if ((rc = check_block_weight(ctx, w, &wa)) != EXL3_OK) return rc;
+    if ((rc = check_product(ctx, n, dtype)) != EXL3_OK) return rc;
+    const int in = transpose ? w->rows : w->cols, out = transpose ? w->cols : w->rows;
+    exl3::BlockProductArgs a{};
+    if (x && xb) return fail(ctx, EXL3_EINVAL, "both x and xblocks are given");
+    if (xb) {
+        if ((rc = check_blocks(ctx, xb, n, in, "xblocks", &a.x)) != EXL3_OK) return rc;
+    } else if ((rc = check_rows(ctx, x, ldx, n, in, "x")) != EXL3_OK) {
+        return rc;
+    }
+    if ((rc = check_rows(ctx, y, ldy, n, out, "y")) != EXL3_OK ||
+        (rc = check_span(ctx, offsets, ((size_t)w->groups + 1) * sizeof(int32_t), "offsets")) !=
+            EXL3_OK)
+        return rc;
+    if (n == 0) return EXL3_OK;
+    if (xb) {
+        if ((rc = check_apart(ctx, a.x, n, in, y, rows_span(ldy, n, out), "y")) != EXL3_OK)
+            return rc;
+    } else if (rows_overlap(x, ldx, in, y, ldy, out, n)) {
+        return fail(ctx, EXL3_EINVAL, "y overlaps x");
+    }
+    if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    Carve c;
+    size_t q_at = 0, s_at = 0;
+    const size_t blocks = (size_t)exl3::blocks_of(in);
+    if (x) {
+        q_at = c.take((size_t)n * blocks * exl3::kBlock);
+        s_at = c.take((size_t)n * blocks * sizeof(float));
+    }
+    if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
+    if (x)
+        a.x = exl3::BlockRowsArgs{reinterpret_cast<uint8_t *>(ctx->d_work + q_at),
+                                  reinterpret_cast<float *>(ctx->d_work + s_at),
+                                  (int64_t)blocks * exl3::kBlock, n};
+    a.n = n;
+    a.offsets = offsets;
+    a.transposed = transpose != 0;
+    a.y = y;
+    a.ldy = ldy;
+    const int id = open_timed(ctx, EXL3_KERNEL_BLOCK,
+                              (int64_t)w->groups * exl3::blocks_of(w->rows) *
+                                  exl3::blocks_of(w->cols));
+    return end_timed(ctx, id, run_block_product(ctx, wa, a, x, ldx, in, dtype == EXL3_BF16));
+}
+
+int run_norm_backward(exl3_ctx *ctx, const exl3::NormBackwardArgs &a, bool bf16) {
+    EXL3_HIP(ctx, exl3::launch_rms_norm_backward(a, bf16, ctx->stream));
+    return EXL3_OK;
+}
+int run_norm(exl3_ctx *ctx, const exl3::NormArgs &a, bool bf16) {
+    EXL3_HIP(ctx, exl3::launch_rms_norm(a, bf16, ctx->n_cu, ctx->stream));
+    return EXL3_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int exl3_block_quantize(exl3_ctx *ctx, const void *x, int64_t ldx, int64_t n, int cols, int dtype,
+                        const exl3_block_rows *out) {
+    if (!ctx) return EXL3_EINVAL;
+    int rc;
+    exl3::BlockRowsArgs q;
+    if ((rc = check_product(ctx, n, dtype)) != EXL3_OK ||
+        (rc = check_side(ctx, cols, "cols")) != EXL3_OK ||
+        (rc = check_rows(ctx, x, ldx, n, cols, "x")) != EXL3_OK ||
+        (rc = check_blocks(ctx, out, n, cols, "out", &q)) != EXL3_OK ||
+        (rc = check_apart(ctx, q, n, cols, x, rows_span(ldx, n, cols), "x")) != EXL3_OK)
+        return rc;
+    if (n == 0) return EXL3_OK;
+    if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    const int id = open_timed(ctx, EXL3_KERNEL_NORM, 0);
+    const hipError_t err = exl3::launch_block_quantize(x, ldx, n, cols, dtype == EXL3_BF16, q,
+                                                       ctx->n_cu, ctx->stream);
+    if (err != hipSuccess) rc = fail(ctx, EXL3_EHIP, "launch failed: %s", hipGetErrorString(err));
+    return end_timed(ctx, id, rc);
+}
+
+int exl3_block_quantize_weight(exl3_ctx *ctx, const void *w, int64_t ldw, int rows, int cols,
+                               int dtype, uint8_t *q, int64_t ldq, float *scale) {
+    if (!ctx) return EXL3_EINVAL;
+    int rc;
+    if (dtype != EXL3_F32 && dtype != EXL3_BF16 && dtype != EXL3_F16)
+        return fail(ctx, EXL3_EINVAL, "dtype %d is not EXL3_F32, EXL3_BF16 or EXL3_F16", dtype);
+    const size_t size = dtype == EXL3_F32 ? 4 : 2;
+    if ((rc = check_side(ctx, rows, "rows")) != EXL3_OK ||
+        (rc = check_side(ctx, cols, "cols")) != EXL3_OK)
+        return rc;
+    if (!w) return fail(ctx, EXL3_EINVAL, "null w");
+    if (ldw < cols || ldw > ((int64_t)1 << 40))
+        return fail(ctx, EXL3_EINVAL, "w: rows of %d elements %lld apart", cols, (long long)ldw);
+    if (reinterpret_cast<uintptr_t>(w) % size)
+        return fail(ctx, EXL3_EINVAL, "w (%p) is not aligned to its elements", w);
+    const size_t span = ((size_t)(rows - 1) * (size_t)ldw + (size_t)cols) * size;
+    if ((rc = check_span(ctx, w, span, "w")) != EXL3_OK) return rc;
+    const exl3_block_weight out{q, scale, 1, rows, cols, ldq};
+    exl3::BlockWeightArgs wa;
+    if ((rc = check_block_weight(ctx, &out, &wa)) != EXL3_OK) return rc;
+    const size_t codes = (size_t)rows * (size_t)ldq;
+    const size_t scales = (size_t)exl3::blocks_of(rows) * exl3::blocks_of(cols) * sizeof(float);
+    if (spans_meet(w, span, q, codes) || spans_meet(w, span, scale, scales) ||
+        spans_meet(q, codes, scale, scales))
+        return fail(ctx, EXL3_EINVAL, "w, q and scale overlap");
+    if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    const int id = open_timed(ctx, EXL3_KERNEL_NORM, 0);
+    const hipError_t err =
+        exl3::launch_block_quantize_weight(w, dtype, ldw, rows, cols, q, ldq, scale, ctx->stream);
+    if (err != hipSuccess) rc = fail(ctx, EXL3_EHIP, "launch failed: %s", hipGetErrorString(err));
+    return end_timed(ctx, id, rc);
+}
+
+int exl3_rms_norm(exl3_ctx *ctx, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                  const void *gain, int gain_dtype, float eps, int64_t n, int cols, int dtype,
+                  void *y, int64_t ldy, const exl3_block_rows *blocks, void *sum, int64_t ldsum) {
+    if (!ctx) return EXL3_EINVAL;
+    int rc;
+    exl3::NormArgs a{};
+    if ((rc = check_norm(ctx, n, cols, dtype, eps, gain, gain_dtype)) != EXL3_OK) return rc;
+    if ((rc = check_rows(ctx, x, ldx, n, cols, "x")) != EXL3_OK) return rc;
+    if (residual && (rc = check_rows(ctx, residual, ldr, n, cols, "residual")) != EXL3_OK) return rc;
+    if (sum && !residual) return fail(ctx, EXL3_EINVAL, "a sum without a residual");
+    if (sum && (rc = check_rows(ctx, sum, ldsum, n, cols, "sum")) != EXL3_OK) return rc;
+    if (blocks && y) return fail(ctx, EXL3_EINVAL, "both y and blocks are given");
+    if (blocks) {
+        if ((rc = check_blocks(ctx, blocks, n, cols, "blocks", &a.q)) != EXL3_OK) return rc;
+    } else if ((rc = check_rows(ctx, y, ldy, n, cols, "y")) != EXL3_OK) {
+        return rc;
+    }
+    if (n == 0) return EXL3_OK;
+    const size_t gain_bytes = (size_t)cols * (gain_dtype == EXL3_F32 ? 4 : 2);
+    if (blocks &&
+        ((rc = check_apart(ctx, a.q, n, cols, x, rows_span(ldx, n, cols), "x")) != EXL3_OK ||
+         (rc = check_apart(ctx, a.q, n, cols, residual, residual ? rows_span(ldr, n, cols) : 0,
+                           "the residual")) != EXL3_OK ||
+         (rc = check_apart(ctx, a.q, n, cols, sum, sum ? rows_span(ldsum, n, cols) : 0, "the sum")) !=
+             EXL3_OK ||
+         (rc = check_apart(ctx, a.q, n, cols, gain, gain_bytes, "the gain")) != EXL3_OK))
+        return rc;
+    if (!same_or_apart(y, ldy, x, ldx, cols, n) || !same_or_apart(y, ldy, residual, ldr, cols, n) ||
+        !same_or_apart(sum, ldsum, x, ldx, cols, n) ||
+        !same_or_apart(sum, ldsum, residual, ldr, cols, n))
+        return fail(ctx, EXL3_EINVAL, "y or sum overlaps x or the residual without being it");
+    if (y && sum && rows_overlap(y, ldy, cols, sum, ldsum, cols, n))
+        return fail(ctx, EXL3_EINVAL, "y overlaps the sum");
+    if ((y && spans_meet(y, rows_span(ldy, n, cols), gain, gain_bytes)) ||
+        (sum && spans_meet(sum, rows_span(ldsum, n, cols), gain, gain_bytes)))
+        return fail(ctx, EXL3_EINVAL, "y or sum overlaps the gain");
+    if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    a.x = x;
+    a.ldx = ldx;
+    a.residual = residual;
+    a.ldr = ldr;
+    a.gain = gain;
+    a.gain32 = gain_dtype == EXL3_F32;
+    a.eps = eps;
+    a.n = n;
+    a.cols = cols;
+    a.y = y;
+    a.ldy = ldy;
+    a.sum = sum;
+    a.ldsum = ldsum;
+    const int id = open_timed(ctx, EXL3_KERNEL_NORM, 0);
+    return end_timed(ctx, id, run_norm(ctx, a, dtype == EXL3_BF16));
+}
+
+int exl3_rms_norm_backward(exl3_ctx *ctx, const void *dy, int64_t lddy, const void *ds,
+                           int64_t ldds, const void *s, int64_t lds, const void *gain,
+                           int gain_dtype, float eps, int64_t n, int cols, int dtype, void *dx,
+                           int64_t lddx, void *dgain) {
+    if (!ctx) return EXL3_EINVAL;
+    int rc;
+    if ((rc = check_norm(ctx, n, cols, dtype, eps, gain, gain_dtype)) != EXL3_OK) return rc;
+    if ((rc = check_rows(ctx, dy, lddy, n, cols, "dy")) != EXL3_OK ||
+        (rc = check_rows(ctx, s, lds, n, cols, "s")) != EXL3_OK)
+        return rc;
+    if (ds && (rc = check_rows(ctx, ds, ldds, n, cols, "ds")) != EXL3_OK) return rc;
+    if (dx && (rc = check_rows(ctx, dx, lddx, n, cols, "dx")) != EXL3_OK) return rc;
+    const size_t gain_bytes = (size_t)cols * (gain_dtype == EXL3_F32 ? 4 : 2);
+    if (dgain) {
+        if ((rc = check_gain(ctx, dgain, gain_dtype, dtype, cols, "dgain")) != EXL3_OK) return rc;
+        if (spans_meet(dgain, gain_bytes, gain, gain_bytes) ||
+            spans_meet(dgain, gain_bytes, dy, rows_span(lddy, n, cols)) ||
+            spans_meet(dgain, gain_bytes, s, rows_span(lds, n, cols)) ||
+            (ds && spans_meet(dgain, gain_bytes, ds, rows_span(ldds, n, cols))) ||
+            (dx && spans_meet(dgain, gain_bytes, dx, rows_span(lddx, n, cols))))
+            return fail(ctx, EXL3_EINVAL, "dgain overlaps another argument");
+    }
+    if (dx && n > 0) {
+        if (!same_or_apart(dx, lddx, dy, lddy, cols, n) ||
+            !same_or_apart(dx, lddx, ds, ldds, cols, n))
+            return fail(ctx, EXL3_EINVAL, "dx overlaps dy or ds without being it");
+        if (rows_overlap(dx, lddx, cols, s, lds, cols, n) ||
+            spans_meet(dx, rows_span(lddx, n, cols), gain, gain_bytes))
+            return fail(ctx, EXL3_EINVAL, "dx overlaps s or the gain");
+    }
+    if ((!dx && !dgain) || (n == 0 && !dgain)) return EXL3_OK;
+    if ((rc = set_device(ctx)) != EXL3_OK) return rc;
+    exl3::NormBackwardArgs a{};
+    a.dy = dy;
+    a.lddy = lddy;
+    a.ds = ds;
+    a.ldds = ldds;
+    a.s = s;
+    a.lds = lds;
+    a.gain = gain;
+    a.gain32 = gain_dtype == EXL3_F32;
+    a.eps = eps;
+    a.n = n;
+    a.cols = cols;
+    a.dx = dx;
+    a.lddx = lddx;
+    a.dgain = dgain;
+    a.parts = exl3::norm_backward_parts(n, cols, ctx->n_cu);
+    Carve c;
+    if (dgain) c.take((size_t)a.parts * cols * sizeof(float));
+    if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
+    a.part = dgain ? reinterpret_cast<float *>(ctx->d_work) : nullptr;
+    const int id = open_timed(ctx, EXL3_KERNEL_NORM, 0);
+    return end_timed(ctx, id, run_norm_backward(ctx, a, dtype == EXL3_BF16));
+}
+
+int exl3_block_linear(exl3_ctx *ctx, const exl3_block_weight *w, int transpose, const void *x,
+                      int64_t ldx, const exl3_block_rows *xblocks, int64_t n, int dtype, void *y,
+                      int64_t ldy) {
+    if (!ctx) return EXL3_EINVAL;
+    if (w && w->groups != 1)
+        return fail(ctx, EXL3_EINVAL, "groups = %d: use exl3_block_grouped_linear", w->groups);
+    return block_linear_any(ctx, w, nullptr, transpose, x, ldx, xblocks, n, dtype, y, ldy);
+}
+
+int exl3_block_grouped_linear(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *offsets,
+                              int transpose, const void *x, int64_t ldx,
+                              const exl3_block_rows *xblocks, int64_t n, int dtype, void *y,
+                              int64_t ldy) {
+    if (!ctx) return EXL3_EINVAL;
+    if (!offsets) return fail(ctx, EXL3_EINVAL, "null offsets");
+    return block_linear_any(ctx, w, offsets, transpose, x, ldx, xblocks, n, dtype, y, ldy);
 }
 
 }  // extern "C"

@@ -1,0 +1,545 @@
+// Root-mean-square norm with the residual's addition, its backward pass, and the writing of
+// activations and matrices as 8-bit blocks (gfx950).  All of them are bound by memory: each
+// element is read once, kept in registers between the reductions, and written once.
+#include "blocks.h"
+
+#include <float.h>
+
+#include "exl3.h"
+
+namespace exl3 {
+
+namespace {
+
+constexpr int kWide = 8;                         // consecutive elements a lane takes at a time
+
+// Eight consecutive 16-bit elements, `valid` of them there; the rest are zero.
+__device__ __forceinline__ u32x4 load8(const uint16_t *p, int valid) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (valid >= kWide) return *reinterpret_cast<const u32x4u *>(p);
+    for (int i = 0; i < valid; ++i) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    return v;
+}
+__device__ __forceinline__ void store8(uint16_t *p, u32x4 v, int valid) {
+    if (valid >= kWide) {
+        *reinterpret_cast<u32x4u *>(p) = v;
+        return;
+    }
+    for (int i = 0; i < valid; ++i) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+}
+template <bool BF>
+__device__ __forceinline__ void widen(u32x4 v, float (&f)[kWide]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = Act<BF>::load((uint16_t)v[i]);
+        f[2 * i + 1] = Act<BF>::load((uint16_t)(v[i] >> 16));
+    }
+}
+template <bool BF>
+__device__ __forceinline__ u32x4 narrow(const float (&f)[kWide]) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = Act<BF>::store2(f[2 * i], f[2 * i + 1]);
+    return v;
+}
+
+// Eight factors of the gain at column c.
+template <bool BF, bool G32>
+__device__ __forceinline__ void load_gain(const void *gain, int c, int valid, float (&f)[kWide]) {
+    if (G32) {
+        const float *p = static_cast<const float *>(gain) + c;
+        if (valid >= kWide) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 v = *reinterpret_cast<const f32x4u *>(p + 4 * h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[4 * h + i] = v[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWide; ++i) f[i] = i < valid ? p[i] : 0.0f;
+        }
+    } else {
+        widen<BF>(load8(static_cast<const uint16_t *>(gain) + c, valid), f);
+    }
+}
+
+// Sum over the workgroup's lanes, the same in all of them and in a fixed order.
+template <int T, typename S>
+__device__ __forceinline__ S sum_all(S v, S *between) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+    if (T == 64) return v;
+    __syncthreads();                             // the last use of `between` is over
+    if ((threadIdx.x & 63) == 0) between[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = between[0];
+#pragma unroll
+    for (int w = 1; w < T / 64; ++w) v += between[w];
+    return v;
+}
+
+// The scale of a block whose largest magnitude has these bits, and its inverse.  The scale stays
+// in the normal range, so that the inverse does too.  NaN where the block holds an infinity or a
+// NaN: magnitudes compare as integers, which keeps a NaN.
+struct CodeScale {
+    float scale, inverse;
+};
+__device__ __forceinline__ CodeScale code_scale(uint32_t big) {
+    CodeScale s;
+    s.scale = __builtin_bit_cast(float, big) / kCodeMax;
+    s.scale = s.scale < FLT_MIN ? FLT_MIN : s.scale;
+    if (big >= 0x7F800000u) s.scale = __builtin_bit_cast(float, 0x7FC00000u);
+    s.inverse = 1.0f / s.scale;
+    return s;
+}
+// v / scale rounded to binary32 as a division does: the product with the correctly rounded
+// inverse is at most one unit off, and the remainder, which is exact, brings it to the nearest
+// (taken with this sign, it leaves a zero's sign alone).
+// The instruction then rounds to e4m3, ties to even; at 448 (1 + 2^-23) nothing overflows.
+__device__ __forceinline__ float quotient(float v, const CodeScale &s) {
+    const float q = v * s.inverse;
+    return __builtin_fmaf(-__builtin_fmaf(q, s.scale, -v), s.inverse, q);
+}
+__device__ __forceinline__ u32x2 to_codes(const float (&f)[kWide], const CodeScale &s) {
+    u32x2 o;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * h], s), quotient(f[4 * h + 1], s), 0,
+                                                false);
+        v = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * h + 2], s), quotient(f[4 * h + 3], s), v,
+                                            true);
+        o[h] = (uint32_t)v;
+    }
+    return o;
+}
+__device__ __forceinline__ uint32_t magnitude(float v) {
+    return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+}
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t largest8(const float (&f)[kWide]) {
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < kWide; ++i) big = larger(big, magnitude(f[i]));
+    return big;
+}
+// Over 16 neighbouring lanes, a block's columns.
+__device__ __forceinline__ uint32_t largest_of_block(uint32_t big) {
+    float f = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<1>(f)));
+    f = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<2>(f)));
+    f = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<4>(f)));
+    f = __builtin_bit_cast(float, big);
+    return larger(big, __builtin_bit_cast(uint32_t, lane_xor<8>(f)));
+}
+
+// Eight columns from c of a row of blocks: the block's scale by its first lane, the codes by all,
+// zeros past the width up to `blocks` whole blocks.  All 16 lanes of a block take part.
+__device__ __forceinline__ void write_codes(const BlockRowsArgs &q, int64_t row, int c, int blocks,
+                                            const float (&f)[kWide]) {
+    const CodeScale s = code_scale(largest_of_block(largest8(f)));
+    if (c >= blocks * kBlock) return;
+    *reinterpret_cast<u32x2 *>(q.q + row * q.ld + c) = to_codes(f, s);
+    if ((c & (kBlock - 1)) == 0) q.scale[(c / kBlock) * q.lds + row] = s.scale;
+}
+
+// A sum of squares that binary32 holds: neither too large nor, beside eps, too small.
+__device__ __forceinline__ bool in_range(float squares, float eps, int cols) {
+    return squares < 0x1p126f && (squares > 0x1p-80f || eps * (float)cols > 0x1p-80f);
+}
+
+// ---- norm ----
+// y = s r gain with r = 1 / sqrt(mean(s^2) + eps) and s = x + residual in binary32, before its
+// rounding to the stored sum.  A row by T lanes, T / 64 waves; each lane keeps V pieces of eight
+// columns.  V = 0: rows too wide for that, which are read twice.  Where the squares leave
+// binary32's range the row is summed again in binary64.
+template <int T, int V, bool BF, bool G32>
+__global__ void __launch_bounds__(T < 256 ? 256 : T)
+rms_norm_kernel(NormArgs a) {
+    constexpr int kRows = T < 256 ? 256 / T : 1; // rows a workgroup
+    constexpr int kKeep = V ? V : 1;
+    __shared__ float between[T / 64];
+    __shared__ double between64[T / 64];
+    const int lane = T < 256 ? threadIdx.x % T : threadIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * kRows + (T < 256 ? threadIdx.x / T : 0);
+    if (row >= a.n) return;                      // a whole wave, and no barrier where T = 64
+    const uint16_t *x = static_cast<const uint16_t *>(a.x) + row * a.ldx;
+    const uint16_t *res = a.residual ? static_cast<const uint16_t *>(a.residual) + row * a.ldr
+                                     : nullptr;
+    const int pieces = V ? V : (a.cols + T * kWide - 1) / (T * kWide);
+    float keep[kKeep][kWide];
+    auto load = [&](int i, float (&f)[kWide]) {
+        const int c = (i * T + lane) * kWide, valid = a.cols - c;
+        widen<BF>(load8(x + c, valid), f);
+        if (res) {
+            float g[kWide];
+            widen<BF>(load8(res + c, valid), g);
+#pragma unroll
+            for (int j = 0; j < kWide; ++j) f[j] += g[j];
+        }
+    };
+    float squares = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (V ? V : pieces); ++i) {
+        load(i, keep[V ? i : 0]);
+#pragma unroll
+        for (int j = 0; j < kWide; ++j)
+            squares = __builtin_fmaf(keep[V ? i : 0][j], keep[V ? i : 0][j], squares);
+    }
+    squares = sum_all<T>(squares, between);
+    float r = 1.0f / sqrtf(squares / (float)a.cols + a.eps);
+    double r64 = 0.0;
+    const bool fits = in_range(squares, a.eps, a.cols);
+    if (!fits) {
+        double d = 0.0;
+        for (int i = 0; i < pieces; ++i) {
+            float f[kWide];
+            load(i, f);
+            for (int j = 0; j < kWide; ++j) d += (double)f[j] * (double)f[j];
+        }
+        r64 = 1.0 / sqrt(sum_all<T>(d, between64) / (double)a.cols + (double)a.eps);
+    }
+#pragma unroll
+    for (int i = 0; i < (V ? V : pieces); ++i) {
+        const int c = (i * T + lane) * kWide, valid = a.cols - c;
+        float f[kWide], g[kWide];
+        if (V) {
+#pragma unroll
+            for (int j = 0; j < kWide; ++j) f[j] = keep[V ? i : 0][j];
+        } else {
+            load(i, f);
+        }
+        if (a.sum && valid > 0)
+            store8(static_cast<uint16_t *>(a.sum) + row * a.ldsum + c, narrow<BF>(f), valid);
+        load_gain<BF, G32>(a.gain, c, valid, g);
+        if (fits) {
+#pragma unroll
+            for (int j = 0; j < kWide; ++j) f[j] = f[j] * r * g[j];
+        } else {
+            for (int j = 0; j < kWide; ++j) f[j] = (float)((double)f[j] * r64 * (double)g[j]);
+        }
+        if (valid < kWide)
+#pragma unroll
+            for (int j = 0; j < kWide; ++j) f[j] = j < valid ? f[j] : 0.0f;
+        if (a.y) {
+            if (valid > 0)
+                store8(static_cast<uint16_t *>(a.y) + row * a.ldy + c, narrow<BF>(f), valid);
+        } else {
+            write_codes(a.q, row, c, blocks_of(a.cols), f);
+        }
+    }
+}
+
+// ---- backward ----
+// With u = s r and du = dy gain: dx = ds + r (du - u mean(du u)), dgain = sum over rows of dy u.
+// A workgroup takes rows blockIdx.x, + parts, ..: one pass over each gives both sums, and the
+// gain's gradient of its columns stays in registers until the rows are done.  The parts are
+// added in order by a second kernel, so no result depends on scheduling.  V = 0: columns too many
+// for registers; dgain goes through the part in memory.
+template <int T, int V, bool BF, bool G32>
+__global__ void __launch_bounds__(T)
+rms_norm_backward_kernel(NormBackwardArgs a) {
+    constexpr int kKeep = V ? V : 1;
+    __shared__ float between[T / 64], between2[T / 64];
+    __shared__ double between64[T / 64], between642[T / 64];
+    const int lane = threadIdx.x;
+    const int pieces = V ? V : (a.cols + T * kWide - 1) / (T * kWide);
+    float *part = a.part ? a.part + (int64_t)blockIdx.x * a.cols : nullptr;
+    float dg[kKeep][kWide] = {};
+    bool first = true;
+    for (int64_t row = blockIdx.x; row < a.n; row += a.parts) {
+        const uint16_t *sp = static_cast<const uint16_t *>(a.s) + row * a.lds;
+        const uint16_t *yp = static_cast<const uint16_t *>(a.dy) + row * a.lddy;
+        u32x4 s8[kKeep], y8[kKeep];
+        float squares = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < (V ? V : pieces); ++i) {
+            const int c = (i * T + lane) * kWide, valid = a.cols - c;
+            u32x4 sv = load8(sp + c, valid), yv = load8(yp + c, valid);
+            float s[kWide], y[kWide], g[kWide];
+            load_gain<BF, G32>(a.gain, c, valid, g);
+            widen<BF>(sv, s);
+            widen<BF>(yv, y);
+            s8[V ? i : 0] = sv;
+            y8[V ? i : 0] = yv;
+#pragma unroll
+            for (int j = 0; j < kWide; ++j) {
+                squares = __builtin_fmaf(s[j], s[j], squares);
+                dot = __builtin_fmaf(y[j] * g[j], s[j], dot);
+            }
+        }
+        squares = sum_all<T>(squares, between);
+        dot = sum_all<T>(dot, between2);
+        const float r = 1.0f / sqrtf(squares / (float)a.cols + a.eps);
+        const float mean = dot * r / (float)a.cols;         // of du u
+        double r64 = 0.0, mean64 = 0.0;
+        const bool fits = in_range(squares, a.eps, a.cols) && magnitude(dot) < 0x7E800000u;
+        if (!fits) {
+            double d = 0.0, e = 0.0;
+            for (int i = 0; i < pieces; ++i) {
+                const int c = (i * T + lane) * kWide, valid = a.cols - c;
+                float s[kWide], y[kWide], g[kWide];
+                load_gain<BF, G32>(a.gain, c, valid, g);
+                widen<BF>(load8(sp + c, valid), s);
+                widen<BF>(load8(yp + c, valid), y);
+                for (int j = 0; j < kWide; ++j) {
+                    d += (double)s[j] * (double)s[j];
+                    e += (double)y[j] * (double)g[j] * (double)s[j];
+                }
+            }
+            d = sum_all<T>(d, between64);
+            e = sum_all<T>(e, between642);
+            r64 = 1.0 / sqrt(d / (double)a.cols + (double)a.eps);
+            mean64 = e * r64 / (double)a.cols;
+        }
+#pragma unroll
+        for (int i = 0; i < (V ? V : pieces); ++i) {
+            const int c = (i * T + lane) * kWide, valid = a.cols - c;
+            if (valid <= 0) continue;
+            float s[kWide], y[kWide], g[kWide], o[kWide], u[kWide];
+            load_gain<BF, G32>(a.gain, c, valid, g);
+            widen<BF>(V ? s8[V ? i : 0] : load8(sp + c, valid), s);
+            widen<BF>(V ? y8[V ? i : 0] : load8(yp + c, valid), y);
+            if (a.ds)
+                widen<BF>(load8(static_cast<const uint16_t *>(a.ds) + row * a.ldds + c, valid), o);
+            else
+#pragma unroll
+                for (int j = 0; j < kWide; ++j) o[j] = 0.0f;
+            if (fits) {
+#pragma unroll
+                for (int j = 0; j < kWide; ++j) {
+                    u[j] = s[j] * r;
+                    o[j] += r * (y[j] * g[j] - u[j] * mean);
+                    u[j] *= y[j];
+                }
+            } else {
+                for (int j = 0; j < kWide; ++j) {
+                    const double u64 = (double)s[j] * r64;
+                    o[j] = (float)((double)o[j] +
+                                   r64 * ((double)y[j] * (double)g[j] - u64 * mean64));
+                    u[j] = (float)(u64 * (double)y[j]);
+                }
+            }
+            if (a.dx)
+                store8(static_cast<uint16_t *>(a.dx) + row * a.lddx + c, narrow<BF>(o), valid);
+            if (V) {
+#pragma unroll
+                for (int j = 0; j < kWide; ++j) dg[V ? i : 0][j] += u[j];
+            } else if (part) {
+                for (int j = 0; j < kWide && j < valid; ++j)
+                    part[c + j] = first ? u[j] : part[c + j] + u[j];
+            }
+        }
+        first = false;
+    }
+    if (!V || !part) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = (i * T + lane) * kWide, valid = a.cols - c;
+        if (valid >= kWide) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<f32x4u *>(part + c + 4 * h) =
+                    f32x4{dg[i][4 * h], dg[i][4 * h + 1], dg[i][4 * h + 2], dg[i][4 * h + 3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < kWide; ++j)
+                if (j < valid) part[c + j] = dg[i][j];
+        }
+    }
+}
+
+// dgain: the parts of 64 columns by 16 waves, each a sixteenth of them in order.
+template <bool BF, bool G32>
+__global__ void __launch_bounds__(1024)
+gain_sum_kernel(const float *__restrict__ part, int parts, int cols, void *__restrict__ dgain) {
+    __shared__ float between[16][64];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    float sum = 0.0f;
+    if (c < cols)
+        for (int p = wv; p < parts; p += 16) sum += part[(int64_t)p * cols + c];
+    between[wv][lane] = sum;
+    __syncthreads();
+    if (wv || c >= cols) return;
+#pragma unroll
+    for (int w = 1; w < 16; ++w) sum += between[w][lane];
+    if (G32)
+        static_cast<float *>(dgain)[c] = sum;
+    else
+        static_cast<uint16_t *>(dgain)[c] = Act<BF>::store(sum);
+}
+
+// ---- blocks ----
+// Activations: 16 lanes a block, as in the norm; 2,048 columns a workgroup.
+template <bool BF>
+__global__ void __launch_bounds__(256)
+block_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int cols,
+                      int row_pieces, BlockRowsArgs q) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / row_pieces;          // row_pieces is a multiple of 16
+    if (row >= n) return;
+    const int c = (int)(i - row * row_pieces) * kWide;
+    float f[kWide];
+    widen<BF>(load8(x + row * ldx + c, cols - c), f);
+    write_codes(q, row, c, row_pieces / 16, f);
+}
+
+// A block of 128 x 128 of a matrix: eight lanes of eight columns a row and 16 lanes a row, 16
+// rows at a time.
+template <int TYPE>
+__global__ void __launch_bounds__(256)
+block_quantize_weight_kernel(const void *__restrict__ w, int64_t ldw, int rows, int cols,
+                             uint8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale) {
+    __shared__ uint32_t wave_big[4];
+    const int c = blockIdx.x * kBlock + (threadIdx.x & 15) * kWide, valid = cols - c;
+    const int64_t r0 = (int64_t)blockIdx.y * kBlock + (threadIdx.x >> 4);
+    float f[8][kWide];
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = r0 + 16 * i;
+        const int there = row < rows ? valid : 0;
+        if (TYPE == EXL3_F32)
+            load_gain<false, true>(static_cast<const float *>(w) + (row < rows ? row : 0) * ldw, c,
+                                   there, f[i]);
+        else
+            widen<TYPE == EXL3_BF16>(
+                load8(static_cast<const uint16_t *>(w) + (row < rows ? row : 0) * ldw + c, there),
+                f[i]);
+        big = larger(big, largest8(f[i]));
+    }
+    for (int m = 1; m < 64; m <<= 1) big = larger(big, (uint32_t)__shfl_xor((int)big, m));
+    if ((threadIdx.x & 63) == 0) wave_big[threadIdx.x >> 6] = big;
+    __syncthreads();
+    big = larger(larger(wave_big[0], wave_big[1]), larger(wave_big[2], wave_big[3]));
+    const CodeScale s = code_scale(big);
+    if (threadIdx.x == 0) scale[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = s.scale;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t row = r0 + 16 * i;
+        if (row < rows) *reinterpret_cast<u32x2 *>(q + row * ldq + c) = to_codes(f[i], s);
+    }
+}
+
+template <int T, int V, bool BF, bool G32>
+hipError_t norm_t(const NormArgs &a, hipStream_t stream) {
+    constexpr int kRows = T < 256 ? 256 / T : 1;
+    NormArgs p = a;
+    // rows a launch: a grid's side has fewer than 2^32 lanes
+    const int64_t per = rows_a_launch(T < 256 ? 256 : T) * kRows;
+    for (int64_t r0 = 0; r0 < a.n; r0 += per) {
+        p.n = a.n - r0 < per ? a.n - r0 : per;
+        p.x = static_cast<const uint16_t *>(a.x) + r0 * a.ldx;
+        if (a.residual) p.residual = static_cast<const uint16_t *>(a.residual) + r0 * a.ldr;
+        if (a.y) p.y = static_cast<uint16_t *>(a.y) + r0 * a.ldy;
+        if (a.sum) p.sum = static_cast<uint16_t *>(a.sum) + r0 * a.ldsum;
+        if (!a.y) {
+            p.q.q = a.q.q + r0 * a.q.ld;
+            p.q.scale = a.q.scale + r0;
+        }
+        hipLaunchKernelGGL((rms_norm_kernel<T, V, BF, G32>),
+                           dim3((unsigned)((p.n + kRows - 1) / kRows)), dim3(T < 256 ? 256 : T), 0,
+                           stream, p);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
+template <bool BF, bool G32>
+hipError_t norm_v(const NormArgs &a, hipStream_t stream) {
+    if (a.cols <= 512) return norm_t<64, 1, BF, G32>(a, stream);
+    if (a.cols <= 1024) return norm_t<64, 2, BF, G32>(a, stream);
+    if (a.cols <= 2048) return norm_t<256, 1, BF, G32>(a, stream);
+    if (a.cols <= 4096) return norm_t<512, 1, BF, G32>(a, stream);
+    if (a.cols <= 8192) return norm_t<1024, 1, BF, G32>(a, stream);
+    if (a.cols <= 16384) return norm_t<1024, 2, BF, G32>(a, stream);
+    return norm_t<1024, 0, BF, G32>(a, stream);
+}
+
+template <bool BF, bool G32>
+hipError_t backward_v(const NormBackwardArgs &a, hipStream_t stream) {
+    const dim3 grid((unsigned)a.parts);
+#define EXL3_BACK(T, V)                                                                       \
+    hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, BF, G32>), grid, dim3(T), 0, stream, a)
+    if (a.n > 0) {
+        if (a.cols <= 2048)
+            EXL3_BACK(256, 1);
+        else if (a.cols <= 4096)
+            EXL3_BACK(256, 2);
+        else if (a.cols <= 8192)
+            EXL3_BACK(512, 2);
+        else if (a.cols <= 16384)
+            EXL3_BACK(1024, 2);
+        else
+            EXL3_BACK(1024, 0);
+    }
+#undef EXL3_BACK
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || !a.dgain) return err;
+    hipLaunchKernelGGL((gain_sum_kernel<BF, G32>), dim3((unsigned)((a.cols + 63) / 64)), dim3(1024),
+                       0, stream, a.part, a.n > 0 ? a.parts : 0, a.cols, a.dgain);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs &a, bool bf16, int n_cu, hipStream_t stream) {
+    (void)n_cu;
+    if (bf16) return a.gain32 ? norm_v<true, true>(a, stream) : norm_v<true, false>(a, stream);
+    return a.gain32 ? norm_v<false, true>(a, stream) : norm_v<false, false>(a, stream);
+}
+
+int norm_backward_parts(int64_t n, int cols, int n_cu) {
+    (void)cols;
+    return (int)(n < n_cu ? n : n_cu);
+}
+
+hipError_t launch_rms_norm_backward(const NormBackwardArgs &a, bool bf16, hipStream_t stream) {
+    if (bf16)
+        return a.gain32 ? backward_v<true, true>(a, stream) : backward_v<true, false>(a, stream);
+    return a.gain32 ? backward_v<false, true>(a, stream) : backward_v<false, false>(a, stream);
+}
+
+hipError_t launch_block_quantize(const void *x, int64_t ldx, int64_t n, int cols, bool bf16,
+                                 const BlockRowsArgs &out, int n_cu, hipStream_t stream) {
+    (void)n_cu;
+    const int row_pieces = (int)(blocks_of(cols) * (kBlock / kWide));
+    const int64_t per = rows_a_launch(row_pieces);
+    for (int64_t r0 = 0; r0 < n; r0 += per) {
+        const int64_t rows = n - r0 < per ? n - r0 : per;
+        const unsigned grid = (unsigned)((rows * row_pieces + 255) / 256);
+        const uint16_t *xx = static_cast<const uint16_t *>(x) + r0 * ldx;
+        const BlockRowsArgs q{out.q + r0 * out.ld, out.scale + r0, out.ld, out.lds};
+        if (bf16)
+            hipLaunchKernelGGL((block_quantize_kernel<true>), dim3(grid), dim3(256), 0, stream, xx,
+                               ldx, rows, cols, row_pieces, q);
+        else
+            hipLaunchKernelGGL((block_quantize_kernel<false>), dim3(grid), dim3(256), 0, stream, xx,
+                               ldx, rows, cols, row_pieces, q);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_block_quantize_weight(const void *w, int dtype, int64_t ldw, int rows, int cols,
+                                        uint8_t *q, int64_t ldq, float *scale, hipStream_t stream) {
+    const dim3 grid((unsigned)blocks_of(cols), (unsigned)blocks_of(rows));
+#define EXL3_WEIGHT(TYPE)                                                                       \
+    hipLaunchKernelGGL((block_quantize_weight_kernel<TYPE>), grid, dim3(256), 0, stream, w, ldw, \
+                       rows, cols, q, ldq, scale)
+    if (dtype == EXL3_F32)
+        EXL3_WEIGHT(EXL3_F32);
+    else if (dtype == EXL3_BF16)
+        EXL3_WEIGHT(EXL3_BF16);
+    else
+        EXL3_WEIGHT(EXL3_F16);
+#undef EXL3_WEIGHT
+    return hipGetLastError();
+}
+
+}  // namespace exl3
