@@ -2275,13 +2275,25 @@ int check_block_weight(exl3_ctx *ctx, const exl3_block_weight *w, exl3::BlockWei
     return EXL3_OK;
 }
 
+// Up to 32 rows a group W is streamed once into registers; up to four of them in 16 bits the
+// workgroups write as blocks themselves.
+bool few_rows(const exl3::BlockWeightArgs &w, int transpose, int64_t n) {
+    return !transpose && n <= (int64_t)32 * w.groups;
+}
+bool own_rows(const exl3::BlockWeightArgs &w, int64_t n) {
+    return n <= (int64_t)4 * w.groups && (size_t)w.cols * 2 <= exl3::kOwnBytes;
+}
+
 int run_block_product(exl3_ctx *ctx, const exl3::BlockWeightArgs &w,
                       const exl3::BlockProductArgs &a, const void *x, int64_t ldx, int in,
                       bool bf16) {
-    if (x)
+    if (x && !a.x16)
         EXL3_HIP(ctx, exl3::launch_block_quantize(x, ldx, a.n, in, bf16, a.x, ctx->n_cu,
                                                   ctx->stream));
-    EXL3_HIP(ctx, exl3::launch_block_gemm(w, a, bf16, ctx->n_cu, ctx->stream));
+    if (few_rows(w, a.transposed, a.n))
+        EXL3_HIP(ctx, exl3::launch_block_rows(w, a, bf16, ctx->n_cu, ctx->stream));
+    else
+        EXL3_HIP(ctx, exl3::launch_block_gemm(w, a, bf16, ctx->n_cu, ctx->stream));
     return EXL3_OK;
 }
 
@@ -2315,12 +2327,16 @@ int block_linear_any(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *o
     Carve c;
     size_t q_at = 0, s_at = 0;
     const size_t blocks = (size_t)exl3::blocks_of(in);
-    if (x) {
+    const bool own = x && few_rows(wa, transpose, n) && own_rows(wa, n);
+    if (own) {
+        a.x16 = x;
+        a.ldx16 = ldx;
+    } else if (x) {
         q_at = c.take((size_t)n * blocks * exl3::kBlock);
         s_at = c.take((size_t)n * blocks * sizeof(float));
     }
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;
-    if (x)
+    if (x && !own)
         a.x = exl3::BlockRowsArgs{reinterpret_cast<uint8_t *>(ctx->d_work + q_at),
                                   reinterpret_cast<float *>(ctx->d_work + s_at),
                                   (int64_t)blocks * exl3::kBlock, n};

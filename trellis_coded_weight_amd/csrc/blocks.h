@@ -3,14 +3,106 @@
 // activations, and for every 128 x 128 elements of a matrix.
 #pragma once
 
+#include <float.h>
+
 #include "coded.h"
 
 namespace exl3 {
 
 constexpr int kBlock = 128;                      // elements a scale serves along a row
 constexpr float kCodeMax = 448.0f;               // the largest e4m3 value
+constexpr size_t kOwnBytes = 48 << 10;           // shared memory for rows a workgroup writes as blocks
 
 __host__ __device__ inline int blocks_of(int width) { return (width + kBlock - 1) / kBlock; }
+
+// ---- device side: 16-bit rows and their codes ----
+constexpr int kWide = 8;                         // consecutive elements a lane takes at a time
+
+// Eight consecutive 16-bit elements, `valid` of them there; the rest are zero.
+__device__ __forceinline__ u32x4 load8(const uint16_t *p, int valid) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (valid >= kWide) return *reinterpret_cast<const u32x4u *>(p);
+    for (int i = 0; i < valid; ++i) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    return v;
+}
+__device__ __forceinline__ void store8(uint16_t *p, u32x4 v, int valid) {
+    if (valid >= kWide) {
+        *reinterpret_cast<u32x4u *>(p) = v;
+        return;
+    }
+    for (int i = 0; i < valid; ++i) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+}
+template <bool BF>
+__device__ __forceinline__ void widen(u32x4 v, float (&f)[kWide]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = Act<BF>::load((uint16_t)v[i]);
+        f[2 * i + 1] = Act<BF>::load((uint16_t)(v[i] >> 16));
+    }
+}
+template <bool BF>
+__device__ __forceinline__ u32x4 narrow(const float (&f)[kWide]) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = Act<BF>::store2(f[2 * i], f[2 * i + 1]);
+    return v;
+}
+
+// The scale of a block whose largest magnitude has these bits, and its inverse.  The scale stays
+// in the normal range, so that the inverse does too.  NaN where the block holds an infinity or a
+// NaN: magnitudes compare as integers, which keeps a NaN.
+struct CodeScale {
+    float scale, inverse;
+};
+__device__ __forceinline__ CodeScale code_scale(uint32_t big) {
+    CodeScale s;
+    s.scale = __builtin_bit_cast(float, big) / kCodeMax;
+    s.scale = s.scale < FLT_MIN ? FLT_MIN : s.scale;
+    if (big >= 0x7F800000u) s.scale = __builtin_bit_cast(float, 0x7FC00000u);
+    s.inverse = 1.0f / s.scale;
+    return s;
+}
+// v / scale rounded to binary32 as a division does: the product with the correctly rounded
+// inverse is at most one unit off, and the remainder, which is exact, brings it to the nearest
+// (taken with this sign, it leaves a zero's sign alone).
+// The instruction then rounds to e4m3, ties to even; at 448 (1 + 2^-23) nothing overflows.
+__device__ __forceinline__ float quotient(float v, const CodeScale &s) {
+    const float q = v * s.inverse;
+    return __builtin_fmaf(-__builtin_fmaf(q, s.scale, -v), s.inverse, q);
+}
+__device__ __forceinline__ u32x2 to_codes(const float (&f)[kWide], const CodeScale &s) {
+    u32x2 o;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * h], s), quotient(f[4 * h + 1], s), 0,
+                                                false);
+        v = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * h + 2], s), quotient(f[4 * h + 3], s), v,
+                                            true);
+        o[h] = (uint32_t)v;
+    }
+    return o;
+}
+__device__ __forceinline__ uint32_t magnitude(float v) {
+    return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+}
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t largest8(const float (&f)[kWide]) {
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < kWide; ++i) big = larger(big, magnitude(f[i]));
+    return big;
+}
+// Over 16 neighbouring lanes, a block's columns.
+__device__ __forceinline__ uint32_t largest_of_block(uint32_t big) {
+    float f = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<1>(f)));
+    f = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<2>(f)));
+    f = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<4>(f)));
+    f = __builtin_bit_cast(float, big);
+    return larger(big, __builtin_bit_cast(uint32_t, lane_xor<8>(f)));
+}
 
 // Rows of activations as blocks: codes [n][ld], ld a multiple of 128, zero past the width;
 // scales [blocks][lds], a row's scales lds apart, so that those of neighbouring rows are
@@ -80,7 +172,12 @@ struct BlockProductArgs {
     bool transposed;
     void *y;
     int64_t ldy;
+    const void *x16;                             // 16-bit rows in place of x (launch_block_rows)
+    int64_t ldx16;
 };
+// Few rows a group, not transposed; x or x16.
+hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
+                             int n_cu, hipStream_t stream);
 hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
                              int n_cu, hipStream_t stream);
 

@@ -10,6 +10,8 @@
 // group g = lane >> 4 takes the 16-byte pieces g and 4 + g of a block's 128 bytes.
 #include "blocks.h"
 
+#include <algorithm>
+
 namespace exl3 {
 
 namespace {
@@ -244,11 +246,141 @@ block_gemm_kernel(GemmArgs p) {
     }
 }
 
+// ---- few rows ----
+// A workgroup takes 16 rows of W, its waves the blocks of the contraction in turn, so that
+// neighbouring waves read neighbouring lines; what they hold of W goes from memory straight into
+// operands, CH blocks at a time in NB sets.  Rows of x meet it 16 TN at a time, and the waves' sums are added in
+// order through shared memory.
+// OWN: x comes in 16 bits and each workgroup writes the rows it needs as blocks in shared memory
+// (P rows at a time, as fit), while its first loads of W are on their way.
+struct RowsKernelArgs {
+    GemmArgs p;
+    const uint16_t *x16;
+    int64_t ldx16;
+    int own_rows;                                // OWN: rows a pass
+};
+template <int TN, int WAVES, int CH, int NB, bool BF, bool OWN>
+__global__ void __launch_bounds__(64 * WAVES)
+block_rows_kernel(RowsKernelArgs a) {
+    const GemmArgs &p = a.p;
+    constexpr int kTok = 16 * TN;
+    __shared__ float part[WAVES][kTok][16];
+    extern __shared__ __align__(16) uint8_t own[];
+    const int lane = threadIdx.x & 63, wv = wave_number();
+    const int r = lane & 15, g = lane >> 4;
+    if (p.offsets) clear_rows_of_no_group(p.offsets, p.groups, p.n, p.y, p.ldy, p.m);
+    const int e = blockIdx.x / p.m_tiles, mt = blockIdx.x - e * p.m_tiles;
+    int64_t lo, hi;
+    group_rows(p.offsets, e, p.n, lo, hi);
+    if (lo >= hi) return;
+    const int m0 = mt * 16;
+    int wr = m0 + r;
+    wr = wr < p.m ? wr : p.m - 1;                // past the edge: repeats, not stored
+    const uint8_t *w_at = p.w + ((int64_t)e * p.m + wr) * p.ldw + 16 * g;
+    const float *ws_at = p.ws + ((int64_t)e * blocks_of(p.m) + m0 / kBlock) * p.blocks;
+    const int steps = (p.blocks + WAVES - 1) / WAVES;
+    const int pitch = p.blocks * kBlock + 16;    // OWN: a row of codes in shared memory
+    float *own_scale = reinterpret_cast<float *>(own + a.own_rows * pitch);
+    const int take = OWN ? a.own_rows : kTok;    // rows of x a pass
+    constexpr int XB = OWN ? 1 : NB;             // of shared memory nothing is held ahead
+    Operand w[NB][CH], x[XB][OWN ? 1 : CH][TN];
+    float xs[XB][OWN ? 1 : CH][TN];
+    auto load_w = [&](int at, int s0) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            int b = (s0 + c) * WAVES + wv;
+            b = b < p.blocks ? b : p.blocks - 1;
+            const u32x4 *from = reinterpret_cast<const u32x4 *>(w_at + (int64_t)b * kBlock);
+            w[at][c].a = from[0];
+            w[at][c].b = from[4];
+        }
+    };
+    for (int64_t t0 = lo; t0 < hi; t0 += take) {
+        const int here = (int)(hi - t0 < take ? hi - t0 : take);
+        auto load_x1 = [&](int b, Operand (&xo)[TN], float (&so)[TN]) {
+            b = b < p.blocks ? b : p.blocks - 1;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int t = 16 * j + r < here ? 16 * j + r : here - 1;
+                const uint8_t *xp = OWN ? own + t * pitch + b * kBlock + 16 * g
+                                        : p.x + (t0 + t) * p.ldx + (int64_t)b * kBlock + 16 * g;
+                xo[j].a = *reinterpret_cast<const u32x4 *>(xp);
+                xo[j].b = *reinterpret_cast<const u32x4 *>(xp + 64);
+                so[j] = OWN ? own_scale[b * a.own_rows + t] : p.xs[(int64_t)b * p.ldxs + t0 + t];
+            }
+        };
+        auto load_x = [&](int at, int s0) {
+            if (!OWN)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) load_x1((s0 + c) * WAVES + wv, x[at][c], xs[at][c]);
+        };
+        load_x(0, 0);
+        load_w(0, 0);
+        if (OWN) {
+            const int pieces = p.blocks * (kBlock / kWide);
+            if (t0 != lo) __syncthreads();       // the last pass has read its codes
+            for (int i = threadIdx.x; i < here * pieces; i += 64 * WAVES) {
+                const int t = i / pieces, c = (i - t * pieces) * kWide;
+                float f[kWide];
+                widen<BF>(load8(a.x16 + (t0 + t) * a.ldx16 + c, p.k - c), f);
+                const CodeScale s = code_scale(largest_of_block(largest8(f)));
+                *reinterpret_cast<u32x2 *>(own + t * pitch + c) = to_codes(f, s);
+                if ((c & (kBlock - 1)) == 0) own_scale[(c / kBlock) * a.own_rows + t] = s.scale;
+            }
+            __syncthreads();
+        }
+        f32x4 acc[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        auto products = [&](int at, int s0) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int b = (s0 + c) * WAVES + wv;
+                if (b >= p.blocks) continue;     // the same for the whole wave
+                const float ws = ws_at[b];
+                if (OWN) load_x1(b, x[0][0], xs[0][0]);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int ax = OWN ? 0 : at, cx = OWN ? 0 : c;
+                    const f32x4 z = block_product(w[at][c], x[ax][cx][j]);
+                    const float f = xs[ax][cx][j] * ws;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_fmaf(z[i], f, acc[j][i]);
+                }
+            }
+        };
+        for (int s = 0; s < steps; s += NB * CH) {
+            if (NB == 2 && s + CH < steps) {
+                load_x(NB - 1, s + CH);
+                load_w(NB - 1, s + CH);
+            }
+            products(0, s);
+            if (s + NB * CH < steps) {
+                load_x(0, s + NB * CH);
+                load_w(0, s + NB * CH);
+            }
+            if (NB == 2 && s + CH < steps) products(NB - 1, s + CH);
+        }
+        if (t0 != lo) __syncthreads();           // the last pass's sums have been read
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            *reinterpret_cast<f32x4 *>(&part[wv][16 * j + r][4 * g]) = acc[j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < kTok * 16; i += 64 * WAVES) {
+            const int t = i / 16, m = i % 16;
+            float sum = part[0][t][m];
+#pragma unroll
+            for (int v = 1; v < WAVES; ++v) sum += part[v][t][m];
+            if (t < here && m0 + m < p.m) p.y[(t0 + t) * p.ldy + m0 + m] = Act<BF>::store(sum);
+        }
+    }
+}
+
 }  // namespace
 
-hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
-                             int n_cu, hipStream_t stream) {
-    (void)n_cu;
+namespace {
+
+GemmArgs gemm_args(const BlockWeightArgs &w, const BlockProductArgs &a) {
     GemmArgs p{};
     p.w = w.q;
     p.ws = w.scale;
@@ -265,6 +397,68 @@ hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a
     p.groups = w.groups;
     p.y = static_cast<uint16_t *>(a.y);
     p.ldy = a.ldy;
+    return p;
+}
+
+}  // namespace
+
+hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
+                             int n_cu, hipStream_t stream) {
+    RowsKernelArgs r{};
+    r.p = gemm_args(w, a);
+    r.p.m_tiles = (r.p.m + 15) / 16;
+    r.x16 = static_cast<const uint16_t *>(a.x16);
+    r.ldx16 = a.ldx16;
+    const int64_t total = (int64_t)r.p.m_tiles * w.groups;
+    const int64_t avg = (a.n + w.groups - 1) / w.groups;
+    (void)n_cu;
+    size_t shared = 0;
+    if (a.x16) {
+        const size_t row = (size_t)r.p.blocks * kBlock + 16 + (size_t)r.p.blocks * 4;
+        r.own_rows = (int)std::min<size_t>(16, std::max<size_t>(1, kOwnBytes / row));
+        shared = r.own_rows * row;
+    }
+#define EXL3_ROWS_T(TN, WAVES, CH, NB, BF, OWN)                                                 \
+    hipLaunchKernelGGL((block_rows_kernel<TN, WAVES, CH, NB, BF, OWN>), dim3((unsigned)total),  \
+                       dim3(64 * WAVES), shared, stream, r)
+#define EXL3_ROWS(TN, WAVES, CH, NB, OWN)                  \
+    do {                                                   \
+        if (bf16)                                          \
+            EXL3_ROWS_T(TN, WAVES, CH, NB, true, OWN);     \
+        else                                               \
+            EXL3_ROWS_T(TN, WAVES, CH, NB, false, OWN);    \
+    } while (0)
+    // The waves and what each has under way, by the contraction's blocks, us:
+    //   16 blocks (64 experts of 1408 x 2048, 64 rows): 8 waves of two blocks 25, 8 of four 47,
+    //   16 of two 43 (idle waves still take their places)
+    //   32 (12288 x 4096, 1 row, own): 8 of four 12.1, 16 of two 12.5, 8 of two 16.6; 16 rows:
+    //   16.4, 13.5 and 15.9
+    //   96 (4096 x 12288, 16 rows): 16 of two 14.0, 8 of four 14.4, 8 of two 15.0
+    const int blocks = r.p.blocks;
+    if (a.x16) {
+        if (blocks <= 16)
+            EXL3_ROWS(1, 8, 2, 1, true);
+        else if (blocks <= 32)
+            EXL3_ROWS(1, 8, 4, 1, true);
+        else
+            EXL3_ROWS(1, 16, 2, 1, true);
+    } else if (avg <= 16) {
+        if (blocks <= 16)
+            EXL3_ROWS(1, 8, 2, 1, false);
+        else
+            EXL3_ROWS(1, 16, 2, 1, false);
+    } else {
+        EXL3_ROWS(2, 8, 1, 2, false);
+    }
+#undef EXL3_ROWS
+#undef EXL3_ROWS_T
+    return hipGetLastError();
+}
+
+hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
+                             int n_cu, hipStream_t stream) {
+    (void)n_cu;
+    GemmArgs p = gemm_args(w, a);
 #define EXL3_BLOCK_T(BM, BN, WM, WN, RING, BF, TR)                                             \
     hipLaunchKernelGGL((block_gemm_kernel<BM, BN, WM, WN, RING, BF, TR>),                      \
                        dim3((unsigned)p.total), dim3(64 * WM * WN), 0, stream, p)

@@ -3,45 +3,11 @@
 // element is read once, kept in registers between the reductions, and written once.
 #include "blocks.h"
 
-#include <float.h>
-
 #include "exl3.h"
 
 namespace exl3 {
 
 namespace {
-
-constexpr int kWide = 8;                         // consecutive elements a lane takes at a time
-
-// Eight consecutive 16-bit elements, `valid` of them there; the rest are zero.
-__device__ __forceinline__ u32x4 load8(const uint16_t *p, int valid) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (valid >= kWide) return *reinterpret_cast<const u32x4u *>(p);
-    for (int i = 0; i < valid; ++i) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-    return v;
-}
-__device__ __forceinline__ void store8(uint16_t *p, u32x4 v, int valid) {
-    if (valid >= kWide) {
-        *reinterpret_cast<u32x4u *>(p) = v;
-        return;
-    }
-    for (int i = 0; i < valid; ++i) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-}
-template <bool BF>
-__device__ __forceinline__ void widen(u32x4 v, float (&f)[kWide]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = Act<BF>::load((uint16_t)v[i]);
-        f[2 * i + 1] = Act<BF>::load((uint16_t)(v[i] >> 16));
-    }
-}
-template <bool BF>
-__device__ __forceinline__ u32x4 narrow(const float (&f)[kWide]) {
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = Act<BF>::store2(f[2 * i], f[2 * i + 1]);
-    return v;
-}
 
 // Eight factors of the gain at column c.
 template <bool BF, bool G32>
@@ -77,62 +43,6 @@ __device__ __forceinline__ S sum_all(S v, S *between) {
 #pragma unroll
     for (int w = 1; w < T / 64; ++w) v += between[w];
     return v;
-}
-
-// The scale of a block whose largest magnitude has these bits, and its inverse.  The scale stays
-// in the normal range, so that the inverse does too.  NaN where the block holds an infinity or a
-// NaN: magnitudes compare as integers, which keeps a NaN.
-struct CodeScale {
-    float scale, inverse;
-};
-__device__ __forceinline__ CodeScale code_scale(uint32_t big) {
-    CodeScale s;
-    s.scale = __builtin_bit_cast(float, big) / kCodeMax;
-    s.scale = s.scale < FLT_MIN ? FLT_MIN : s.scale;
-    if (big >= 0x7F800000u) s.scale = __builtin_bit_cast(float, 0x7FC00000u);
-    s.inverse = 1.0f / s.scale;
-    return s;
-}
-// v / scale rounded to binary32 as a division does: the product with the correctly rounded
-// inverse is at most one unit off, and the remainder, which is exact, brings it to the nearest
-// (taken with this sign, it leaves a zero's sign alone).
-// The instruction then rounds to e4m3, ties to even; at 448 (1 + 2^-23) nothing overflows.
-__device__ __forceinline__ float quotient(float v, const CodeScale &s) {
-    const float q = v * s.inverse;
-    return __builtin_fmaf(-__builtin_fmaf(q, s.scale, -v), s.inverse, q);
-}
-__device__ __forceinline__ u32x2 to_codes(const float (&f)[kWide], const CodeScale &s) {
-    u32x2 o;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        int v = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * h], s), quotient(f[4 * h + 1], s), 0,
-                                                false);
-        v = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(f[4 * h + 2], s), quotient(f[4 * h + 3], s), v,
-                                            true);
-        o[h] = (uint32_t)v;
-    }
-    return o;
-}
-__device__ __forceinline__ uint32_t magnitude(float v) {
-    return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
-}
-__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t largest8(const float (&f)[kWide]) {
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < kWide; ++i) big = larger(big, magnitude(f[i]));
-    return big;
-}
-// Over 16 neighbouring lanes, a block's columns.
-__device__ __forceinline__ uint32_t largest_of_block(uint32_t big) {
-    float f = __builtin_bit_cast(float, big);
-    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<1>(f)));
-    f = __builtin_bit_cast(float, big);
-    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<2>(f)));
-    f = __builtin_bit_cast(float, big);
-    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<4>(f)));
-    f = __builtin_bit_cast(float, big);
-    return larger(big, __builtin_bit_cast(uint32_t, lane_xor<8>(f)));
 }
 
 // Eight columns from c of a row of blocks: the block's scale by its first lane, the codes by all,
