@@ -517,7 +517,8 @@ int exl3_adapter_linear_backward(exl3_ctx *ctx, const exl3_weight *w, const exl3
  */
 
 /* Rows of activations, `width` elements each.
- *   q      [n][ldq] codes, 16-byte aligned; ldq a multiple of 128, at least width.
+ *   q      [n][ldq] codes, 16-byte aligned; ldq a multiple of 128, at least width and
+ *          at most 2^23.
  *          Bytes from width to the next multiple of 128 belong to the last block:
  *          written as zeros, and read, where they must be zero.
  *   scale  float [blocks][lds], blocks = width / 128 rounded up: the scale of row
@@ -530,7 +531,7 @@ typedef struct {
 
 /* A matrix W [rows][cols] of codes, or one after the other for `groups` (experts).
  *   q      [groups][rows][ldq] codes, 16-byte aligned; ldq a multiple of 128, at
- *          least cols.  Bytes from cols to the next multiple of 128 are read and
+ *          least cols and at most 2^21.  Bytes from cols to the next multiple of 128 are read and
  *          must not be NaN (0x7F, 0xFF).
  *   scale  float [groups][rows / 128][cols / 128], both rounded up
  * rows and cols 1 .. 2^20, groups 1 .. 65535. */

@@ -23,7 +23,7 @@ SOURCES = ["api.hip", "viterbi_fwd.hip", "viterbi_fwd_f16.hip", "traceback.hip",
 # Matrix instructions on vector registers throughout: where a kernel has more than
 # 256 registers a lane, the compiler otherwise moves accumulators to and from the
 # accumulation registers in the product's inner loop.
-EXTRA = {"dense.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in ("dense.hip", "blocks.hip")}
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 COMMON = [

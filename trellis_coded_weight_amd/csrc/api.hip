@@ -2184,9 +2184,10 @@ int check_blocks(exl3_ctx *ctx, const exl3_block_rows *b, int64_t n, int width, 
     if (n == 0) return EXL3_OK;
     const int blocks = exl3::blocks_of(width);
     if (!b->q || !b->scale) return fail(ctx, EXL3_EINVAL, "%s: null q or scale", name);
-    if (b->ldq < width || b->ldq % exl3::kBlock || b->ldq > ((int64_t)1 << 40))
-        return fail(ctx, EXL3_EINVAL, "%s: rows of %d codes %lld apart (a multiple of %d)", name,
-                    width, (long long)b->ldq, exl3::kBlock);
+    // (a tile's rows of codes lie within 32-bit offsets)
+    if (b->ldq < width || b->ldq % exl3::kBlock || b->ldq > ((int64_t)1 << 23))
+        return fail(ctx, EXL3_EINVAL, "%s: rows of %d codes %lld apart (a multiple of %d, at most %d)",
+                    name, width, (long long)b->ldq, exl3::kBlock, 1 << 23);
     if (b->lds < n || b->lds > ((int64_t)1 << 40))
         return fail(ctx, EXL3_EINVAL, "%s: scales of %lld rows %lld apart", name, (long long)n,
                     (long long)b->lds);

@@ -11,6 +11,7 @@
 #include "blocks.h"
 
 #include <algorithm>
+#include <cmath>
 
 namespace exl3 {
 
@@ -43,10 +44,20 @@ __device__ __forceinline__ u32x2 read_turned8(const uint8_t *from) {
         (__attribute__((address_space(3))) i32x2 *)from));
 }
 
-// Four bytes a lane straight into shared memory, at to + 4 lane.
-__device__ __forceinline__ void load4_to_lds(const void *from, void *to) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     (__attribute__((address_space(3))) void *)to, 4, 0, 0);
+// 16 (or four) bytes a lane straight into shared memory, at to + 16 (4) lane, from a uniform base
+// and a lane's offset.  Written out because the compiler, which knows what its own form of it
+// writes, waits for all such loads under way before the next read of shared memory; here the
+// caller's wait_loads and barriers order them.  (The move to m0 needs one state before its use.)
+__device__ __forceinline__ void stage16(const uint8_t *base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(offset), "s"(base), "s"(to) : "memory");
+}
+__device__ __forceinline__ void stage4(const float *base, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                 :: "v"(offset), "s"(base), "s"(to) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
 }
 
 // Sets the rows of y before the first group and from the last offset on to zero; all workgroups
@@ -74,31 +85,50 @@ struct GemmArgs {
 };
 
 // ---- tiles ----
-// A workgroup computes BM columns of y by BN rows.  Slices of one block of k pass through RING
-// places in shared memory, loaded straight into them, with the x scales of each wave's rows
-// behind them.  The swizzle that spreads rows over the banks is in which piece a lane fetches:
-// slot s of row r holds piece s ^ (r & 7).
+// A workgroup computes BM columns of y by BN rows, each wave SM x SN of them.  Slices of one block
+// of k pass through RING places in shared memory, loaded straight into them, with the x scales of
+// each wave's rows behind them.  The swizzle that spreads rows over the banks is in which piece a
+// lane fetches: slot s of row r holds piece s ^ (r & 7).
+// While the matrix units work on 16 rows of W, the next 16 are read and the results before are
+// scaled and added.  The one barrier a slice stands where its last rows have just been read: its
+// place is free for the slice RING later, and the next slice is there.
 // TR: W is contracted over its rows.  A slice is 128 rows of W by BM bytes, and the operand is
-// turned as it is read.
-template <int BM, int BN, int WM, int WN, int RING, bool BF, bool TR>
-__global__ void __launch_bounds__(64 * WM * WN)
-block_gemm_kernel(GemmArgs p) {
+// turned as it is read: 16 lanes read eight rows of 16 bytes, and turned_slot puts the rows that a
+// wave's 32 lanes read at a time into different banks.
+template <int BM>
+__device__ __forceinline__ int turned_slot(int row) {
+    return BM == 256 ? (row & 7) | (row >> 4 & 1) << 3 : (row >> 1 & 3) | (row >> 4 & 1) << 2;
+}
+
+template <int BM, int BN, int WM, int WN, int WK, int RING, int SPREAD, bool BF, bool TR>
+__global__ void __launch_bounds__(64 * WM * WN * WK)
+block_gemm_kernel(const uint8_t *__restrict__ w, const float *__restrict__ w_scale,
+                  const uint8_t *__restrict__ x, const float *__restrict__ x_scale,
+                  const int32_t *__restrict__ offsets, uint16_t *__restrict__ y, GemmArgs p) {
     constexpr int kThreads = 64 * WM * WN, SM = BM / WM, SN = BN / WN, TM = SM / 16, TN = SN / 16;
     constexpr int kPiecesW = BM * 8 / kThreads, kPiecesX = BN * 8 / kThreads;
     constexpr int kPieces = kPiecesW + kPiecesX;
     constexpr int kLoads = kPieces + 1;                   // a slice's loads a wave
-    constexpr int kSlice = (BM + BN) * kBlock, kScales = WM * WN * 64;
+    constexpr int kScales = (BM + BN) * kBlock, kSlice = kScales + WM * WN * 64 * 4;
+    constexpr int kSpread = SPREAD, kSlots = kSpread * TN;
     constexpr int kPitch = SM * 2 + 16;                   // bytes a row of y takes in the epilogue
     static_assert(SN <= 64 && SM <= 128 && 128 % SM == 0, "a wave's scales");
-    static_assert(WM * WN * 16 * kPitch <= RING * kSlice, "the epilogue fits the ring");
-    __shared__ __align__(16) uint8_t ring[RING * kSlice];
-    __shared__ float scales[RING * kScales];
-    const int lane = threadIdx.x & 63, wv = wave_number();
+    static_assert(SPREAD < TM || (SPREAD == TM && RING > 2), "a slice's loads precede its wait");
+    static_assert(TM % 2 == 0 && (!TR || BM == 256 || BM == 128), "two places for rows of W");
+    static_assert((WK - 1) * BM * BN * 4 + WM * WN * 16 * kPitch <= WK * RING * kSlice,
+                  "the sets' sums and the epilogue fit the rings");
+    // (one array: with two, the compiler takes waits between them)
+    __shared__ __align__(16) uint8_t rings[WK * RING * kSlice + WK * WM * WN * 256];
+    const int lane = threadIdx.x & 63, wk = WK == 1 ? 0 : wave_number() / (WM * WN);
+    const int wv = WK == 1 ? wave_number() : wave_number() % (WM * WN);
+    const int tid = WK == 1 ? (int)threadIdx.x : (int)threadIdx.x % (64 * WM * WN);
+    uint8_t *ring = rings + wk * RING * kSlice;           // this set's
     const int r = lane & 15, g = lane >> 4, wm = wv % WM, wn = wv / WM;
     int total = p.total;
-    if (p.offsets) {
-        clear_rows_of_no_group(p.offsets, p.groups, p.n, p.y, p.ldy, p.m);
-        total = count_tiles(p.offsets, 0, p.groups, p.n, BN, total / p.m_tiles) * p.m_tiles;
+    if (offsets) {
+        clear_rows_of_no_group(offsets, p.groups, p.n, y, p.ldy, p.m);
+        total = count_tiles(offsets, 0, p.groups, p.n, BN, total / p.m_tiles) * p.m_tiles;
+        total = __builtin_amdgcn_readfirstlane(total);    // all lanes have the same
         if ((int)blockIdx.x >= total) return;             // fewer tiles than the grid allows for
     }
     // each die takes a run of tiles, in panels eight tiles wide, so that the tiles it works on at
@@ -110,117 +140,230 @@ block_gemm_kernel(GemmArgs p) {
     const int mt = 8 * panel + id % wide;
     int nt = id / wide, e = 0;
     int64_t lo = 0, hi = p.n;
-    if (p.offsets) {
-        e = group_of_tile(p.offsets, 0, p.groups, p.n, BN, nt);
+    if (offsets) {
+        e = group_of_tile(offsets, 0, p.groups, p.n, BN, nt);
         if (e < 0) return;
-        group_rows(p.offsets, e, p.n, lo, hi);
+        e = __builtin_amdgcn_readfirstlane(e);
+        nt = __builtin_amdgcn_readfirstlane(nt);
+        group_rows(offsets, e, p.n, lo, hi);
     }
     const int64_t row0 = lo + (int64_t)nt * BN;
     const int m0 = mt * BM + wm * SM;
-    // the tile's operands
+    // this set's blocks: first, first + WK, .. (a set without any computes with factors of zero)
+    const int first = wk < p.blocks ? wk : 0, steps = (p.blocks + WK - 1) / WK;
+    // the tile's operands from uniform bases that move along k, and 32-bit offsets of the
+    // thread's pieces
     const int w_rows = TR ? p.k : p.m;
-    const uint8_t *w_at = p.w + (int64_t)e * w_rows * p.ldw + (TR ? mt * BM : (int64_t)mt * BM * p.ldw);
-    const uint8_t *x_at = p.x + row0 * p.ldx;
-    int64_t piece_at[kPieces];
+    const uint8_t *w_at = w + (int64_t)e * w_rows * p.ldw +
+                          (TR ? mt * BM + (int64_t)first * kBlock * p.ldw
+                              : (int64_t)mt * BM * p.ldw + first * kBlock);
+    const uint8_t *x_at = x + row0 * p.ldx + first * kBlock;
+    const float *xs_at = x_scale + row0 + first * p.ldxs;
+    uint32_t xs_lane;                                     // this lane's row of them
+    {
+        const int64_t t = wn * SN + lane % SN, last = hi - 1 - row0;
+        xs_lane = (uint32_t)(t < last ? t : last) * 4;
+    }
+    uint32_t piece_at[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        const int q = (i < kPiecesW ? i : i - kPiecesW) * kThreads + threadIdx.x;
+        const int q = (i < kPiecesW ? i : i - kPiecesW) * kThreads + tid;
+        const int row = i < kPiecesW && TR ? q / (BM / 16) : q >> 3;
         if (i < kPiecesW && TR) {
-            const int row = q / (BM / 16), s = q % (BM / 16);
-            const int left = (int)p.ldw - mt * BM - 16;  // past the edge: repeats, not stored
-            const int c = s * 16;
-            piece_at[i] = (int64_t)row * p.ldw + (c < left ? c : left);
-        } else if (i < kPiecesW) {
-            const int row = q >> 3, kp = ((q & 7) ^ (row & 7)) * 16;
-            const int left = p.m - mt * BM - 1;
-            piece_at[i] = (int64_t)(row < left ? row : left) * p.ldw + kp;
+            const int c = ((q % (BM / 16)) ^ turned_slot<BM>(row)) * 16;
+            const int left = (int)p.ldw - mt * BM - 16;   // past the edge: repeats, not stored
+            piece_at[i] = (uint32_t)row * (uint32_t)p.ldw + (uint32_t)(c < left ? c : left);
         } else {
-            const int row = q >> 3, kp = ((q & 7) ^ (row & 7)) * 16;
-            const int64_t left = hi - row0 - 1;
-            piece_at[i] = (row < left ? row : left) * p.ldx + kp;
+            const int kp = ((q & 7) ^ (row & 7)) * 16;
+            const int64_t left = i < kPiecesW ? p.m - mt * BM - 1 : hi - row0 - 1;
+            piece_at[i] = (uint32_t)(row < left ? row : left) *
+                              (uint32_t)(i < kPiecesW ? p.ldw : p.ldx) + (uint32_t)kp;
         }
     }
-    const float *xs_at;
-    {
-        const int64_t t = row0 + wn * SN + lane % SN, last = hi - 1;
-        xs_at = p.xs + (t < last ? t : last);
-    }
-    // W's scale of this wave's columns of y
-    const int m_block = (m0 < p.m ? m0 : p.m - 1) / kBlock;
-    const int w_blocks = blocks_of(TR ? p.m : p.k);       // scales a row of them
-    const float *ws_at = p.ws + (int64_t)e * blocks_of(p.m) * blocks_of(p.k) +
-                         (TR ? m_block : (int64_t)m_block * w_blocks);
-    const int ws_step = TR ? w_blocks : 1;
-    auto load_slice = [&](int s) {
-        const int b = s < p.blocks ? s : p.blocks - 1;    // the last is repeated, not used
-        uint8_t *to = ring + (s % RING) * kSlice;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int q = i < kPiecesW ? i : BM * 8 / kThreads + i - kPiecesW;
-            const uint8_t *from;
-            if (i < kPiecesW && TR) {
-                // rows past the contraction's end meet codes of zero: repeats
-                const int row = (i * kThreads + threadIdx.x) / (BM / 16);
-                const int over = b * kBlock + row - (p.k - 1);
-                from = w_at + piece_at[i] + (int64_t)(b * kBlock - (over > 0 ? over : 0)) * p.ldw;
-            } else {
-                from = (i < kPiecesW ? w_at : x_at) + piece_at[i] + b * kBlock;
-            }
-            load_to_lds(from, to + (q * kThreads + wv * 64) * 16);
+    const uint32_t ring_at = lds_address(ring);
+    // the last slice of TR: rows past the contraction's end meet codes of zero and repeat its last
+    const int short_by = TR ? p.blocks * kBlock - p.k : 0;
+    auto load_piece = [&](int i, int b, int place) {
+        const int q = i < kPiecesW ? i : BM * 8 / kThreads + i - kPiecesW;
+        uint32_t at = piece_at[i];
+        if (TR && i < kPiecesW && short_by && b >= p.blocks - 1) {
+            const int row = (i * kThreads + tid) / (BM / 16);
+            const int over = row - (kBlock - 1 - short_by);
+            at -= (uint32_t)(over > 0 ? over : 0) * (uint32_t)p.ldw;
         }
-        load4_to_lds(xs_at + (int64_t)b * p.ldxs, scales + (s % RING) * kScales + wv * 64);
+        stage16(i < kPiecesW ? w_at : x_at, at, ring_at + place * kSlice + (q * kThreads + wv * 64) * 16);
     };
-    f32x4 acc[TM][TN];
+    auto load_scales = [&](int place) {
+        stage4(xs_at, xs_lane, ring_at + place * kSlice + kScales + wv * 256);
+    };
+    auto read_scale = [&](int j, int place) {
+        return *reinterpret_cast<const float *>(ring + place * kSlice + kScales + wv * 256 +
+                                                (16 * j + r) * 4);
+    };
+    // from the slice of step s to the next; the last is repeated into places that nobody reads
+    auto advance = [&](int s) {
+        if (wk + WK * (s + 1) >= p.blocks) return;
+        w_at += TR ? (int64_t)WK * kBlock * p.ldw : WK * kBlock;
+        x_at += WK * kBlock;
+        xs_at += WK * p.ldxs;
+    };
+    // W's scales of this wave's columns of y
+    const int m_block = (m0 < p.m ? m0 : p.m - 1) / kBlock;
+    // 64 steps' at a time, a step's in a lane: a scalar load is one that each wait for shared
+    // memory would wait for, some 400 cycles (0 for a step past the last).  The first come with
+    // the slices' loads, so that nothing waits for all of these.
+    const float *ws_at = w_scale + (int64_t)e * blocks_of(p.m) * p.blocks +
+                         (TR ? m_block : (int64_t)m_block * p.blocks);
+    auto w_place = [&](int s) {                           // of step s + lane, in bytes
+        const int now = wk + WK * (s + lane);
+        return (uint32_t)(now < p.blocks ? now : 0) * (TR ? (uint32_t)blocks_of(p.m) * 4u : 4u);
+    };
+    auto w_there = [&](int s, float v) { return wk + WK * (s + lane) < p.blocks ? v : 0.0f; };
+    const int w_first = WK * RING * kSlice + (wk * WM * WN + wv) * 256;
+    stage4(ws_at, w_place(0), lds_address(rings) + w_first);
+    auto of_lane = [](float v, int l) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+    };
+    Operand a[2], b[TN];
+    float f[TN], f_last[TN];
+    f32x4 acc[TM][TN], z[2][TN];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int j = 0; j < TN; ++j) {
+        f_last[j] = 0.0f;
+        z[1][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < TM; ++i) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const int at_a = (g ^ (r & 7)) * 16, at_b = ((4 + g) ^ (r & 7)) * 16;
+    auto read_a = [&](int i, int place, Operand &to) {
+        const uint8_t *at = ring + place * kSlice;
+        if (TR) {
+            u32x2 t[4];
 #pragma unroll
-    for (int s = 0; s < RING - 1; ++s) load_slice(s);
-    for (int s = 0; s < p.blocks; ++s) {
-        wait_loads<(RING - 2) * kLoads>();
-        barrier_in_place();                               // slice s is there, s - 1 is used up
-        load_slice(s + RING - 1);
-        const uint8_t *at = ring + (s % RING) * kSlice;
-        const uint8_t *xa = at + BM * kBlock + (wn * SN + r) * kBlock;
-        const float wscale = ws_at[(int64_t)s * ws_step];
-        Operand b[TN];
-        float f[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            b[j].a = *reinterpret_cast<const u32x4 *>(xa + 16 * j * kBlock + (g ^ (r & 7)) * 16);
-            b[j].b = *reinterpret_cast<const u32x4 *>(xa + 16 * j * kBlock + ((4 + g) ^ (r & 7)) * 16);
-            f[j] = scales[(s % RING) * kScales + wv * 64 + 16 * j + r] * wscale;
+            for (int q = 0; q < 4; ++q) {
+                const int row = 16 * g + 64 * (q >> 1) + 8 * (q & 1) + (r >> 1);
+                const int slot = (wm * (SM / 16) + i) ^ turned_slot<BM>(row);
+                t[q] = read_turned8(at + row * BM + slot * 16 + (r & 1) * 8);
+            }
+            to.a = u32x4{t[0][0], t[0][1], t[1][0], t[1][1]};
+            to.b = u32x4{t[2][0], t[2][1], t[3][0], t[3][1]};
+        } else {
+            const uint8_t *wa = at + (wm * SM + 16 * i + r) * kBlock;
+            to.a = *reinterpret_cast<const u32x4 *>(wa + at_a);
+            to.b = *reinterpret_cast<const u32x4 *>(wa + at_b);
         }
+    };
+    auto read_b = [&](int j, int place, Operand &to) {
+        const uint8_t *xa = ring + place * kSlice + (BM + wn * SN + 16 * j + r) * kBlock;
+        to.a = *reinterpret_cast<const u32x4 *>(xa + at_a);
+        to.b = *reinterpret_cast<const u32x4 *>(xa + at_b);
+    };
+    auto scale_add = [&](int i, int j, float by) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            Operand a;
-            if (TR) {
-                const uint8_t *wa = at + wm * SM + 16 * i + (r & 1) * 8;
-                u32x2 t[4];
+        for (int c = 0; c < 4; ++c)
+            acc[i][j][c] = __builtin_fmaf(z[i & 1][j][c], by, acc[i][j][c]);
+    };
+    // A slice's loads go out one after the other over kSpread rows of matrix instructions: all at
+    // once they wait for one another, and the wave with them.
+    auto load_slot = [&](int slot, int s, int place) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    t[q] = read_turned8(wa + (16 * g + 64 * (q >> 1) + 8 * (q & 1) + (r >> 1)) * BM);
-                a.a = u32x4{t[0][0], t[0][1], t[1][0], t[1][1]};
-                a.b = u32x4{t[2][0], t[2][1], t[3][0], t[3][1]};
-            } else {
-                const uint8_t *wa = at + (wm * SM + 16 * i + r) * kBlock;
-                a.a = *reinterpret_cast<const u32x4 *>(wa + (g ^ (r & 7)) * 16);
-                a.b = *reinterpret_cast<const u32x4 *>(wa + ((4 + g) ^ (r & 7)) * 16);
+        for (int q = 0; q < kLoads; ++q)
+            if (q * kSlots / kLoads == slot) {
+                if (q < kPieces)
+                    load_piece(q, wk + WK * s, place);
+                else
+                    load_scales(place);
+            }
+    };
+#pragma unroll
+    for (int s = 0; s < RING; ++s) {
+#pragma unroll
+        for (int slot = 0; slot < (s + 1 < RING ? kSlots : TN); ++slot) load_slot(slot, s, s);
+        if (s + 1 < RING || kSpread == 1) advance(s);
+    }
+    wait_loads<(RING - 2) * kLoads + (kLoads * TN + kSlots - 1) / kSlots>();
+    barrier_in_place();
+    float w64 = w_there(0, *reinterpret_cast<const float *>(rings + w_first + lane * 4));
+    const float ws = of_lane(w64, 0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+        read_b(j, 0, b[j]);
+        f[j] = read_scale(j, 0) * ws;
+    }
+    read_a(0, 0, a[0]);
+    int place = 0, before = RING - 1;
+    for (int s0 = 0; s0 < steps; s0 += 63) {              // a step takes the next one's scale
+        if (s0)
+            w64 = w_there(s0, *reinterpret_cast<const float *>(
+                                  reinterpret_cast<const char *>(ws_at) + w_place(s0)));
+        for (int s = s0; s < steps && s < s0 + 63; ++s) {
+            const int after = place + 1 == RING ? 0 : place + 1;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    z[i & 1][j] = block_product(a[i & 1], b[j]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    // under the matrix instructions: the next operands, the results before and loads
+                    if (j == 0 && i + 1 < TM) read_a(i + 1, place, a[(i + 1) & 1]);
+                    if (i + 1 == TM) {
+                        if (j == 0) read_a(0, after, a[0]);         // the next slice's
+                        read_b(j, after, b[j]);
+                        load_slot(j, s + RING, place);
+                    } else if (i + 1 < kSpread) {
+                        load_slot((i + 1) * TN + j, s - 1 + RING, before);
+                    }
+                    if (i == 0)
+                        scale_add(TM - 1, j, f_last[j]);
+                    else
+                        scale_add(i - 1, j, f[j]);
+                    if (i + 1 == TM) {
+                        f_last[j] = f[j];
+                        f[j] = read_scale(j, after);
+                    }
+                }
+                if (i + 2 == kSpread) advance(s + RING - 1);  // the last of its loads is out
+                if (kSpread == 1 && i + 1 == TM) advance(s + RING);
+                if (i + 2 == TM) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    wait_loads<(RING - 2) * kLoads>();
+                    barrier_in_place();
+                }
             }
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const f32x4 z = block_product(a, b[j]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[i][j][c] = __builtin_fmaf(z[c], f[j], acc[i][j][c]);
-            }
+            for (int j = 0; j < TN; ++j) f[j] *= of_lane(w64, s - s0 + 1);
+            before = place;
+            place = after;
         }
     }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) scale_add(TM - 1, j, f_last[j]);
     // 16 rows of y at a time through the wave's part of the ring, so that whole lines are written
     wait_loads<0>();
     __syncthreads();
+    if constexpr (WK > 1) {
+        // the sets' sums, added in order
+        f32x4 *sums = reinterpret_cast<f32x4 *>(rings);
+        if (wk > 0)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    sums[((wk - 1) * TM * TN + i * TN + j) * kThreads + tid] = acc[i][j];
+        __syncthreads();
+        if (wk > 0) return;
+#pragma unroll
+        for (int v = 1; v < WK; ++v)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] += sums[((v - 1) * TM * TN + i * TN + j) * kThreads + tid];
+        // (a wave's place in the epilogue lies where sums of any wave were: past them)
+    }
     const int64_t t0 = row0 + wn * SN;
-    uint8_t *out = ring + wv * 16 * kPitch;
+    uint8_t *out = rings + (WK - 1) * BM * BN * 4 + wv * 16 * kPitch;
     constexpr int kPer = SM / 8;                          // 16-byte pieces a row
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
@@ -235,7 +378,7 @@ block_gemm_kernel(GemmArgs p) {
             const int64_t tok = t0 + 16 * j + row;
             if (piece >= 16 * kPer || tok >= hi || m0 + c >= p.m) continue;
             const u32x4 o = *reinterpret_cast<const u32x4 *>(out + row * kPitch + c * 2);
-            uint16_t *yo = p.y + tok * p.ldy + m0 + c;
+            uint16_t *yo = y + tok * p.ldy + m0 + c;
             const int left = p.m - m0 - c;
             if (left >= 8) {
                 *reinterpret_cast<u32x4u *>(yo) = o;
@@ -457,25 +600,54 @@ hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a
 
 hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
                              int n_cu, hipStream_t stream) {
-    (void)n_cu;
     GemmArgs p = gemm_args(w, a);
-#define EXL3_BLOCK_T(BM, BN, WM, WN, RING, BF, TR)                                             \
-    hipLaunchKernelGGL((block_gemm_kernel<BM, BN, WM, WN, RING, BF, TR>),                      \
-                       dim3((unsigned)p.total), dim3(64 * WM * WN), 0, stream, p)
-#define EXL3_BLOCK(BM, BN, WM, WN, RING)                                                       \
+#define EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, BF, TR)                                 \
+    hipLaunchKernelGGL((block_gemm_kernel<BM, BN, WM, WN, WK, RING, SPREAD, BF, TR>),          \
+                       dim3((unsigned)p.total), dim3(64 * WM * WN * WK), 0, stream, p.w, p.ws, \
+                       p.x, p.xs, p.offsets, p.y, p)
+#define EXL3_BLOCK(BM, BN, WM, WN, WK, RING, SPREAD)                                           \
     do {                                                                                       \
         p.m_tiles = (p.m + BM - 1) / BM;                                                       \
-        p.total = (int)(p.m_tiles * (a.offsets ? a.n / BN + w.groups : (a.n + BN - 1) / BN));  \
+        const int64_t total =                                                                  \
+            p.m_tiles * (a.offsets ? a.n / BN + w.groups : (a.n + BN - 1) / BN);               \
+        /* a launch has fewer than 2^32 lanes, of up to 512 a workgroup */                     \
+        if (total >= (int64_t)1 << 23) return hipErrorInvalidConfiguration;                    \
+        p.total = (int)total;                                                                  \
         if (bf16 && a.transposed)                                                              \
-            EXL3_BLOCK_T(BM, BN, WM, WN, RING, true, true);                                    \
+            EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, true, true);                        \
         else if (bf16)                                                                         \
-            EXL3_BLOCK_T(BM, BN, WM, WN, RING, true, false);                                   \
+            EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, true, false);                       \
         else if (a.transposed)                                                                 \
-            EXL3_BLOCK_T(BM, BN, WM, WN, RING, false, true);                                   \
+            EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, false, true);                       \
         else                                                                                   \
-            EXL3_BLOCK_T(BM, BN, WM, WN, RING, false, false);                                  \
+            EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, false, false);                      \
     } while (0)
-    EXL3_BLOCK(128, 128, 2, 2, 2);
+    // What a round of tiles takes at k = 4096, us, one or (128 x 128 with a ring of two) two tiles a
+    // compute unit: measured for 4,096 columns at n = 200 (128 x 32: 11.3, 128 x 64: 12.6), 512
+    // (21.4, 14.2, 128 x 128: 19.6), 1,024 (27 in two rounds of 128 x 64, 128 x 128: 21.9, 256 x 128:
+    // 26.3), 2,000 (128 x 128 twice a unit: 36, 256 x 128: 34, 256 x 256: 43), 12,288 columns at n =
+    // 4,096 (three rounds of 256 x 256: 167, six of 256 x 128: 199).  Experts' tiles: each group's
+    // last is half empty on average, and rounds run into one another.
+    enum { kHuge, kLarge, kTwice, kMedium, kSmall, kSmallest };
+    auto cost = [&](int bm, int bn, int places, double us) {
+        const double m_tiles = (p.m + bm - 1) / bm;
+        if (a.offsets)
+            return us * std::max(1.0, m_tiles * ((double)a.n / bn + 0.5 * w.groups) / (places * n_cu));
+        return us * std::ceil(m_tiles * (double)((a.n + bn - 1) / bn) / (places * n_cu));
+    };
+    const double costs[6] = {cost(256, 256, 1, 55), cost(256, 128, 1, 33), cost(128, 128, 2, 34),
+                             cost(128, 128, 1, 21), cost(128, 64, 1, 14),  cost(128, 32, 1, 11)};
+    int best = 0;
+    for (int i = 1; i < 6; ++i)
+        if (costs[i] < costs[best]) best = i;
+    switch (best) {
+        case kHuge: EXL3_BLOCK(256, 256, 2, 4, 1, 2, 4); break;
+        case kLarge: EXL3_BLOCK(256, 128, 4, 2, 1, 3, 4); break;
+        case kTwice: EXL3_BLOCK(128, 128, 2, 2, 1, 2, 1); break;
+        case kMedium: EXL3_BLOCK(128, 128, 2, 2, 1, 4, 4); break;
+        case kSmall: EXL3_BLOCK(128, 64, 2, 2, 2, 3, 4); break;
+        default: EXL3_BLOCK(128, 32, 2, 2, 2, 3, 4);
+    }
 #undef EXL3_BLOCK
 #undef EXL3_BLOCK_T
     return hipGetLastError();
