@@ -483,3 +483,96 @@ def test_differentiable_products(T, ctx):
     got = xg.grad.double().cpu()
     one = x.grad.reshape(24, 256).double().cpu()
     assert torch.equal(got[:10], one[:10]) and torch.equal(got[10:], 2 * one[10:])
+
+
+LONG = [(3, 40, 9000), (20, 40, 20000), (40, 70, 20000), (200, 260, 17000), (300, 1100, 8200)]
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("n,m,k", LONG)
+def test_long_contractions(T, ctx, n, m, k, back):
+    """More blocks than a wave has lanes, in every tile."""
+    rows, cols = (k, m) if back else (m, k)
+    q, scale = matrix(rows, cols, n + m + k)
+    x, host = rows_of(n, k, BF, n + k)
+    xq, xs = to_blocks(host.float())
+    y = ctx.block_linear(x, T.BlockWeight(q.cuda(), scale.cuda()), transpose=back)
+    dense = from_blocks(q, scale, 128)
+    check_product(y, from_blocks(xq, xs), dense.t() if back else dense, BF, k)
+
+
+# sizes at which each of the tiles is chosen (one matrix), by rows and result columns
+TILES = [(4096, 4096, 130), (1500, 4096, 257), (1800, 4100, 128), (1000, 4096, 300), (500, 4097, 200),
+         (150, 4096, 390)]
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("n,m,k", TILES)
+def test_every_tile(T, ctx, n, m, k, back):
+    rows, cols = (k, m) if back else (m, k)
+    q, scale = matrix(rows, cols, n + m)
+    x, host = rows_of(n, k, BF, n + k)
+    xq, xs = to_blocks(host.float())
+    y = ctx.block_linear(x, T.BlockWeight(q.cuda(), scale.cuda()), transpose=back)
+    dense = from_blocks(q, scale, 128)
+    dense = dense.t() if back else dense
+    # a sample of the rows, the first and the last tiles among them
+    at = torch.cat([torch.arange(0, n, 37), torch.arange(max(0, n - 40), n)])
+    check_product(y[at.cuda()], from_blocks(xq, xs)[at], dense, BF, k)
+    assert torch.equal(y, ctx.block_linear(ctx.block_quantize(x), T.BlockWeight(q.cuda(), scale.cuda()),
+                                           transpose=back))
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_many_groups_of_many_rows(T, ctx, back):
+    """Tiles of experts' rows: empty groups, groups of one row and of several tiles."""
+    sizes = [0, 1, 700, 0, 129, 128, 127, 300, 2, 0, 513, 64, 1000, 0]
+    offsets = torch.tensor([3] + sizes, dtype=torch.int32).cumsum(0).int()
+    E, n = len(sizes), int(offsets[-1]) + 2
+    rows, cols = (320, 1408)
+    q, scale = matrix(rows, cols, 5, groups=E)
+    k = rows if back else cols
+    x, host = rows_of(n, k, F16, 6)
+    xq, xs = to_blocks(host.float())
+    y = ctx.block_grouped_linear(x, T.BlockWeight(q.cuda(), scale.cuda()), offsets.cuda(),
+                                 transpose=back)
+    xd = from_blocks(xq, xs)
+    for e in range(E):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if b > a:
+            dense = from_blocks(q[e], scale[e], 128)
+            check_product(y[a:b], xd[a:b], dense.t() if back else dense, F16, k)
+    assert (y[:3] == 0).all() and (y[-2:] == 0).all()
+
+
+@pytest.mark.parametrize("offsets", [[0, 50, 20, 60], [-5, 10, 40, 500], [60, 60, 0, 0],
+                                     [-(1 << 31), 0, (1 << 31) - 1, 5]])
+@pytest.mark.parametrize("n", [60, 700])
+@pytest.mark.parametrize("back", [False, True])
+def test_offsets_that_make_no_sense_stay_inside(T, ctx, offsets, n, back):
+    """Unspecified rows of y, and nothing outside it."""
+    q, scale = matrix(130, 200, 7, groups=3)
+    w = T.BlockWeight(q.cuda(), scale.cuda())
+    k, m = (130, 200) if back else (200, 130)
+    x, _ = rows_of(n, k, BF, 8)
+    out = torch.full((n + 20, m + 5), 3.0, dtype=BF, device="cuda")
+    ctx.block_grouped_linear(x, w, torch.tensor(offsets, dtype=torch.int32).cuda(), transpose=back,
+                             out=out[10:n + 10, :m])
+    torch.cuda.synchronize()
+    assert (out[:10] == 3).all() and (out[n + 10:] == 3).all() and (out[:, m:] == 3).all()
+
+
+def test_more_groups_than_a_launch_holds(T, ctx):
+    """Few rows a group of many groups: 65,535 matrices of 520 rows, in two launches."""
+    E, rows = 65535, 520
+    q = torch.zeros(E, rows, 128, dtype=torch.uint8, device="cuda")
+    q[:, :, 0] = 0x38                                      # 1.0
+    scale = torch.ones(E, 5, 1, device="cuda")
+    w = T.BlockWeight(q.view(E4M3), scale)
+    n = 200
+    x = torch.zeros(n, 128, dtype=BF, device="cuda")
+    x[:, 0] = torch.arange(1, n + 1, device="cuda").to(BF)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[E - 50:] = torch.cat([torch.arange(0, 50), torch.tensor([n])]).int().cuda()
+    y = ctx.block_grouped_linear(x, w, offsets)
+    assert torch.equal(y, x[:, :1].expand(n, rows))

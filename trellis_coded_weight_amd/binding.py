@@ -311,21 +311,31 @@ class BlockRows:
                                                    by_block.stride(0) < n):
             by_block = by_block.contiguous()
         lds = by_block.stride(0) if by_block.shape[0] > 1 else max(n, 1)
-        self._set(q[:, :cols], by_block.t(), ldq, lds)
+        self._set(q, by_block, n, cols, ldq, lds)
 
-    def _set(self, q, scale, ldq, lds):
-        self.q, self.scale, self.device = q, scale, q.device
-        self.n, self.cols = q.shape
-        self._c = _BlockRows(q.data_ptr(), scale.data_ptr(), ldq, lds)
+    def _set(self, codes, by_block, n, cols, ldq, lds):
+        self._codes, self._by_block = codes, by_block
+        self.n, self.cols, self.device = n, cols, codes.device
+        self._c = _BlockRows(codes.data_ptr(), by_block.data_ptr(), ldq, lds)
         self._ref = ctypes.byref(self._c)
 
     @classmethod
     def _empty(cls, n: int, cols: int, device) -> "BlockRows":
         rows = cls.__new__(cls)
-        q = torch.empty(n, BLOCK * _blocks(cols), dtype=_E4M3, device=device)
-        scale = torch.empty(_blocks(cols), n, dtype=torch.float32, device=device)
-        rows._set(q[:, :cols], scale.t(), q.shape[1], max(n, 1))
+        blocks = _blocks(cols)
+        rows._set(torch.empty(n, BLOCK * blocks, dtype=_E4M3, device=device),
+                  torch.empty(blocks, n, dtype=torch.float32, device=device), n, cols,
+                  BLOCK * blocks, n or 1)
         return rows
+
+    @property
+    def q(self) -> torch.Tensor:
+        codes = self._codes
+        return codes if codes.shape[1] == self.cols else codes[:, :self.cols]
+
+    @property
+    def scale(self) -> torch.Tensor:
+        return self._by_block.t()
 
     def dequantize(self) -> torch.Tensor:
         """The values [n, cols] in float32."""

@@ -2276,25 +2276,35 @@ int check_block_weight(exl3_ctx *ctx, const exl3_block_weight *w, exl3::BlockWei
     return EXL3_OK;
 }
 
-// Up to 32 rows a group W is streamed once into registers; up to four of them in 16 bits the
-// workgroups write as blocks themselves.
-bool few_rows(const exl3::BlockWeightArgs &w, int transpose, int64_t n) {
+// Up to 32 rows a group W is streamed once into registers.
+bool few_rows(const exl3::BlockWeightArgs &w, bool transpose, int64_t n) {
     return !transpose && n <= (int64_t)32 * w.groups;
 }
-bool own_rows(const exl3::BlockWeightArgs &w, int64_t n) {
-    return n <= (int64_t)4 * w.groups && (size_t)w.cols * 2 <= exl3::kOwnBytes;
+
+// Whether its workgroups write 16-bit rows as blocks themselves, each all that it needs, in place
+// of a launch before: up to some 28,000 elements on a compute unit, us with and without:
+// 2 rows, 12288 x 4096 (24,576): 13.1, 15.1; 4 rows, 4096 x 4096 (16,384): 7.9, 10.0; 8 rows
+// (32,768): 10.6, 10.1; 4 rows, 12288 x 4096 (49,152): 15.4, 14.8; 16 experts of 1408 x 2048, 32
+// rows (22,528): 11.6, 12.3, 64 rows (45,056): 14.4, 13.7.
+bool own_rows(const exl3::BlockWeightArgs &w, int64_t n, int n_cu) {
+    const int64_t rows = (n + w.groups - 1) / w.groups;
+    const int64_t workgroups = (int64_t)((w.rows + 15) / 16) * w.groups;
+    return rows * w.cols * std::max<int64_t>(n_cu, workgroups) <= (int64_t)28000 * n_cu;
 }
 
 int run_block_product(exl3_ctx *ctx, const exl3::BlockWeightArgs &w,
                       const exl3::BlockProductArgs &a, const void *x, int64_t ldx, int in,
                       bool bf16) {
     if (x && !a.x16)
-        EXL3_HIP(ctx, exl3::launch_block_quantize(x, ldx, a.n, in, bf16, a.x, ctx->n_cu,
-                                                  ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_block_quantize(x, ldx, a.n, in, bf16, a.x, ctx->stream));
     if (few_rows(w, a.transposed, a.n))
-        EXL3_HIP(ctx, exl3::launch_block_rows(w, a, bf16, ctx->n_cu, ctx->stream));
-    else
-        EXL3_HIP(ctx, exl3::launch_block_gemm(w, a, bf16, ctx->n_cu, ctx->stream));
+        EXL3_HIP(ctx, exl3::launch_block_rows(w, a, bf16, ctx->stream));
+    else {
+        const hipError_t err = exl3::launch_block_gemm(w, a, bf16, ctx->n_cu, ctx->stream);
+        if (err == hipErrorInvalidConfiguration)
+            return fail(ctx, EXL3_EUNSUPPORTED, "a product of over 2^23 tiles: split its groups");
+        EXL3_HIP(ctx, err);
+    }
     return EXL3_OK;
 }
 
@@ -2328,7 +2338,7 @@ int block_linear_any(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *o
     Carve c;
     size_t q_at = 0, s_at = 0;
     const size_t blocks = (size_t)exl3::blocks_of(in);
-    const bool own = x && few_rows(wa, transpose, n) && own_rows(wa, n);
+    const bool own = x && few_rows(wa, transpose != 0, n) && own_rows(wa, n, ctx->n_cu);
     if (own) {
         a.x16 = x;
         a.ldx16 = ldx;
@@ -2357,7 +2367,7 @@ int run_norm_backward(exl3_ctx *ctx, const exl3::NormBackwardArgs &a, bool bf16)
     return EXL3_OK;
 }
 int run_norm(exl3_ctx *ctx, const exl3::NormArgs &a, bool bf16) {
-    EXL3_HIP(ctx, exl3::launch_rms_norm(a, bf16, ctx->n_cu, ctx->stream));
+    EXL3_HIP(ctx, exl3::launch_rms_norm(a, bf16, ctx->stream));
     return EXL3_OK;
 }
 
@@ -2380,7 +2390,7 @@ int exl3_block_quantize(exl3_ctx *ctx, const void *x, int64_t ldx, int64_t n, in
     if ((rc = set_device(ctx)) != EXL3_OK) return rc;
     const int id = open_timed(ctx, EXL3_KERNEL_NORM, 0);
     const hipError_t err = exl3::launch_block_quantize(x, ldx, n, cols, dtype == EXL3_BF16, q,
-                                                       ctx->n_cu, ctx->stream);
+                                                       ctx->stream);
     if (err != hipSuccess) rc = fail(ctx, EXL3_EHIP, "launch failed: %s", hipGetErrorString(err));
     return end_timed(ctx, id, rc);
 }
@@ -2519,7 +2529,7 @@ int exl3_rms_norm_backward(exl3_ctx *ctx, const void *dy, int64_t lddy, const vo
     a.dx = dx;
     a.lddx = lddx;
     a.dgain = dgain;
-    a.parts = exl3::norm_backward_parts(n, cols, ctx->n_cu);
+    a.parts = exl3::norm_backward_parts(n, ctx->n_cu);
     Carve c;
     if (dgain) c.take((size_t)a.parts * cols * sizeof(float));
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;

@@ -136,7 +136,7 @@ struct NormArgs {
     int64_t ldsum;
     BlockRowsArgs q;
 };
-hipError_t launch_rms_norm(const NormArgs &a, bool bf16, int n_cu, hipStream_t stream);
+hipError_t launch_rms_norm(const NormArgs &a, bool bf16, hipStream_t stream);
 
 struct NormBackwardArgs {
     const void *dy, *s, *ds;                     // ds: null for none
@@ -152,11 +152,11 @@ struct NormBackwardArgs {
     float *part;                                 // [parts][cols]
     int parts;
 };
-int norm_backward_parts(int64_t n, int cols, int n_cu);
+int norm_backward_parts(int64_t n, int n_cu);
 hipError_t launch_rms_norm_backward(const NormBackwardArgs &a, bool bf16, hipStream_t stream);
 
 hipError_t launch_block_quantize(const void *x, int64_t ldx, int64_t n, int cols, bool bf16,
-                                 const BlockRowsArgs &out, int n_cu, hipStream_t stream);
+                                 const BlockRowsArgs &out, hipStream_t stream);
 
 // dtype: EXL3_F32, EXL3_BF16 or EXL3_F16; w [rows][ldw].
 hipError_t launch_block_quantize_weight(const void *w, int dtype, int64_t ldw, int rows, int cols,
@@ -177,7 +177,8 @@ struct BlockProductArgs {
 };
 // Few rows a group, not transposed; x or x16.
 hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
-                             int n_cu, hipStream_t stream);
+                             hipStream_t stream);
+// hipErrorInvalidConfiguration: more tiles than a launch holds.
 hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
                              int n_cu, hipStream_t stream);
 

@@ -401,6 +401,7 @@ struct RowsKernelArgs {
     const uint16_t *x16;
     int64_t ldx16;
     int own_rows;                                // OWN: rows a pass
+    int group0;                                  // the first of this launch
 };
 template <int TN, int WAVES, int CH, int NB, bool BF, bool OWN>
 __global__ void __launch_bounds__(64 * WAVES)
@@ -412,7 +413,7 @@ block_rows_kernel(RowsKernelArgs a) {
     const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 15, g = lane >> 4;
     if (p.offsets) clear_rows_of_no_group(p.offsets, p.groups, p.n, p.y, p.ldy, p.m);
-    const int e = blockIdx.x / p.m_tiles, mt = blockIdx.x - e * p.m_tiles;
+    const int e = a.group0 + blockIdx.x / p.m_tiles, mt = blockIdx.x % p.m_tiles;
     int64_t lo, hi;
     group_rows(p.offsets, e, p.n, lo, hi);
     if (lo >= hi) return;
@@ -546,15 +547,13 @@ GemmArgs gemm_args(const BlockWeightArgs &w, const BlockProductArgs &a) {
 }  // namespace
 
 hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
-                             int n_cu, hipStream_t stream) {
+                             hipStream_t stream) {
     RowsKernelArgs r{};
     r.p = gemm_args(w, a);
     r.p.m_tiles = (r.p.m + 15) / 16;
     r.x16 = static_cast<const uint16_t *>(a.x16);
     r.ldx16 = a.ldx16;
-    const int64_t total = (int64_t)r.p.m_tiles * w.groups;
     const int64_t avg = (a.n + w.groups - 1) / w.groups;
-    (void)n_cu;
     size_t shared = 0;
     if (a.x16) {
         const size_t row = (size_t)r.p.blocks * kBlock + 16 + (size_t)r.p.blocks * 4;
@@ -562,7 +561,7 @@ hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a
         shared = r.own_rows * row;
     }
 #define EXL3_ROWS_T(TN, WAVES, CH, NB, BF, OWN)                                                 \
-    hipLaunchKernelGGL((block_rows_kernel<TN, WAVES, CH, NB, BF, OWN>), dim3((unsigned)total),  \
+    hipLaunchKernelGGL((block_rows_kernel<TN, WAVES, CH, NB, BF, OWN>), dim3(grid),             \
                        dim3(64 * WAVES), shared, stream, r)
 #define EXL3_ROWS(TN, WAVES, CH, NB, OWN)                  \
     do {                                                   \
@@ -578,24 +577,31 @@ hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a
     //   16.4, 13.5 and 15.9
     //   96 (4096 x 12288, 16 rows): 16 of two 14.0, 8 of four 14.4, 8 of two 15.0
     const int blocks = r.p.blocks;
-    if (a.x16) {
-        if (blocks <= 16)
-            EXL3_ROWS(1, 8, 2, 1, true);
-        else if (blocks <= 32)
-            EXL3_ROWS(1, 8, 4, 1, true);
-        else
-            EXL3_ROWS(1, 16, 2, 1, true);
-    } else if (avg <= 16) {
-        if (blocks <= 16)
-            EXL3_ROWS(1, 8, 2, 1, false);
-        else
-            EXL3_ROWS(1, 16, 2, 1, false);
-    } else {
-        EXL3_ROWS(2, 8, 1, 2, false);
+    // a launch has fewer than 2^32 lanes, of up to 1,024 a workgroup
+    const int per = std::max(1, (1 << 21) / r.p.m_tiles);
+    for (r.group0 = 0; r.group0 < w.groups; r.group0 += per) {
+        const unsigned grid = (unsigned)(r.p.m_tiles * std::min(per, w.groups - r.group0));
+        if (a.x16) {
+            if (blocks <= 16)
+                EXL3_ROWS(1, 8, 2, 1, true);
+            else if (blocks <= 32)
+                EXL3_ROWS(1, 8, 4, 1, true);
+            else
+                EXL3_ROWS(1, 16, 2, 1, true);
+        } else if (avg <= 16) {
+            if (blocks <= 16)
+                EXL3_ROWS(1, 8, 2, 1, false);
+            else
+                EXL3_ROWS(1, 16, 2, 1, false);
+        } else {
+            EXL3_ROWS(2, 8, 1, 2, false);
+        }
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
     }
 #undef EXL3_ROWS
 #undef EXL3_ROWS_T
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,

@@ -55,9 +55,48 @@ __device__ __forceinline__ void write_codes(const BlockRowsArgs &q, int64_t row,
     if ((c & (kBlock - 1)) == 0) q.scale[(c / kBlock) * q.lds + row] = s.scale;
 }
 
+// Two sums at once through places used in turn, so that one barrier serves (a lane is past the
+// reads of one place when it writes to it again, as the other's barrier lies between).
+template <int T>
+__device__ __forceinline__ void sum_both(float &v, float &w, float2 (&between)[2][T / 64],
+                                         int &turn) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        v += __shfl_xor(v, m);
+        w += __shfl_xor(w, m);
+    }
+    if (T == 64) return;
+    if ((threadIdx.x & 63) == 0) between[turn][threadIdx.x >> 6] = float2{v, w};
+    __syncthreads();
+    v = between[turn][0].x;
+    w = between[turn][0].y;
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) {
+        v += between[turn][i].x;
+        w += between[turn][i].y;
+    }
+    turn ^= 1;
+}
+
 // A sum of squares that binary32 holds: neither too large nor, beside eps, too small.
 __device__ __forceinline__ bool in_range(float squares, float eps, int cols) {
     return squares < 0x1p126f && (squares > 0x1p-80f || eps * (float)cols > 0x1p-80f);
+}
+
+// 1 / sqrt(mean + eps) as mantissa * 2^exponent: the factor itself, and what it multiplies, may
+// lie outside binary32's normal range while their product does not.
+struct Rsqrt {
+    float mantissa;
+    int exponent;
+};
+__device__ __forceinline__ Rsqrt split(float r) {
+    return Rsqrt{__builtin_amdgcn_frexp_mantf(r), __builtin_amdgcn_frexp_expf(r)};
+}
+__device__ __forceinline__ Rsqrt split(double r) {
+    return Rsqrt{(float)__builtin_amdgcn_frexp_mant(r), __builtin_amdgcn_frexp_exp(r)};
+}
+__device__ __forceinline__ float times(float v, const Rsqrt &r) {
+    return __builtin_ldexpf(v, r.exponent) * r.mantissa;
 }
 
 // ---- norm ----
@@ -69,7 +108,7 @@ template <int T, int V, bool BF, bool G32>
 __global__ void __launch_bounds__(T < 256 ? 256 : T)
 rms_norm_kernel(NormArgs a) {
     constexpr int kRows = T < 256 ? 256 / T : 1; // rows a workgroup
-    constexpr int kKeep = V ? V : 1;
+    constexpr int kKeep = V ? V : 1, kUnroll = kKeep;
     __shared__ float between[T / 64];
     __shared__ double between64[T / 64];
     const int lane = T < 256 ? threadIdx.x % T : threadIdx.x;
@@ -91,7 +130,7 @@ rms_norm_kernel(NormArgs a) {
         }
     };
     float squares = 0.0f;
-#pragma unroll
+#pragma unroll kUnroll
     for (int i = 0; i < (V ? V : pieces); ++i) {
         load(i, keep[V ? i : 0]);
 #pragma unroll
@@ -99,19 +138,19 @@ rms_norm_kernel(NormArgs a) {
             squares = __builtin_fmaf(keep[V ? i : 0][j], keep[V ? i : 0][j], squares);
     }
     squares = sum_all<T>(squares, between);
-    float r = 1.0f / sqrtf(squares / (float)a.cols + a.eps);
-    double r64 = 0.0;
-    const bool fits = in_range(squares, a.eps, a.cols);
-    if (!fits) {
+    Rsqrt r = split(1.0f / sqrtf(squares / (float)a.cols + a.eps));
+    if (!in_range(squares, a.eps, a.cols)) {
         double d = 0.0;
+#pragma unroll 1
         for (int i = 0; i < pieces; ++i) {
             float f[kWide];
             load(i, f);
+#pragma unroll
             for (int j = 0; j < kWide; ++j) d += (double)f[j] * (double)f[j];
         }
-        r64 = 1.0 / sqrt(sum_all<T>(d, between64) / (double)a.cols + (double)a.eps);
+        r = split(1.0 / sqrt(sum_all<T>(d, between64) / (double)a.cols + (double)a.eps));
     }
-#pragma unroll
+#pragma unroll kUnroll
     for (int i = 0; i < (V ? V : pieces); ++i) {
         const int c = (i * T + lane) * kWide, valid = a.cols - c;
         float f[kWide], g[kWide];
@@ -124,12 +163,8 @@ rms_norm_kernel(NormArgs a) {
         if (a.sum && valid > 0)
             store8(static_cast<uint16_t *>(a.sum) + row * a.ldsum + c, narrow<BF>(f), valid);
         load_gain<BF, G32>(a.gain, c, valid, g);
-        if (fits) {
 #pragma unroll
-            for (int j = 0; j < kWide; ++j) f[j] = f[j] * r * g[j];
-        } else {
-            for (int j = 0; j < kWide; ++j) f[j] = (float)((double)f[j] * r64 * (double)g[j]);
-        }
+        for (int j = 0; j < kWide; ++j) f[j] = times(f[j], r) * g[j];
         if (valid < kWide)
 #pragma unroll
             for (int j = 0; j < kWide; ++j) f[j] = j < valid ? f[j] : 0.0f;
@@ -151,49 +186,77 @@ rms_norm_kernel(NormArgs a) {
 template <int T, int V, bool BF, bool G32>
 __global__ void __launch_bounds__(T)
 rms_norm_backward_kernel(NormBackwardArgs a) {
-    constexpr int kKeep = V ? V : 1;
-    __shared__ float between[T / 64], between2[T / 64];
+    constexpr int kKeep = V ? V : 1, kUnroll = kKeep;
+    __shared__ float2 between[2][T / 64];
     __shared__ double between64[T / 64], between642[T / 64];
     const int lane = threadIdx.x;
     const int pieces = V ? V : (a.cols + T * kWide - 1) / (T * kWide);
     float *part = a.part ? a.part + (int64_t)blockIdx.x * a.cols : nullptr;
     float dg[kKeep][kWide] = {};
     bool first = true;
+    int turn = 0;
+    u32x4 s8[kKeep], y8[kKeep], d8[kKeep], sn[kKeep], yn[kKeep], dn[kKeep];
+    constexpr bool kAhead = V > 0 && T < 1024;   // by a row, where there are registers for it
+    auto load_row = [&](int64_t row) {
+        const uint16_t *sp = static_cast<const uint16_t *>(a.s) + row * a.lds;
+        const uint16_t *yp = static_cast<const uint16_t *>(a.dy) + row * a.lddy;
+        const uint16_t *dp = static_cast<const uint16_t *>(a.ds) + row * a.ldds;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * T + lane) * kWide, valid = a.cols - c;
+            sn[i] = load8(sp + c, valid);
+            yn[i] = load8(yp + c, valid);
+            dn[i] = a.ds ? load8(dp + c, valid) : u32x4{0u, 0u, 0u, 0u};
+        }
+    };
+    if (kAhead) load_row(blockIdx.x);
     for (int64_t row = blockIdx.x; row < a.n; row += a.parts) {
         const uint16_t *sp = static_cast<const uint16_t *>(a.s) + row * a.lds;
         const uint16_t *yp = static_cast<const uint16_t *>(a.dy) + row * a.lddy;
-        u32x4 s8[kKeep], y8[kKeep];
-        float squares = 0.0f, dot = 0.0f;
+        const uint16_t *dp = static_cast<const uint16_t *>(a.ds) + row * a.ldds;
+        if (V) {
+            if (!kAhead) load_row(row);
 #pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s8[i] = sn[i];
+                y8[i] = yn[i];
+                d8[i] = dn[i];
+            }
+            if (kAhead && row + a.parts < a.n) load_row(row + a.parts);
+        }
+        // (V = 0: read where they are used, twice)
+        auto piece = [&](int i, int c, int valid, float (&s)[kWide], float (&y)[kWide],
+                         float (&g)[kWide]) {
+            load_gain<BF, G32>(a.gain, c, valid, g);
+            widen<BF>(V ? s8[V ? i : 0] : load8(sp + c, valid), s);
+            widen<BF>(V ? y8[V ? i : 0] : load8(yp + c, valid), y);
+        };
+        float squares = 0.0f, dot = 0.0f;
+#pragma unroll kUnroll
         for (int i = 0; i < (V ? V : pieces); ++i) {
             const int c = (i * T + lane) * kWide, valid = a.cols - c;
-            u32x4 sv = load8(sp + c, valid), yv = load8(yp + c, valid);
             float s[kWide], y[kWide], g[kWide];
-            load_gain<BF, G32>(a.gain, c, valid, g);
-            widen<BF>(sv, s);
-            widen<BF>(yv, y);
-            s8[V ? i : 0] = sv;
-            y8[V ? i : 0] = yv;
+            piece(i, c, valid, s, y, g);
 #pragma unroll
             for (int j = 0; j < kWide; ++j) {
                 squares = __builtin_fmaf(s[j], s[j], squares);
                 dot = __builtin_fmaf(y[j] * g[j], s[j], dot);
             }
         }
-        squares = sum_all<T>(squares, between);
-        dot = sum_all<T>(dot, between2);
-        const float r = 1.0f / sqrtf(squares / (float)a.cols + a.eps);
-        const float mean = dot * r / (float)a.cols;         // of du u
-        double r64 = 0.0, mean64 = 0.0;
-        const bool fits = in_range(squares, a.eps, a.cols) && magnitude(dot) < 0x7E800000u;
-        if (!fits) {
+        sum_both<T>(squares, dot, between, turn);
+        const float r32 = 1.0f / sqrtf(squares / (float)a.cols + a.eps);
+        Rsqrt r = split(r32);
+        float mean = dot * r32 / (float)a.cols;             // of du u
+        if (!(in_range(squares, a.eps, a.cols) && magnitude(dot) < 0x7E800000u)) {
             double d = 0.0, e = 0.0;
+#pragma unroll 1
             for (int i = 0; i < pieces; ++i) {
                 const int c = (i * T + lane) * kWide, valid = a.cols - c;
                 float s[kWide], y[kWide], g[kWide];
                 load_gain<BF, G32>(a.gain, c, valid, g);
                 widen<BF>(load8(sp + c, valid), s);
                 widen<BF>(load8(yp + c, valid), y);
+#pragma unroll
                 for (int j = 0; j < kWide; ++j) {
                     d += (double)s[j] * (double)s[j];
                     e += (double)y[j] * (double)g[j] * (double)s[j];
@@ -201,36 +264,22 @@ rms_norm_backward_kernel(NormBackwardArgs a) {
             }
             d = sum_all<T>(d, between64);
             e = sum_all<T>(e, between642);
-            r64 = 1.0 / sqrt(d / (double)a.cols + (double)a.eps);
-            mean64 = e * r64 / (double)a.cols;
+            const double r64 = 1.0 / sqrt(d / (double)a.cols + (double)a.eps);
+            r = split(r64);
+            mean = (float)(e * r64 / (double)a.cols);
         }
-#pragma unroll
+#pragma unroll kUnroll
         for (int i = 0; i < (V ? V : pieces); ++i) {
             const int c = (i * T + lane) * kWide, valid = a.cols - c;
             if (valid <= 0) continue;
             float s[kWide], y[kWide], g[kWide], o[kWide], u[kWide];
-            load_gain<BF, G32>(a.gain, c, valid, g);
-            widen<BF>(V ? s8[V ? i : 0] : load8(sp + c, valid), s);
-            widen<BF>(V ? y8[V ? i : 0] : load8(yp + c, valid), y);
-            if (a.ds)
-                widen<BF>(load8(static_cast<const uint16_t *>(a.ds) + row * a.ldds + c, valid), o);
-            else
+            piece(i, c, valid, s, y, g);
+            widen<BF>(V ? d8[V ? i : 0] : a.ds ? load8(dp + c, valid) : u32x4{0u, 0u, 0u, 0u}, o);
 #pragma unroll
-                for (int j = 0; j < kWide; ++j) o[j] = 0.0f;
-            if (fits) {
-#pragma unroll
-                for (int j = 0; j < kWide; ++j) {
-                    u[j] = s[j] * r;
-                    o[j] += r * (y[j] * g[j] - u[j] * mean);
-                    u[j] *= y[j];
-                }
-            } else {
-                for (int j = 0; j < kWide; ++j) {
-                    const double u64 = (double)s[j] * r64;
-                    o[j] = (float)((double)o[j] +
-                                   r64 * ((double)y[j] * (double)g[j] - u64 * mean64));
-                    u[j] = (float)(u64 * (double)y[j]);
-                }
+            for (int j = 0; j < kWide; ++j) {
+                u[j] = times(s[j], r);
+                o[j] += times(y[j] * g[j] - u[j] * mean, r);
+                u[j] *= y[j];
             }
             if (a.dx)
                 store8(static_cast<uint16_t *>(a.dx) + row * a.lddx + c, narrow<BF>(o), valid);
@@ -261,40 +310,66 @@ rms_norm_backward_kernel(NormBackwardArgs a) {
     }
 }
 
-// dgain: the parts of 64 columns by 16 waves, each a sixteenth of them in order.
+// dgain: the parts of 32 columns by a workgroup, eight lanes a part and 128 parts at a time, whose
+// sums are added in two stages; always in the same order.
 template <bool BF, bool G32>
 __global__ void __launch_bounds__(1024)
 gain_sum_kernel(const float *__restrict__ part, int parts, int cols, void *__restrict__ dgain) {
-    __shared__ float between[16][64];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
-    float sum = 0.0f;
-    if (c < cols)
-        for (int p = wv; p < parts; p += 16) sum += part[(int64_t)p * cols + c];
-    between[wv][lane] = sum;
-    __syncthreads();
-    if (wv || c >= cols) return;
-#pragma unroll
-    for (int w = 1; w < 16; ++w) sum += between[w][lane];
-    if (G32)
-        static_cast<float *>(dgain)[c] = sum;
+    __shared__ float between[128][33], again[8][32];
+    const int set = threadIdx.x >> 3, c4 = (threadIdx.x & 7) * 4, c = blockIdx.x * 32 + c4;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c + 4 <= cols)
+        for (int p = set; p < parts; p += 128)
+            sum += *reinterpret_cast<const f32x4u *>(part + (int64_t)p * cols + c);
     else
-        static_cast<uint16_t *>(dgain)[c] = Act<BF>::store(sum);
+        for (int p = set; p < parts; p += 128)
+            for (int i = 0; i < cols - c; ++i) sum[i] += part[(int64_t)p * cols + c + i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) between[set][c4 + i] = sum[i];
+    __syncthreads();
+    const int col = threadIdx.x & 31, sixteen = threadIdx.x >> 5;
+    if (sixteen < 8) {
+        float v = between[16 * sixteen][col];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) v += between[16 * sixteen + i][col];
+        again[sixteen][col] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x >= 32 || (int)blockIdx.x * 32 + col >= cols) return;
+    float v = again[0][col];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += again[i][col];
+    if (G32)
+        static_cast<float *>(dgain)[blockIdx.x * 32 + col] = v;
+    else
+        static_cast<uint16_t *>(dgain)[blockIdx.x * 32 + col] = Act<BF>::store(v);
 }
 
 // ---- blocks ----
-// Activations: 16 lanes a block, as in the norm; 2,048 columns a workgroup.
+// Activations: a lane takes 16 columns and eight lanes a block, so that a wave writes 1 KiB at a
+// time.  A workgroup takes 2^(8 - shift) rows of up to 4,096 columns.  4,096 x 12,288: FIGQ us.
 template <bool BF>
 __global__ void __launch_bounds__(256)
-block_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int cols,
-                      int row_pieces, BlockRowsArgs q) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = i / row_pieces;          // row_pieces is a multiple of 16
-    if (row >= n) return;
-    const int c = (int)(i - row * row_pieces) * kWide;
-    float f[kWide];
-    widen<BF>(load8(x + row * ldx + c, cols - c), f);
-    write_codes(q, row, c, row_pieces / 16, f);
+block_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int cols, int shift,
+                      BlockRowsArgs q) {
+    const int64_t row = ((int64_t)blockIdx.x << (8 - shift)) + (threadIdx.x >> shift);
+    const int c = (int)((blockIdx.y << shift) + (threadIdx.x & ((1 << shift) - 1))) * 16;
+    if (row >= n || c >= blocks_of(cols) * kBlock) return;    // whole blocks' lanes
+    const uint16_t *at = x + row * ldx + c;
+    float f[2][kWide];
+    widen<BF>(load8(at, cols - c), f[0]);
+    widen<BF>(load8(at + kWide, cols - c - kWide), f[1]);
+    uint32_t big = larger(largest8(f[0]), largest8(f[1]));
+    float v = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<1>(v)));
+    v = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<2>(v)));
+    v = __builtin_bit_cast(float, big);
+    big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<4>(v)));
+    const CodeScale s = code_scale(big);
+    const u32x2 lo = to_codes(f[0], s), hi = to_codes(f[1], s);
+    *reinterpret_cast<u32x4 *>(q.q + row * q.ld + c) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    if ((c & (kBlock - 1)) == 0) q.scale[(c / kBlock) * q.lds + row] = s.scale;
 }
 
 // A block of 128 x 128 of a matrix: eight lanes of eight columns a row and 16 lanes a row, 16
@@ -390,22 +465,20 @@ hipError_t backward_v(const NormBackwardArgs &a, hipStream_t stream) {
 #undef EXL3_BACK
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || !a.dgain) return err;
-    hipLaunchKernelGGL((gain_sum_kernel<BF, G32>), dim3((unsigned)((a.cols + 63) / 64)), dim3(1024),
+    hipLaunchKernelGGL((gain_sum_kernel<BF, G32>), dim3((unsigned)((a.cols + 31) / 32)), dim3(1024),
                        0, stream, a.part, a.n > 0 ? a.parts : 0, a.cols, a.dgain);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_rms_norm(const NormArgs &a, bool bf16, int n_cu, hipStream_t stream) {
-    (void)n_cu;
+hipError_t launch_rms_norm(const NormArgs &a, bool bf16, hipStream_t stream) {
     if (bf16) return a.gain32 ? norm_v<true, true>(a, stream) : norm_v<true, false>(a, stream);
     return a.gain32 ? norm_v<false, true>(a, stream) : norm_v<false, false>(a, stream);
 }
 
-int norm_backward_parts(int64_t n, int cols, int n_cu) {
-    (void)cols;
-    return (int)(n < n_cu ? n : n_cu);
+int norm_backward_parts(int64_t n, int n_cu) {
+    return (int)(n < 2 * n_cu ? n : 2 * n_cu);
 }
 
 hipError_t launch_rms_norm_backward(const NormBackwardArgs &a, bool bf16, hipStream_t stream) {
@@ -415,21 +488,23 @@ hipError_t launch_rms_norm_backward(const NormBackwardArgs &a, bool bf16, hipStr
 }
 
 hipError_t launch_block_quantize(const void *x, int64_t ldx, int64_t n, int cols, bool bf16,
-                                 const BlockRowsArgs &out, int n_cu, hipStream_t stream) {
-    (void)n_cu;
-    const int row_pieces = (int)(blocks_of(cols) * (kBlock / kWide));
-    const int64_t per = rows_a_launch(row_pieces);
+                                 const BlockRowsArgs &out, hipStream_t stream) {
+    const int pieces = blocks_of(cols) * (kBlock / 16);
+    int shift = 3;                               // lanes a row, a power of two
+    while (shift < 8 && (1 << shift) < pieces) ++shift;
+    const unsigned across = (unsigned)((pieces + (1 << shift) - 1) >> shift);
+    const int64_t per = rows_a_launch(256) << (8 - shift);
     for (int64_t r0 = 0; r0 < n; r0 += per) {
         const int64_t rows = n - r0 < per ? n - r0 : per;
-        const unsigned grid = (unsigned)((rows * row_pieces + 255) / 256);
+        const dim3 grid((unsigned)((rows + (256 >> shift) - 1) >> (8 - shift)), across);
         const uint16_t *xx = static_cast<const uint16_t *>(x) + r0 * ldx;
         const BlockRowsArgs q{out.q + r0 * out.ld, out.scale + r0, out.ld, out.lds};
         if (bf16)
-            hipLaunchKernelGGL((block_quantize_kernel<true>), dim3(grid), dim3(256), 0, stream, xx,
-                               ldx, rows, cols, row_pieces, q);
+            hipLaunchKernelGGL((block_quantize_kernel<true>), grid, dim3(256), 0, stream, xx, ldx,
+                               rows, cols, shift, q);
         else
-            hipLaunchKernelGGL((block_quantize_kernel<false>), dim3(grid), dim3(256), 0, stream, xx,
-                               ldx, rows, cols, row_pieces, q);
+            hipLaunchKernelGGL((block_quantize_kernel<false>), grid, dim3(256), 0, stream, xx, ldx,
+                               rows, cols, shift, q);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
