@@ -2529,7 +2529,7 @@ int exl3_rms_norm_backward(exl3_ctx *ctx, const void *dy, int64_t lddy, const vo
     a.dx = dx;
     a.lddx = lddx;
     a.dgain = dgain;
-    a.parts = exl3::norm_backward_parts(n, ctx->n_cu);
+    a.parts = exl3::norm_backward_parts(n, cols, ctx->n_cu);
     Carve c;
     if (dgain) c.take((size_t)a.parts * cols * sizeof(float));
     if ((rc = work_space(ctx, c.used)) != EXL3_OK) return rc;

@@ -152,7 +152,7 @@ struct NormBackwardArgs {
     float *part;                                 // [parts][cols]
     int parts;
 };
-int norm_backward_parts(int64_t n, int n_cu);
+int norm_backward_parts(int64_t n, int cols, int n_cu);
 hipError_t launch_rms_norm_backward(const NormBackwardArgs &a, bool bf16, hipStream_t stream);
 
 hipError_t launch_block_quantize(const void *x, int64_t ldx, int64_t n, int cols, bool bf16,

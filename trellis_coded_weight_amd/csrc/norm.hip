@@ -451,10 +451,12 @@ hipError_t backward_v(const NormBackwardArgs &a, hipStream_t stream) {
 #define EXL3_BACK(T, V)                                                                       \
     hipLaunchKernelGGL((rms_norm_backward_kernel<T, V, BF, G32>), grid, dim3(T), 0, stream, a)
     if (a.n > 0) {
-        if (a.cols <= 2048)
+        if (a.cols <= 1024)
+            EXL3_BACK(128, 1);
+        else if (a.cols <= 2048)
             EXL3_BACK(256, 1);
         else if (a.cols <= 4096)
-            EXL3_BACK(256, 2);
+            EXL3_BACK(512, 1);
         else if (a.cols <= 8192)
             EXL3_BACK(512, 2);
         else if (a.cols <= 16384)
@@ -477,8 +479,12 @@ hipError_t launch_rms_norm(const NormArgs &a, bool bf16, hipStream_t stream) {
     return a.gain32 ? norm_v<false, true>(a, stream) : norm_v<false, false>(a, stream);
 }
 
-int norm_backward_parts(int64_t n, int n_cu) {
-    return (int)(n < 2 * n_cu ? n : 2 * n_cu);
+// Workgroups, each with a part of dgain, that write 4 bytes a column more.  A compute unit's, us:
+// 2,000 x 4,096: one 22.9, two 19.8, three 22.4; 4,000 x 1,000: one 29, two 21, four 17.4;
+// 2,000 x 8,192: one 39, two 42.
+int norm_backward_parts(int64_t n, int cols, int n_cu) {
+    const int64_t most = (int64_t)n_cu * (cols <= 1024 ? 4 : cols <= 2048 ? 3 : cols <= 4096 ? 2 : 1);
+    return (int)(n < most ? n : most);
 }
 
 hipError_t launch_rms_norm_backward(const NormBackwardArgs &a, bool bf16, hipStream_t stream) {
