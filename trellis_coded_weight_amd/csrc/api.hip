@@ -2276,9 +2276,21 @@ int check_block_weight(exl3_ctx *ctx, const exl3_block_weight *w, exl3::BlockWei
     return EXL3_OK;
 }
 
-// Up to 32 rows a group W is streamed once into registers.
-bool few_rows(const exl3::BlockWeightArgs &w, bool transpose, int64_t n) {
-    return !transpose && n <= (int64_t)32 * w.groups;
+// Whether W is streamed through registers for few rows (up to 32 a group) or goes through the
+// tiles, whose smallest have 128 columns of the result: those read x less, but take the whole
+// contraction in a chain of two blocks a step.  Estimates in us; both measured, in us: 16 rows,
+// 4096 x 4096: 7.1 and 9.7, 12288 x 4096: 13.7 and 11.4, 4096 x 12288: 14.1 and 22.4; 24 rows,
+// 4096 x 12288: 17.1 and 23.1; 64 experts of 1408 x 2048, 256 rows: 36.9 and 41.0, 512: 45.8 and
+// 41.8, 2,048: 97 and 50; 16 of 2048 x 1408, 64 rows: 13.6 and 11.7.
+bool few_rows(const exl3::BlockWeightArgs &w, bool transpose, int64_t n, int n_cu) {
+    if (transpose || n > (int64_t)32 * w.groups) return false;
+    const double rows = (double)n / w.groups, mb = 1e-6 * w.rows * w.cols * w.groups;
+    const double streamed = 3.5 + mb * (w.groups == 1 ? 0.17 + 0.004 * rows : 0.16 + 0.01 * rows);
+    const double tiles = (w.rows + 127) / 128 * (w.groups == 1 ? 1.0 : n / 32 + 0.5 * w.groups);
+    const double steps = (exl3::blocks_of(w.cols) + 1) / 2;
+    const double tiled =
+        3.2 + std::max(0.44 * steps * std::max(1.0, tiles / n_cu), mb / 4.9);
+    return streamed < tiled;
 }
 
 // Whether its workgroups write 16-bit rows as blocks themselves, each all that it needs, in place
@@ -2297,7 +2309,7 @@ int run_block_product(exl3_ctx *ctx, const exl3::BlockWeightArgs &w,
                       bool bf16) {
     if (x && !a.x16)
         EXL3_HIP(ctx, exl3::launch_block_quantize(x, ldx, a.n, in, bf16, a.x, ctx->stream));
-    if (few_rows(w, a.transposed, a.n))
+    if (a.x16 || few_rows(w, a.transposed, a.n, ctx->n_cu))
         EXL3_HIP(ctx, exl3::launch_block_rows(w, a, bf16, ctx->stream));
     else {
         const hipError_t err = exl3::launch_block_gemm(w, a, bf16, ctx->n_cu, ctx->stream);
@@ -2338,7 +2350,7 @@ int block_linear_any(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *o
     Carve c;
     size_t q_at = 0, s_at = 0;
     const size_t blocks = (size_t)exl3::blocks_of(in);
-    const bool own = x && few_rows(wa, transpose != 0, n) && own_rows(wa, n, ctx->n_cu);
+    const bool own = x && !transpose && own_rows(wa, n, ctx->n_cu);
     if (own) {
         a.x16 = x;
         a.ldx16 = ldx;
