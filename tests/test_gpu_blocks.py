@@ -480,9 +480,11 @@ def test_differentiable_products(T, ctx):
                         torch.stack([s, 2 * s]).cuda())
     xg = x.detach().reshape(24, 256).requires_grad_()
     T.block_grouped_linear(ctx, xg, two, off).backward(dy)
-    got = xg.grad.double().cpu()
-    one = x.grad.reshape(24, 256).double().cpu()
-    assert torch.equal(got[:10], one[:10]) and torch.equal(got[10:], 2 * one[10:])
+    # (against the formula: a single matrix and groups may add a contraction's blocks in another
+    # order, each within the same bound)
+    ref = from_blocks(dq, ds)
+    check_product(xg.grad[:10], ref[:10], dense.t(), BF, 300)
+    check_product(xg.grad[10:], ref[10:], 2 * dense.t(), BF, 300)
 
 
 LONG = [(3, 40, 9000), (20, 40, 20000), (40, 70, 20000), (200, 260, 17000), (300, 1100, 8200)]
@@ -502,8 +504,9 @@ def test_long_contractions(T, ctx, n, m, k, back):
 
 
 # sizes at which each of the tiles is chosen (one matrix), by rows and result columns
-TILES = [(4096, 4096, 130), (1500, 4096, 257), (1800, 4100, 128), (1000, 4096, 300), (500, 4097, 200),
-         (150, 4096, 390)]
+TILES = [(4096, 4096, 1030), (1500, 4096, 1300), (3840, 2176, 900), (1000, 4096, 1100),
+         (500, 4096, 1200), (150, 4096, 1390), (100, 4096, 2000), (60, 4096, 1500),
+         (1800, 4100, 128)]
 
 
 @pytest.mark.parametrize("back", [False, True])
@@ -576,3 +579,62 @@ def test_more_groups_than_a_launch_holds(T, ctx):
     offsets[E - 50:] = torch.cat([torch.arange(0, 50), torch.tensor([n])]).int().cuda()
     y = ctx.block_grouped_linear(x, w, offsets)
     assert torch.equal(y, x[:, :1].expand(n, rows))
+
+
+def test_subnormal_codes_count(T, ctx):
+    """Codes below e4m3's normal range, in W and in x."""
+    for n in (2, 40, 300):
+        q = torch.full((200, 256), 3.0 * 2.0 ** -9).to(E4M3)
+        xq = torch.full((n, 256), 2.0 ** -9).to(E4M3)
+        one, xs = torch.ones(2, 2), torch.ones(n, 2)
+        y = ctx.block_linear(T.BlockRows(xq.cuda(), xs.cuda()), T.BlockWeight(q.cuda(), one.cuda()))
+        assert (y.float() == 256 * 3.0 * 2.0 ** -18).all()
+
+
+def test_a_capture_that_would_grow_the_workspace_is_refused_and_goes_on(T):
+    q, s = matrix(260, 384, 111)
+    w = T.BlockWeight(q.cuda(), s.cuda())
+    x, _ = rows_of(300, 384, BF, 112)
+    rows = torch.zeros(4, device="cuda")
+    with T.Context(0) as c:
+        c.rms_norm(x, torch.ones(384, dtype=BF, device="cuda"))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            rows += 1
+            with pytest.raises(T.Exl3Error) as e:
+                c.block_linear(x, w)
+        assert e.value.code == T.EXL3_ENOMEM
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (rows == 1).all()
+        assert torch.isfinite(c.block_linear(x, w)).all()
+        torch.cuda.synchronize()
+        del graph
+
+
+def test_two_products_in_one_graph_and_two_contexts_at_once(T):
+    """Calls that share a context's workspace run one after the other; contexts do not meet."""
+    q, s = matrix(520, 1024, 121)
+    w = T.BlockWeight(q.cuda(), s.cuda())
+    xs = [rows_of(n, 1024, BF, 122 + n)[0] for n in (200, 33)]
+    with T.Context(0) as a, T.Context(0) as b:
+        want = [a.block_linear(x, w) for x in xs]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        got = [[], []]
+        for _ in range(4):
+            for i, c in enumerate((a, b)):
+                with torch.cuda.stream(streams[i]):
+                    got[i].append([c.block_linear(x, w) for x in xs])
+        torch.cuda.synchronize()
+        for side in got:
+            for pair in side:
+                assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+        # one context on two streams by turns
+        for turn in range(4):
+            with torch.cuda.stream(streams[turn % 2]):
+                y = a.block_linear(xs[0], w)
+                z = a.block_linear(xs[1], w)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(z, want[1])

@@ -2276,17 +2276,16 @@ int check_block_weight(exl3_ctx *ctx, const exl3_block_weight *w, exl3::BlockWei
     return EXL3_OK;
 }
 
-// Whether W is streamed through registers for few rows (up to 32 a group) or goes through the
-// tiles, whose smallest have 128 columns of the result: those read x less, but take the whole
-// contraction in a chain of two blocks a step.  Estimates in us; both measured, in us: 16 rows,
-// 4096 x 4096: 7.1 and 9.7, 12288 x 4096: 13.7 and 11.4, 4096 x 12288: 14.1 and 22.4; 24 rows,
-// 4096 x 12288: 17.1 and 23.1; 64 experts of 1408 x 2048, 256 rows: 36.9 and 41.0, 512: 45.8 and
-// 41.8, 2,048: 97 and 50; 16 of 2048 x 1408, 64 rows: 13.6 and 11.7.
+// Whether experts' matrices are streamed through registers for few rows each (up to 16), or go
+// through the tiles, whose smallest for them have 128 columns of the result by 32 rows.  A single
+// matrix goes through tiles, the smallest of 32 x 32 (or is streamed as below).  Estimates in us,
+// of both as measured: 64 experts of 1408 x 2048, 64 rows: 25.4 and 26.7, 256: 36.9 and 41.0, 512:
+// 45.8 and 41.8; 16 of 2048 x 1408, 16 rows: 9.8 and 9.4, 64: 13.6 and 11.7.
 bool few_rows(const exl3::BlockWeightArgs &w, bool transpose, int64_t n, int n_cu) {
-    if (transpose || n > (int64_t)32 * w.groups) return false;
+    if (transpose || w.groups == 1 || n > (int64_t)16 * w.groups) return false;
     const double rows = (double)n / w.groups, mb = 1e-6 * w.rows * w.cols * w.groups;
-    const double streamed = 3.5 + mb * (w.groups == 1 ? 0.17 + 0.004 * rows : 0.16 + 0.01 * rows);
-    const double tiles = (w.rows + 127) / 128 * (w.groups == 1 ? 1.0 : n / 32 + 0.5 * w.groups);
+    const double streamed = 3.5 + mb * (0.16 + 0.01 * rows);
+    const double tiles = (w.rows + 127) / 128 * (n / 32 + 0.5 * w.groups);
     const double steps = (exl3::blocks_of(w.cols) + 1) / 2;
     const double tiled =
         3.2 + std::max(0.44 * steps * std::max(1.0, tiles / n_cu), mb / 4.9);

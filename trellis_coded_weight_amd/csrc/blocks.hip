@@ -97,7 +97,8 @@ struct GemmArgs {
 // wave's 32 lanes read at a time into different banks.
 template <int BM>
 __device__ __forceinline__ int turned_slot(int row) {
-    return BM == 256 ? (row & 7) | (row >> 4 & 1) << 3 : (row >> 1 & 3) | (row >> 4 & 1) << 2;
+    constexpr int kSame = BM == 256 ? 1 : BM == 128 ? 2 : BM == 64 ? 4 : 8;   // rows in 256 bytes
+    return (row & 7) / kSame | (row >> 4 & 1) * (8 / kSame);
 }
 
 template <int BM, int BN, int WM, int WN, int WK, int RING, int SPREAD, bool BF, bool TR>
@@ -114,7 +115,7 @@ block_gemm_kernel(const uint8_t *__restrict__ w, const float *__restrict__ w_sca
     constexpr int kPitch = SM * 2 + 16;                   // bytes a row of y takes in the epilogue
     static_assert(SN <= 64 && SM <= 128 && 128 % SM == 0, "a wave's scales");
     static_assert(SPREAD < TM || (SPREAD == TM && RING > 2), "a slice's loads precede its wait");
-    static_assert(TM % 2 == 0 && (!TR || BM == 256 || BM == 128), "two places for rows of W");
+    static_assert(TM % 2 == 0, "two places for rows of W");
     static_assert((WK - 1) * BM * BN * 4 + WM * WN * 16 * kPitch <= WK * RING * kSlice,
                   "the sets' sums and the epilogue fit the rings");
     // (one array: with two, the compiler takes waits between them)
@@ -392,10 +393,12 @@ block_gemm_kernel(const uint8_t *__restrict__ w, const float *__restrict__ w_sca
 // ---- few rows ----
 // A workgroup takes 16 rows of W, its waves the blocks of the contraction in turn, so that
 // neighbouring waves read neighbouring lines; what they hold of W goes from memory straight into
-// operands, CH blocks at a time in NB sets.  Rows of x meet it 16 TN at a time, and the waves' sums are added in
+// operands, CH blocks at a time.  Rows of x meet it 16 at a time, and the waves' sums are added in
 // order through shared memory.
 // OWN: x comes in 16 bits and each workgroup writes the rows it needs as blocks in shared memory
-// (P rows at a time, as fit), while its first loads of W are on their way.
+// (own_rows at a time, as fit), while its first loads of W are on their way.
+// 1 row, 12288 x 4096: 12 us, 4.2 TB/s, in one launch; bound by the loads of W, of which all are
+// under way at once, and the launch's start and end.
 struct RowsKernelArgs {
     GemmArgs p;
     const uint16_t *x16;
@@ -403,12 +406,11 @@ struct RowsKernelArgs {
     int own_rows;                                // OWN: rows a pass
     int group0;                                  // the first of this launch
 };
-template <int TN, int WAVES, int CH, int NB, bool BF, bool OWN>
+template <int WAVES, int CH, bool BF, bool OWN>
 __global__ void __launch_bounds__(64 * WAVES)
 block_rows_kernel(RowsKernelArgs a) {
     const GemmArgs &p = a.p;
-    constexpr int kTok = 16 * TN;
-    __shared__ float part[WAVES][kTok][16];
+    __shared__ float part[WAVES][16][16];
     extern __shared__ __align__(16) uint8_t own[];
     const int lane = threadIdx.x & 63, wv = wave_number();
     const int r = lane & 15, g = lane >> 4;
@@ -425,104 +427,79 @@ block_rows_kernel(RowsKernelArgs a) {
     const int steps = (p.blocks + WAVES - 1) / WAVES;
     const int pitch = p.blocks * kBlock + 16;    // OWN: a row of codes in shared memory
     float *own_scale = reinterpret_cast<float *>(own + a.own_rows * pitch);
-    const int take = OWN ? a.own_rows : kTok;    // rows of x a pass
-    constexpr int XB = OWN ? 1 : NB;             // of shared memory nothing is held ahead
-    Operand w[NB][CH], x[XB][OWN ? 1 : CH][TN];
-    float xs[XB][OWN ? 1 : CH][TN];
-    auto load_w = [&](int at, int s0) {
+    const int take = OWN ? a.own_rows : 16;      // rows of x a pass
+    Operand w[CH], x[OWN ? 1 : CH];
+    float xs[OWN ? 1 : CH];
+    auto load_w = [&](int s0) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             int b = (s0 + c) * WAVES + wv;
             b = b < p.blocks ? b : p.blocks - 1;
             const u32x4 *from = reinterpret_cast<const u32x4 *>(w_at + (int64_t)b * kBlock);
-            w[at][c].a = from[0];
-            w[at][c].b = from[4];
+            w[c].a = from[0];
+            w[c].b = from[4];
         }
     };
     for (int64_t t0 = lo; t0 < hi; t0 += take) {
-        const int here = (int)(hi - t0 < take ? hi - t0 : take);
-        auto load_x1 = [&](int b, Operand (&xo)[TN], float (&so)[TN]) {
+        const int here = (int)(hi - t0 < take ? hi - t0 : take), t = r < here ? r : here - 1;
+        auto load_x1 = [&](int b, Operand &to, float &scale) {
             b = b < p.blocks ? b : p.blocks - 1;
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int t = 16 * j + r < here ? 16 * j + r : here - 1;
-                const uint8_t *xp = OWN ? own + t * pitch + b * kBlock + 16 * g
-                                        : p.x + (t0 + t) * p.ldx + (int64_t)b * kBlock + 16 * g;
-                xo[j].a = *reinterpret_cast<const u32x4 *>(xp);
-                xo[j].b = *reinterpret_cast<const u32x4 *>(xp + 64);
-                so[j] = OWN ? own_scale[b * a.own_rows + t] : p.xs[(int64_t)b * p.ldxs + t0 + t];
-            }
+            const uint8_t *xp = OWN ? own + t * pitch + b * kBlock + 16 * g
+                                    : p.x + (t0 + t) * p.ldx + (int64_t)b * kBlock + 16 * g;
+            to.a = *reinterpret_cast<const u32x4 *>(xp);
+            to.b = *reinterpret_cast<const u32x4 *>(xp + 64);
+            scale = OWN ? own_scale[b * a.own_rows + t] : p.xs[(int64_t)b * p.ldxs + t0 + t];
         };
-        auto load_x = [&](int at, int s0) {
+        auto load_x = [&](int s0) {              // of shared memory nothing is held ahead
             if (!OWN)
 #pragma unroll
-                for (int c = 0; c < CH; ++c) load_x1((s0 + c) * WAVES + wv, x[at][c], xs[at][c]);
+                for (int c = 0; c < CH; ++c) load_x1((s0 + c) * WAVES + wv, x[c], xs[c]);
         };
-        load_x(0, 0);
-        load_w(0, 0);
+        load_x(0);
+        load_w(0);
         if (OWN) {
             const int pieces = p.blocks * (kBlock / kWide);
             if (t0 != lo) __syncthreads();       // the last pass has read its codes
             for (int i = threadIdx.x; i < here * pieces; i += 64 * WAVES) {
-                const int t = i / pieces, c = (i - t * pieces) * kWide;
+                const int row = i / pieces, c = (i - row * pieces) * kWide;
                 float f[kWide];
-                widen<BF>(load8(a.x16 + (t0 + t) * a.ldx16 + c, p.k - c), f);
+                widen<BF>(load8(a.x16 + (t0 + row) * a.ldx16 + c, p.k - c), f);
                 const CodeScale s = code_scale(largest_of_block(largest8(f)));
-                *reinterpret_cast<u32x2 *>(own + t * pitch + c) = to_codes(f, s);
-                if ((c & (kBlock - 1)) == 0) own_scale[(c / kBlock) * a.own_rows + t] = s.scale;
+                *reinterpret_cast<u32x2 *>(own + row * pitch + c) = to_codes(f, s);
+                if ((c & (kBlock - 1)) == 0) own_scale[(c / kBlock) * a.own_rows + row] = s.scale;
             }
             __syncthreads();
         }
-        f32x4 acc[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        auto products = [&](int at, int s0) {
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < steps; s += CH) {
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const int b = (s0 + c) * WAVES + wv;
+                const int b = (s + c) * WAVES + wv, cx = OWN ? 0 : c;
                 if (b >= p.blocks) continue;     // the same for the whole wave
-                const float ws = ws_at[b];
-                if (OWN) load_x1(b, x[0][0], xs[0][0]);
+                if (OWN) load_x1(b, x[0], xs[0]);
+                const f32x4 z = block_product(w[c], x[cx]);
+                const float f = xs[cx] * ws_at[b];
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const int ax = OWN ? 0 : at, cx = OWN ? 0 : c;
-                    const f32x4 z = block_product(w[at][c], x[ax][cx][j]);
-                    const float f = xs[ax][cx][j] * ws;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_fmaf(z[i], f, acc[j][i]);
-                }
+                for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(z[i], f, acc[i]);
             }
-        };
-        for (int s = 0; s < steps; s += NB * CH) {
-            if (NB == 2 && s + CH < steps) {
-                load_x(NB - 1, s + CH);
-                load_w(NB - 1, s + CH);
+            if (s + CH < steps) {
+                load_x(s + CH);
+                load_w(s + CH);
             }
-            products(0, s);
-            if (s + NB * CH < steps) {
-                load_x(0, s + NB * CH);
-                load_w(0, s + NB * CH);
-            }
-            if (NB == 2 && s + CH < steps) products(NB - 1, s + CH);
         }
         if (t0 != lo) __syncthreads();           // the last pass's sums have been read
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            *reinterpret_cast<f32x4 *>(&part[wv][16 * j + r][4 * g]) = acc[j];
+        *reinterpret_cast<f32x4 *>(&part[wv][r][4 * g]) = acc;
         __syncthreads();
-        for (int i = threadIdx.x; i < kTok * 16; i += 64 * WAVES) {
-            const int t = i / 16, m = i % 16;
-            float sum = part[0][t][m];
+        if (threadIdx.x < 256) {
+            const int row = threadIdx.x / 16, m = threadIdx.x % 16;
+            float sum = part[0][row][m];
 #pragma unroll
-            for (int v = 1; v < WAVES; ++v) sum += part[v][t][m];
-            if (t < here && m0 + m < p.m) p.y[(t0 + t) * p.ldy + m0 + m] = Act<BF>::store(sum);
+            for (int v = 1; v < WAVES; ++v) sum += part[v][row][m];
+            if (row < here && m0 + m < p.m)
+                p.y[(t0 + row) * p.ldy + m0 + m] = Act<BF>::store(sum);
         }
     }
 }
-
-}  // namespace
-
-namespace {
 
 GemmArgs gemm_args(const BlockWeightArgs &w, const BlockProductArgs &a) {
     GemmArgs p{};
@@ -553,49 +530,42 @@ hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a
     r.p.m_tiles = (r.p.m + 15) / 16;
     r.x16 = static_cast<const uint16_t *>(a.x16);
     r.ldx16 = a.ldx16;
-    const int64_t avg = (a.n + w.groups - 1) / w.groups;
     size_t shared = 0;
     if (a.x16) {
         const size_t row = (size_t)r.p.blocks * kBlock + 16 + (size_t)r.p.blocks * 4;
         r.own_rows = (int)std::min<size_t>(16, std::max<size_t>(1, kOwnBytes / row));
         shared = r.own_rows * row;
     }
-#define EXL3_ROWS_T(TN, WAVES, CH, NB, BF, OWN)                                                 \
-    hipLaunchKernelGGL((block_rows_kernel<TN, WAVES, CH, NB, BF, OWN>), dim3(grid),             \
-                       dim3(64 * WAVES), shared, stream, r)
-#define EXL3_ROWS(TN, WAVES, CH, NB, OWN)                  \
-    do {                                                   \
-        if (bf16)                                          \
-            EXL3_ROWS_T(TN, WAVES, CH, NB, true, OWN);     \
-        else                                               \
-            EXL3_ROWS_T(TN, WAVES, CH, NB, false, OWN);    \
+#define EXL3_ROWS_T(WAVES, CH, BF, OWN)                                                          \
+    hipLaunchKernelGGL((block_rows_kernel<WAVES, CH, BF, OWN>), dim3(grid), dim3(64 * WAVES),    \
+                       shared, stream, r)
+#define EXL3_ROWS(WAVES, CH)                   \
+    do {                                       \
+        if (a.x16 && bf16)                     \
+            EXL3_ROWS_T(WAVES, CH, true, true); \
+        else if (a.x16)                        \
+            EXL3_ROWS_T(WAVES, CH, false, true); \
+        else if (bf16)                         \
+            EXL3_ROWS_T(WAVES, CH, true, false); \
+        else                                   \
+            EXL3_ROWS_T(WAVES, CH, false, false); \
     } while (0)
     // The waves and what each has under way, by the contraction's blocks, us:
     //   16 blocks (64 experts of 1408 x 2048, 64 rows): 8 waves of two blocks 25, 8 of four 47,
     //   16 of two 43 (idle waves still take their places)
-    //   32 (12288 x 4096, 1 row, own): 8 of four 12.1, 16 of two 12.5, 8 of two 16.6; 16 rows:
-    //   16.4, 13.5 and 15.9
+    //   32 (12288 x 4096, 1 row, own): 8 of four 12.1, 16 of two 12.5, 8 of two 16.6
     //   96 (4096 x 12288, 16 rows): 16 of two 14.0, 8 of four 14.4, 8 of two 15.0
     const int blocks = r.p.blocks;
     // a launch has fewer than 2^32 lanes, of up to 1,024 a workgroup
     const int per = std::max(1, (1 << 21) / r.p.m_tiles);
     for (r.group0 = 0; r.group0 < w.groups; r.group0 += per) {
         const unsigned grid = (unsigned)(r.p.m_tiles * std::min(per, w.groups - r.group0));
-        if (a.x16) {
-            if (blocks <= 16)
-                EXL3_ROWS(1, 8, 2, 1, true);
-            else if (blocks <= 32)
-                EXL3_ROWS(1, 8, 4, 1, true);
-            else
-                EXL3_ROWS(1, 16, 2, 1, true);
-        } else if (avg <= 16) {
-            if (blocks <= 16)
-                EXL3_ROWS(1, 8, 2, 1, false);
-            else
-                EXL3_ROWS(1, 16, 2, 1, false);
-        } else {
-            EXL3_ROWS(2, 8, 1, 2, false);
-        }
+        if (blocks <= 16)
+            EXL3_ROWS(8, 2);
+        else if (blocks <= 32)
+            EXL3_ROWS(8, 4);
+        else
+            EXL3_ROWS(16, 2);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
@@ -628,23 +598,31 @@ hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a
         else                                                                                   \
             EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, false, false);                      \
     } while (0)
-    // What a round of tiles takes at k = 4096, us, one or (128 x 128 with a ring of two) two tiles a
-    // compute unit: measured for 4,096 columns at n = 200 (128 x 32: 11.3, 128 x 64: 12.6), 512
-    // (21.4, 14.2, 128 x 128: 19.6), 1,024 (27 in two rounds of 128 x 64, 128 x 128: 21.9, 256 x 128:
-    // 26.3), 2,000 (128 x 128 twice a unit: 36, 256 x 128: 34, 256 x 256: 43), 12,288 columns at n =
-    // 4,096 (three rounds of 256 x 256: 167, six of 256 x 128: 199).  Experts' tiles: each group's
-    // last is half empty on average, and rounds run into one another.
-    enum { kHuge, kLarge, kTwice, kMedium, kSmall, kSmallest };
-    auto cost = [&](int bm, int bn, int places, double us) {
-        const double m_tiles = (p.m + bm - 1) / bm;
-        if (a.offsets)
-            return us * std::max(1.0, m_tiles * ((double)a.n / bn + 0.5 * w.groups) / (places * n_cu));
-        return us * std::ceil(m_tiles * (double)((a.n + bn - 1) / bn) / (places * n_cu));
+    // What a step of a round takes, us (a tile a compute unit, but two of kTwice; WK blocks a step),
+    // from calls of 4,096 columns from 4,096 with 64 rows (32 x 32: 7.4), 128 (64 x 32: 8.5), 200
+    // (128 x 32: 11.3), 512 (128 x 64: 14.2), 1,024 (128 x 128: 21.9; two rounds of 128 x 64: 27),
+    // 2,000 (256 x 128: 33; 128 x 128, two a unit: 36) and of 12,288 with 4,096 rows (three rounds
+    // of 256 x 256: 167; six of 256 x 128: 199); some 3 us of each are not in steps.  The contraction
+    // in four sets where tiles are few: 4,096 columns from 12,288, 24 rows: 11.8, 128 x 32 in two
+    // sets: 23.  Experts' tiles: each group's last is half empty on average, and rounds run into
+    // one another.
+    enum { kHuge, kLarge, kTwice, kMedium, kSmall, kSmallest, kThin, kThinnest, kForms };
+    auto cost = [&](int bm, int bn, int wk, int places, double us) {
+        const double m_tiles = (p.m + bm - 1) / bm, steps = (p.blocks + wk - 1) / wk;
+        if (m_tiles * ((double)a.n / bn + w.groups) >= (double)(1 << 23)) return 1e30;
+        if (!a.offsets)
+            return us * steps * std::ceil(m_tiles * (double)((a.n + bn - 1) / bn) / (places * n_cu));
+        // (16 of 2048 x 1408, 64 rows: 128 x 32 11.6, 64 x 32 15.2, 32 x 32 21.7)
+        if (bm < 128) return 1e30;
+        return us * steps *
+               std::max(1.0, m_tiles * ((double)a.n / bn + 0.5 * w.groups) / (places * n_cu));
     };
-    const double costs[6] = {cost(256, 256, 1, 55), cost(256, 128, 1, 33), cost(128, 128, 2, 34),
-                             cost(128, 128, 1, 21), cost(128, 64, 1, 14),  cost(128, 32, 1, 11)};
+    const double costs[kForms] = {
+        cost(256, 256, 1, 1, 1.7), cost(256, 128, 1, 1, 1.0), cost(128, 128, 1, 2, 1.03),
+        cost(128, 128, 1, 1, 0.6), cost(128, 64, 2, 1, 0.83), cost(128, 32, 2, 1, 0.67),
+        cost(64, 32, 4, 1, 0.78),  cost(32, 32, 4, 1, 0.5)};
     int best = 0;
-    for (int i = 1; i < 6; ++i)
+    for (int i = 1; i < kForms; ++i)
         if (costs[i] < costs[best]) best = i;
     switch (best) {
         case kHuge: EXL3_BLOCK(256, 256, 2, 4, 1, 2, 4); break;
@@ -652,7 +630,9 @@ hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a
         case kTwice: EXL3_BLOCK(128, 128, 2, 2, 1, 2, 1); break;
         case kMedium: EXL3_BLOCK(128, 128, 2, 2, 1, 4, 4); break;
         case kSmall: EXL3_BLOCK(128, 64, 2, 2, 2, 3, 4); break;
-        default: EXL3_BLOCK(128, 32, 2, 2, 2, 3, 4);
+        case kSmallest: EXL3_BLOCK(128, 32, 2, 2, 2, 3, 4); break;
+        case kThin: EXL3_BLOCK(64, 32, 1, 1, 4, 3, 4); break;
+        default: EXL3_BLOCK(32, 32, 1, 1, 4, 4, 2);
     }
 #undef EXL3_BLOCK
 #undef EXL3_BLOCK_T
