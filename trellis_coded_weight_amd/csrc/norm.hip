@@ -103,7 +103,10 @@ __device__ __forceinline__ float times(float v, const Rsqrt &r) {
 // y = s r gain with r = 1 / sqrt(mean(s^2) + eps) and s = x + residual in binary32, before its
 // rounding to the stored sum.  A row by T lanes, T / 64 waves; each lane keeps V pieces of eight
 // columns.  V = 0: rows too wide for that, which are read twice.  Where the squares leave
-// binary32's range the row is summed again in binary64.
+// binary32's range the row is summed again in binary64.  Roundings: s to its stored type, y once
+// to its type, or its quotient by the block's scale to binary32 and then e4m3.
+// 8,200 x 4,096, bfloat16, residual and blocks: 43 us, 5.4 TB/s where a large copy reaches 4.88;
+// 1 x 4,096: 2.9 us, the rest of a call's 14.5 is the host's.
 template <int T, int V, bool BF, bool G32>
 __global__ void __launch_bounds__(T < 256 ? 256 : T)
 rms_norm_kernel(NormArgs a) {
@@ -182,7 +185,10 @@ rms_norm_kernel(NormArgs a) {
 // A workgroup takes rows blockIdx.x, + parts, ..: one pass over each gives both sums, and the
 // gain's gradient of its columns stays in registers until the rows are done.  The parts are
 // added in order by a second kernel, so no result depends on scheduling.  V = 0: columns too many
-// for registers; dgain goes through the part in memory.
+// for registers; dgain goes through the part in memory.  The next row's loads go out before this
+// one's sums, whose barrier they would else wait behind: 2,000 x 4,096 with ds: 17.6 us,
+// then 3.8 for the parts, 19.4 a call (13.4 the floor); 25.8 and 5.0 with this row's loads behind
+// the last one's sums, 256 lanes a row and one workgroup a compute unit.  8,200 rows: 58.5 (55).
 template <int T, int V, bool BF, bool G32>
 __global__ void __launch_bounds__(T)
 rms_norm_backward_kernel(NormBackwardArgs a) {
@@ -347,7 +353,8 @@ gain_sum_kernel(const float *__restrict__ part, int parts, int cols, void *__res
 
 // ---- blocks ----
 // Activations: a lane takes 16 columns and eight lanes a block, so that a wave writes 1 KiB at a
-// time.  A workgroup takes 2^(8 - shift) rows of up to 4,096 columns.  4,096 x 12,288: FIGQ us.
+// time.  A workgroup takes 2^(8 - shift) rows of up to 4,096 columns.  4,096 x 12,288: 28.7 us, 5.3
+// TB/s; 8,200 x 2,048: 11.2 (12.9 with eight columns a lane and a division for the row).
 template <bool BF>
 __global__ void __launch_bounds__(256)
 block_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, int cols, int shift,
@@ -372,8 +379,8 @@ block_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, in
     if ((c & (kBlock - 1)) == 0) q.scale[(c / kBlock) * q.lds + row] = s.scale;
 }
 
-// A block of 128 x 128 of a matrix: eight lanes of eight columns a row and 16 lanes a row, 16
-// rows at a time.
+// A block of 128 x 128 of a matrix: 16 lanes of eight columns a row, 16 rows at a time, all held
+// until the largest is known.  12,288 x 4,096, bfloat16: 27.4 us, 5.5 TB/s.
 template <int TYPE>
 __global__ void __launch_bounds__(256)
 block_quantize_weight_kernel(const void *__restrict__ w, int64_t ldw, int rows, int cols,
