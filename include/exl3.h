@@ -596,7 +596,8 @@ int exl3_rms_norm_backward(exl3_ctx *ctx, const void *dy, int64_t lddy, const vo
  *   x        [n][in] of `dtype` (EXL3_BF16 or EXL3_F16), rows ldx elements apart,
  *            written as blocks in the call; in = cols, or rows when transposed
  *   xblocks  x as blocks instead of x (which is then null); exactly one of both
- *   y        [n][out] of `dtype`, rows ldy elements apart; shares no element with x
+ *   y        [n][out] of `dtype`, rows ldy elements apart; shares no element with x and
+ *            does not lie over W or the offsets
  * The products of a block are summed by the matrix units, which keep those of eight
  * neighbouring k's to 13 bits below the leading one of the largest and add the rest in
  * binary32 (a loss of at most 7 * 2^-13 of the magnitudes' sum), the blocks'

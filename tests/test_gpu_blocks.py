@@ -638,3 +638,31 @@ def test_two_products_in_one_graph_and_two_contexts_at_once(T):
                 z = a.block_linear(xs[1], w)
         torch.cuda.synchronize()
         assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+
+
+def test_a_result_over_the_weight_or_the_offsets_is_refused(T, ctx):
+    """And neither is changed; one right behind the codes is written."""
+    memory = torch.zeros(256 * 384 + 4 * 256 * 2, dtype=torch.uint8, device="cuda")
+    q, s = matrix(256, 384, 131)
+    memory[:256 * 384] = q.view(torch.uint8).flatten().cuda()
+    scale = torch.zeros(1024, dtype=torch.float32, device="cuda")
+    scale[:6] = s.flatten().cuda()
+    offsets = torch.zeros(1024, dtype=torch.int32, device="cuda")
+    offsets[1] = 4
+    w = T.BlockWeight(memory[:256 * 384].view(E4M3).view(256, 384), scale[:6].view(2, 3))
+    assert w.q.data_ptr() == memory.data_ptr() and w.scale.data_ptr() == scale.data_ptr()
+    x, _ = rows_of(4, 384, BF, 132)
+    before = [t.clone() for t in (memory, scale, offsets)]
+
+    def out(t, at):
+        return t.view(torch.uint8)[at:at + 2048].view(BF).view(4, 256)
+    for over in [out(memory, 0), out(memory, 256 * 384 - 16), out(scale, 0), out(offsets, 0)]:
+        for rows in [x, ctx.block_quantize(x)]:
+            with pytest.raises(T.Exl3Error) as e:
+                ctx.block_grouped_linear(rows, w, offsets[:2], out=over)
+            assert e.value.code == T.EXL3_EINVAL
+    assert all(torch.equal(a, b) for a, b in zip(before, (memory, scale, offsets)))
+    behind = out(memory, 256 * 384)
+    ctx.block_linear(x, w, out=behind)
+    assert torch.equal(behind, ctx.block_linear(x, w))
+    assert torch.equal(memory[:256 * 384], before[0][:256 * 384])

@@ -2345,6 +2345,12 @@ int block_linear_any(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *o
     } else if (rows_overlap(x, ldx, in, y, ldy, out, n)) {
         return fail(ctx, EXL3_EINVAL, "y overlaps x");
     }
+    const size_t y_bytes = rows_span(ldy, n, out), g = (size_t)w->groups;
+    if (spans_meet(y, y_bytes, w->q, g * w->rows * (size_t)w->ldq) ||
+        spans_meet(y, y_bytes, w->scale,
+                   g * exl3::blocks_of(w->rows) * exl3::blocks_of(w->cols) * sizeof(float)) ||
+        (offsets && spans_meet(y, y_bytes, offsets, (g + 1) * sizeof(int32_t))))
+        return fail(ctx, EXL3_EINVAL, "y overlaps the weight or the offsets");
     if ((rc = set_device(ctx)) != EXL3_OK) return rc;
     Carve c;
     size_t q_at = 0, s_at = 0;

@@ -103,8 +103,8 @@ struct GemmArgs {
 // wave's 32 lanes read at a time into different banks.
 // WK: sets of waves with rings of their own that take the contraction's blocks by turns, for calls
 // of few tiles; their sums are added in order.
-// 4,096 rows, 12288 x 4096: 166 to 175 us by the card, 2.35 to 2.48 PFLOP/s, where the library's
-// product with one scale for each operand takes 169 to 176.  Counted before the loads were
+// 4,096 rows, 12288 x 4096: 166 to 182 us by the card, 2.27 to 2.48 PFLOP/s; 176 on one where the
+// library's product with one scale for each operand took 173 to 175.  Counted before the loads were
 // spread (188 us): matrix units busy 54 % of the kernel's cycles, vector instructions issued on 47 %
 // of a unit's busy ones, shared memory active on 27 %.
 // 24 rows, 4096 x 12288: 11.6 us, 4.3 TB/s (32 x 32 tiles, four sets).
