@@ -1,0 +1,128 @@
+"""Products in 8-bit blocks whose two scales multiply to what binary32 does not hold, while the
+products of the values themselves do.  Codes are whole numbers times one power of two, so that every
+sum is exact and the results are the formula's, rounded once."""
+import pytest
+import torch
+
+from block_reference import E4M3, blocks, from_blocks, to_blocks
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def T():
+    import trellis_coded_weight_amd as T
+    return T
+
+
+@pytest.fixture(scope="module")
+def ctx(T):
+    with T.Context(0) as c:
+        yield c
+
+
+# (exponents of the rows' scales, of W's scales, what the codes +-1 and 0 are multiplied by)
+RANGES = {
+    "small": ([-70, -69, -66, -60, -40], -78, 2.0 ** 8),       # their product is subnormal or zero
+    "least": ([-126, -120, -110, -100], -22, 2.0 ** 8),        # as those of rows of tiny values
+    "large": ([68, 69, 70, -100], 60, 2.0 ** -9),              # infinite
+    "high": ([50, 49, 0], 50, 2.0 ** 3),                       # sums above 2^104
+    "subnormal": ([-130, -135, -127, -126], 20, 2.0 ** 3),     # scales below the normal range
+    "zero": ([None, 0, None, 40], 60, 2.0 ** -9),             # scales of zero
+}
+
+
+def power(e):
+    return 0.0 if e is None else 1.25 * 2.0 ** e
+
+
+def case(which, n, m, k, seed):
+    """(x's codes and scales, W's codes and scales): W [m, k], some of its rows empty."""
+    rows_e, w_e, unit = RANGES[which]
+    g = torch.Generator().manual_seed(seed)
+    xq = (torch.randint(-1, 2, (n, k), generator=g).float() * unit).to(E4M3)
+    w = torch.randint(-1, 2, (m, k), generator=g).float() * unit
+    w[::7] = 0
+    at = torch.randint(0, len(rows_e), (n, 1), generator=g).expand(n, blocks(k))
+    xs = torch.tensor([power(e) for e in rows_e])[at].contiguous()
+    ws = torch.full((blocks(m), blocks(k)), 1.75 * 2.0 ** w_e)
+    return xq, xs, w.to(E4M3), ws
+
+
+def rounded(v):
+    return v.float().to(BF)                                # (exact in binary32, so rounded once)
+
+
+# the streamed form (16-bit rows), and tiles of 32 to 256 columns
+SIZES = [(24, 300, 384), (70, 2100, 300), (150, 4096, 1300), (500, 4096, 300), (1500, 4096, 260),
+         (3840, 2176, 130)]
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("which", list(RANGES))
+@pytest.mark.parametrize("n,m,k", SIZES)
+def test_scales_far_apart(T, ctx, n, m, k, which, back):
+    xq, xs, wq, ws = case(which, n, m, k, n + m)
+    want = rounded(from_blocks(xq, xs) @ from_blocks(wq, ws, 128).t())
+    if back:                                               # W's transpose, contracted over its rows
+        wq, ws = wq.t().contiguous(), ws.t().contiguous()
+    y = ctx.block_linear(T.BlockRows(xq.cuda(), xs.cuda()), T.BlockWeight(wq.cuda(), ws.cuda()),
+                         transpose=back)
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("which", list(RANGES))
+@pytest.mark.parametrize("k", [384, 2500, 5000])
+def test_scales_far_apart_by_group(T, ctx, k, which):
+    """Few rows an expert, streamed."""
+    E, n, m = 6, 13, 200
+    xq, xs, wq, ws = case(which, n, E * 256, k, k)
+    wq, ws = wq.view(torch.uint8).view(E, 256, k)[:, :m].contiguous(), ws.view(E, 2, blocks(k))
+    offsets = [0, 2, 2, 7, 8, 12, 13]
+    y = ctx.block_grouped_linear(T.BlockRows(xq.cuda(), xs.cuda()),
+                                 T.BlockWeight(wq.view(E4M3).cuda(), ws.cuda()),
+                                 torch.tensor(offsets, dtype=torch.int32).cuda()).cpu()
+    x = from_blocks(xq, xs)
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        want = rounded(x[a:b] @ from_blocks(wq[e].view(E4M3), ws[e], 128).t())
+        assert torch.equal(y[a:b], want)
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("e,w_e", [(-70, -78), (-117, -22), (60, 62)])
+def test_rows_in_16_bits(T, ctx, n, e, w_e):
+    """Their blocks written in the call: 448 times a power of two has that power as its scale."""
+    m, k, unit = 300, 640, 2.0 ** 8 if e < 0 else 2.0 ** -9
+    g = torch.Generator().manual_seed(n)
+    x = torch.randint(-1, 2, (n, k), generator=g).float() * 7 * 2.0 ** (6 + e)
+    x[:, ::128] = 448 * 2.0 ** e
+    w = torch.randint(-1, 2, (m, k), generator=g).float() * unit
+    w[::7] = 0
+    if e > 0:
+        w[:, ::128] = 0                                    # (the others' products are in range)
+        x[:, 1::2] = 2.0 ** (e - 9)
+        x[:, 2::2] = 0
+        x[:, ::128] = 448 * 2.0 ** e
+    x = x.to(BF)
+    xq, xs = to_blocks(x.float())
+    assert (xs == 2.0 ** e).all()
+    ws = torch.full((blocks(m), blocks(k)), 1.75 * 2.0 ** w_e)
+    want = rounded(from_blocks(xq, xs) @ from_blocks(w.to(E4M3), ws, 128).t())
+    y = ctx.block_linear(x.cuda(), T.BlockWeight(w.to(E4M3).cuda(), ws.cuda()))
+    assert torch.isfinite(want).all() and torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("n,m,k", SIZES)
+def test_rows_of_zeros_leave_the_others_as_they_are(T, ctx, n, m, k, back):
+    """Their scale is the smallest, and meets any of W's."""
+    g = torch.Generator().manual_seed(k)
+    w = ctx.block_quantize_weight((torch.randn((k, m) if back else (m, k), generator=g) * 0.02).cuda())
+    x = torch.randn(n, k, generator=g).to(BF).cuda()
+    want = ctx.block_linear(ctx.block_quantize(x), w, transpose=back)
+    x[1::3] = 0
+    want[1::3] = 0
+    assert torch.equal(ctx.block_linear(ctx.block_quantize(x), w, transpose=back), want)
