@@ -126,3 +126,52 @@ def test_rows_of_zeros_leave_the_others_as_they_are(T, ctx, n, m, k, back):
     x[1::3] = 0
     want[1::3] = 0
     assert torch.equal(ctx.block_linear(ctx.block_quantize(x), w, transpose=back), want)
+
+
+def blocks_with_ties():
+    """Rows of one block whose largest a is tiny, with values whose quotient by a / 448 lies halfway
+    between two codes: 7 * 2^-10 (a * 2^-16) below e4m3's normal range, 21 * 2^j (3 a * 2^i) in it."""
+    g = torch.Generator().manual_seed(17)
+    rows = []
+    for e in list(range(-125, -90)) + [-62, -61, -60, -59, -58, -50, 0, 100]:
+        for m in range(128, 256, 3):
+            a = m * 2.0 ** (e - 7)
+            row = a * (2 * torch.rand(128, generator=g, dtype=torch.float64) - 1)
+            row[0] = a
+            for i in range(8):
+                row[1 + i] = (-1) ** i * a * 2.0 ** -(16 - i)
+                row[20 + i] = (-1) ** i * 3 * a * 2.0 ** -(6 + i)
+            rows.append(row)
+    return torch.stack(rows).float()
+
+
+def same(got, want):
+    return torch.equal(got.cpu().contiguous().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_codes_of_tiny_blocks_are_those_of_a_division(ctx, dtype):
+    v = blocks_with_ties().to(dtype)
+    if dtype == BF:
+        q, scale = to_blocks(v.float())
+        got = ctx.block_quantize(v.cuda())
+        assert torch.equal(got.scale.cpu(), scale) and same(got.q, q)
+        # and where the product's workgroups write the rows themselves: times a multiple of the unit
+        # matrix, each result one code times two scales
+        one = torch.eye(128).to(E4M3).cuda()
+        w = ctx_weight(one, 2.0 ** 60)
+        for t in range(0, v.shape[0], 97):
+            y = ctx.block_linear(v[t:t + 1].cuda(), w)
+            want = (from_blocks(q[t:t + 1], scale[t:t + 1]) * 2.0 ** 60).float().to(BF)
+            assert torch.equal(y.cpu(), want)
+    # matrices: a row's values one to a row of its own, 128 x 128 with the same largest
+    for t in range(0, v.shape[0], 53):
+        w = v[t:t + 1].expand(128, 128).contiguous()
+        q, scale = to_blocks(w.float(), 128)
+        got = ctx.block_quantize_weight(w.cuda())
+        assert torch.equal(got.scale.cpu(), scale) and same(got.q, q)
+
+
+def ctx_weight(codes, scale):
+    from trellis_coded_weight_amd import BlockWeight
+    return BlockWeight(codes, torch.full((1, 1), scale, device="cuda"))

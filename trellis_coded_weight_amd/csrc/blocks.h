@@ -48,27 +48,33 @@ __device__ __forceinline__ u32x4 narrow(const float (&f)[kWide]) {
     return v;
 }
 
-// The scale of a block whose largest magnitude has these bits, and its inverse.  The scale stays
-// in the normal range, so that the inverse does too.  NaN where the block holds an infinity or a
-// NaN: magnitudes compare as integers, which keeps a NaN.
+// The scale of a block whose largest magnitude has these bits; what its values are multiplied by
+// first (2^64 for tiny blocks, else one), the scale times that, and the inverse of the latter.  The
+// scale stays in the normal range, so that the inverse does too.  NaN where the block holds an
+// infinity or a NaN: magnitudes compare as integers, which keeps a NaN.
 struct CodeScale {
-    float scale, inverse;
+    float scale, lift, lifted, inverse;
 };
 __device__ __forceinline__ CodeScale code_scale(uint32_t big) {
     CodeScale s;
     s.scale = __builtin_bit_cast(float, big) / kCodeMax;
     s.scale = s.scale < FLT_MIN ? FLT_MIN : s.scale;
     if (big >= 0x7F800000u) s.scale = __builtin_bit_cast(float, 0x7FC00000u);
-    s.inverse = 1.0f / s.scale;
+    s.lift = s.scale < 0x1p-60f ? 0x1p64f : 1.0f;
+    s.lifted = s.scale * s.lift;
+    s.inverse = 1.0f / s.lifted;
     return s;
 }
 // v / scale rounded to binary32 as a division does: the product with the correctly rounded
-// inverse is at most one unit off, and the remainder, which is exact, brings it to the nearest
-// (taken with this sign, it leaves a zero's sign alone).
+// inverse is at most one unit off, and the remainder brings it to the nearest (taken with this
+// sign, it leaves a zero's sign alone).  The remainder is exact, as the lift keeps it out of the
+// subnormal numbers for every value that has a code other than zero (its last place, 2^-47 of v or
+// less, stays above 2^-149 for v from 2^-102 on; codes end at 2^-10 of the scale).
 // The instruction then rounds to e4m3, ties to even; at 448 (1 + 2^-23) nothing overflows.
 __device__ __forceinline__ float quotient(float v, const CodeScale &s) {
+    v *= s.lift;
     const float q = v * s.inverse;
-    return __builtin_fmaf(-__builtin_fmaf(q, s.scale, -v), s.inverse, q);
+    return __builtin_fmaf(-__builtin_fmaf(q, s.lifted, -v), s.inverse, q);
 }
 __device__ __forceinline__ u32x2 to_codes(const float (&f)[kWide], const CodeScale &s) {
     u32x2 o;
