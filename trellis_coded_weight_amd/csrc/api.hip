@@ -2276,46 +2276,15 @@ int check_block_weight(exl3_ctx *ctx, const exl3_block_weight *w, exl3::BlockWei
     return EXL3_OK;
 }
 
-// Whether experts' matrices are streamed through registers for few rows each (up to 16), or go
-// through the tiles, whose smallest for them have 128 columns of the result by 32 rows.  A single
-// matrix goes through tiles, the smallest of 32 x 32 (or is streamed as below).  Estimates in us,
-// of both as measured: 64 experts of 1408 x 2048, 64 rows: 25.4 and 26.7, 256: 36.9 and 41.0, 512:
-// 45.8 and 41.8; 16 of 2048 x 1408, 16 rows: 9.8 and 9.4, 64: 13.6 and 11.7.
-bool few_rows(const exl3::BlockWeightArgs &w, bool transpose, int64_t n, int n_cu) {
-    if (transpose || w.groups == 1 || n > (int64_t)16 * w.groups) return false;
-    const double rows = (double)n / w.groups, mb = 1e-6 * w.rows * w.cols * w.groups;
-    const double streamed = 3.5 + mb * (0.16 + 0.01 * rows);
-    const double tiles = (w.rows + 127) / 128 * (n / 32 + 0.5 * w.groups);
-    const double steps = (exl3::blocks_of(w.cols) + 1) / 2;
-    const double tiled =
-        3.2 + std::max(0.44 * steps * std::max(1.0, tiles / n_cu), mb / 4.9);
-    return streamed < tiled;
-}
-
-// Whether its workgroups write 16-bit rows as blocks themselves, each all that it needs, in place
-// of a launch before: up to some 28,000 elements on a compute unit, us with and without:
-// 2 rows, 12288 x 4096 (24,576): 13.1, 15.1; 4 rows, 4096 x 4096 (16,384): 7.9, 10.0; 8 rows
-// (32,768): 10.6, 10.1; 4 rows, 12288 x 4096 (49,152): 15.4, 14.8; 16 experts of 1408 x 2048, 32
-// rows (22,528): 11.6, 12.3, 64 rows (45,056): 14.4, 13.7.
-bool own_rows(const exl3::BlockWeightArgs &w, int64_t n, int n_cu) {
-    const int64_t rows = (n + w.groups - 1) / w.groups;
-    const int64_t workgroups = (int64_t)((w.rows + 15) / 16) * w.groups;
-    return rows * w.cols * std::max<int64_t>(n_cu, workgroups) <= (int64_t)28000 * n_cu;
-}
-
 int run_block_product(exl3_ctx *ctx, const exl3::BlockWeightArgs &w,
-                      const exl3::BlockProductArgs &a, const void *x, int64_t ldx, int in,
-                      bool bf16) {
+                      const exl3::BlockProductArgs &a, exl3::BlockForm form, const void *x,
+                      int64_t ldx, int in, bool bf16) {
     if (x && !a.x16)
         EXL3_HIP(ctx, exl3::launch_block_quantize(x, ldx, a.n, in, bf16, a.x, ctx->stream));
-    if (a.x16 || few_rows(w, a.transposed, a.n, ctx->n_cu))
+    if (form == exl3::kOwnRows || form == exl3::kFewRows)
         EXL3_HIP(ctx, exl3::launch_block_rows(w, a, bf16, ctx->stream));
-    else {
-        const hipError_t err = exl3::launch_block_gemm(w, a, bf16, ctx->n_cu, ctx->stream);
-        if (err == hipErrorInvalidConfiguration)
-            return fail(ctx, EXL3_EUNSUPPORTED, "a product of over 2^23 tiles: split its groups");
-        EXL3_HIP(ctx, err);
-    }
+    else
+        EXL3_HIP(ctx, exl3::launch_block_gemm(w, a, form, bf16, ctx->stream));
     return EXL3_OK;
 }
 
@@ -2355,7 +2324,12 @@ int block_linear_any(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *o
     Carve c;
     size_t q_at = 0, s_at = 0;
     const size_t blocks = (size_t)exl3::blocks_of(in);
-    const bool own = x && !transpose && own_rows(wa, n, ctx->n_cu);
+    const exl3::BlockForm form = exl3::block_form(
+        exl3::BlockCall{n, out, in, w->groups, offsets != nullptr, transpose != 0}, x != nullptr,
+        ctx->n_cu);
+    if (form == exl3::kNoForm)
+        return fail(ctx, EXL3_EUNSUPPORTED, "a product of over 2^23 tiles: split its groups");
+    const bool own = form == exl3::kOwnRows;
     if (own) {
         a.x16 = x;
         a.ldx16 = ldx;
@@ -2376,7 +2350,7 @@ int block_linear_any(exl3_ctx *ctx, const exl3_block_weight *w, const int32_t *o
     const int id = open_timed(ctx, EXL3_KERNEL_BLOCK,
                               (int64_t)w->groups * exl3::blocks_of(w->rows) *
                                   exl3::blocks_of(w->cols));
-    return end_timed(ctx, id, run_block_product(ctx, wa, a, x, ldx, in, dtype == EXL3_BF16));
+    return end_timed(ctx, id, run_block_product(ctx, wa, a, form, x, ldx, in, dtype == EXL3_BF16));
 }
 
 int run_norm_backward(exl3_ctx *ctx, const exl3::NormBackwardArgs &a, bool bf16) {

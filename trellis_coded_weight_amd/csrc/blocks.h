@@ -5,15 +5,13 @@
 
 #include <float.h>
 
+#include "block_forms.h"
 #include "coded.h"
 
 namespace exl3 {
 
-constexpr int kBlock = 128;                      // elements a scale serves along a row
 constexpr float kCodeMax = 448.0f;               // the largest e4m3 value
 constexpr size_t kOwnBytes = 48 << 10;           // shared memory for rows a workgroup writes as blocks
-
-__host__ __device__ inline int blocks_of(int width) { return (width + kBlock - 1) / kBlock; }
 
 // ---- device side: 16-bit rows and their codes ----
 constexpr int kWide = 8;                         // consecutive elements a lane takes at a time
@@ -184,8 +182,8 @@ struct BlockProductArgs {
 // Few rows a group, not transposed; x or x16.
 hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
                              hipStream_t stream);
-// hipErrorInvalidConfiguration: more tiles than a launch holds.
-hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
-                             int n_cu, hipStream_t stream);
+// form: one of the tiles.
+hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, BlockForm form,
+                             bool bf16, hipStream_t stream);
 
 }  // namespace exl3

@@ -17,7 +17,6 @@
 #include "blocks.h"
 
 #include <algorithm>
-#include <cmath>
 
 namespace exl3 {
 
@@ -698,8 +697,8 @@ hipError_t launch_block_rows(const BlockWeightArgs &w, const BlockProductArgs &a
     return hipSuccess;
 }
 
-hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, bool bf16,
-                             int n_cu, hipStream_t stream) {
+hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a, BlockForm form,
+                             bool bf16, hipStream_t stream) {
     GemmArgs p = gemm_args(w, a);
 #define EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, BF, TR)                                 \
     hipLaunchKernelGGL((block_gemm_kernel<BM, BN, WM, WN, WK, RING, SPREAD, BF, TR>),          \
@@ -708,11 +707,8 @@ hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a
 #define EXL3_BLOCK(BM, BN, WM, WN, WK, RING, SPREAD)                                           \
     do {                                                                                       \
         p.m_tiles = (p.m + BM - 1) / BM;                                                       \
-        const int64_t total =                                                                  \
-            p.m_tiles * (a.offsets ? a.n / BN + w.groups : (a.n + BN - 1) / BN);               \
-        /* a launch has fewer than 2^32 lanes, of up to 512 a workgroup */                     \
-        if (total >= (int64_t)1 << 23) return hipErrorInvalidConfiguration;                    \
-        p.total = (int)total;                                                                  \
+        p.total =                                                                              \
+            (int)(p.m_tiles * (a.offsets ? a.n / BN + w.groups : (a.n + BN - 1) / BN));        \
         if (bf16 && a.transposed)                                                              \
             EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, true, true);                        \
         else if (bf16)                                                                         \
@@ -722,41 +718,16 @@ hipError_t launch_block_gemm(const BlockWeightArgs &w, const BlockProductArgs &a
         else                                                                                   \
             EXL3_BLOCK_T(BM, BN, WM, WN, WK, RING, SPREAD, false, false);                      \
     } while (0)
-    // What a step of a round takes, us (a tile a compute unit, but two of kTwice; WK blocks a step),
-    // from calls of 4,096 columns from 4,096 with 64 rows (32 x 32: 7.4), 128 (64 x 32: 8.5), 200
-    // (128 x 32: 11.3), 512 (128 x 64: 14.2), 1,024 (128 x 128: 21.9; two rounds of 128 x 64: 27),
-    // 2,000 (256 x 128: 33; 128 x 128, two a unit: 36) and of 12,288 with 4,096 rows (three rounds
-    // of 256 x 256: 167; six of 256 x 128: 199); some 3 us of each are not in steps.  The contraction
-    // in four sets where tiles are few: 4,096 columns from 12,288, 24 rows: 11.8, 128 x 32 in two
-    // sets: 23.  Experts' tiles: each group's last is half empty on average, and rounds run into
-    // one another.
-    enum { kHuge, kLarge, kTwice, kMedium, kSmall, kSmallest, kThin, kThinnest, kForms };
-    auto cost = [&](int bm, int bn, int wk, int places, double us) {
-        const double m_tiles = (p.m + bm - 1) / bm, steps = (p.blocks + wk - 1) / wk;
-        if (m_tiles * ((double)a.n / bn + w.groups) >= (double)(1 << 23)) return 1e30;
-        if (!a.offsets)
-            return us * steps * std::ceil(m_tiles * (double)((a.n + bn - 1) / bn) / (places * n_cu));
-        // (16 of 2048 x 1408, 64 rows: 128 x 32 11.6, 64 x 32 15.2, 32 x 32 21.7)
-        if (bm < 128) return 1e30;
-        return us * steps *
-               std::max(1.0, m_tiles * ((double)a.n / bn + 0.5 * w.groups) / (places * n_cu));
-    };
-    const double costs[kForms] = {
-        cost(256, 256, 1, 1, 1.7), cost(256, 128, 1, 1, 1.0), cost(128, 128, 1, 2, 1.03),
-        cost(128, 128, 1, 1, 0.6), cost(128, 64, 2, 1, 0.83), cost(128, 32, 2, 1, 0.67),
-        cost(64, 32, 4, 1, 0.78),  cost(32, 32, 4, 1, 0.5)};
-    int best = 0;
-    for (int i = 1; i < kForms; ++i)
-        if (costs[i] < costs[best]) best = i;
-    switch (best) {
-        case kHuge: EXL3_BLOCK(256, 256, 2, 4, 1, 2, 4); break;
-        case kLarge: EXL3_BLOCK(256, 128, 4, 2, 1, 3, 4); break;
-        case kTwice: EXL3_BLOCK(128, 128, 2, 2, 1, 2, 1); break;
-        case kMedium: EXL3_BLOCK(128, 128, 2, 2, 1, 4, 4); break;
-        case kSmall: EXL3_BLOCK(128, 64, 2, 2, 2, 3, 4); break;
-        case kSmallest: EXL3_BLOCK(128, 32, 2, 2, 2, 3, 4); break;
-        case kThin: EXL3_BLOCK(64, 32, 1, 1, 4, 3, 4); break;
-        default: EXL3_BLOCK(32, 32, 1, 1, 4, 4, 2);
+    switch (form) {
+        case kTile256x256: EXL3_BLOCK(256, 256, 2, 4, 1, 2, 4); break;
+        case kTile256x128: EXL3_BLOCK(256, 128, 4, 2, 1, 3, 4); break;
+        case kTile128x128Twice: EXL3_BLOCK(128, 128, 2, 2, 1, 2, 1); break;
+        case kTile128x128: EXL3_BLOCK(128, 128, 2, 2, 1, 4, 4); break;
+        case kTile128x64: EXL3_BLOCK(128, 64, 2, 2, 2, 3, 4); break;
+        case kTile128x32: EXL3_BLOCK(128, 32, 2, 2, 2, 3, 4); break;
+        case kTile64x32: EXL3_BLOCK(64, 32, 1, 1, 4, 3, 4); break;
+        case kTile32x32: EXL3_BLOCK(32, 32, 1, 1, 4, 4, 2); break;
+        default: return hipErrorInvalidValue;
     }
 #undef EXL3_BLOCK
 #undef EXL3_BLOCK_T
