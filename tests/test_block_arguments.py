@@ -51,3 +51,12 @@ def test_reference_rounds_to_the_nearest_code():
     # the quotient's own rounding may decide what lies within it of a tie
     assert (got <= best + 2.0 ** -23 * 448).all()
     assert torch.equal(from_blocks(q, scale), q.double() * s)
+
+
+def test_a_residual_of_another_shape_is_refused():
+    """Also one of as many rows, which flattening would pair with others."""
+    from trellis_coded_weight_amd import rms_norm
+    x, gain = torch.zeros(2, 3, 8).bfloat16(), torch.ones(8)
+    for shape in [(3, 2, 8), (6, 8), (1, 3, 8), (2, 3, 1), (8,)]:
+        with pytest.raises(ValueError, match="residual must have shape"):
+            rms_norm(None, x, gain, residual=torch.zeros(shape).bfloat16())

@@ -165,5 +165,8 @@ def rms_norm(context: Context, x: torch.Tensor, gain: torch.Tensor, eps: float =
     (y, s) with a residual.  Differentiable in x, gain and the residual."""
     if residual is None:
         return _RmsNorm.apply(_rows(x), gain, None, context, eps).reshape(x.shape)
+    if residual.shape != x.shape:
+        raise ValueError("residual must have shape %s, got %s" %
+                         (tuple(x.shape), tuple(residual.shape)))
     y, total = _RmsNorm.apply(_rows(x), gain, _rows(residual), context, eps)
     return y.reshape(x.shape), total.reshape(x.shape)
