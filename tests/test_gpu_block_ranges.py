@@ -175,3 +175,19 @@ def test_codes_of_tiny_blocks_are_those_of_a_division(ctx, dtype):
 def ctx_weight(codes, scale):
     from trellis_coded_weight_amd import BlockWeight
     return BlockWeight(codes, torch.full((1, 1), scale, device="cuda"))
+
+
+@pytest.mark.parametrize("cols", [1, 130, 300, 1003, 20001])
+def test_codes_behind_a_row_are_zero_also_after_a_nan(ctx, cols):
+    """Up to whole blocks, as products read them."""
+    x = torch.ones(3, cols, dtype=BF)
+    x[1, cols - 1] = float("nan")
+    x = x.cuda()
+    gain = torch.ones(cols, dtype=BF, device="cuda")
+    for got in (ctx.block_quantize(x), ctx.rms_norm(x, gain, blocks=True),
+                ctx.block_quantize_weight(x)):
+        codes = got.q.as_strided((3, 128 * blocks(cols)), (128 * blocks(cols), 1))
+        codes = codes.view(torch.uint8)
+        assert (codes[:, cols:] == 0).all()
+        assert (codes[1, cols - 1] & 0x7F) == 0x7F
+        assert torch.isnan(got.scale[-1 if got.scale.shape[0] == 1 else 1, -1])

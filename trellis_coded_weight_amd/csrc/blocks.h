@@ -86,6 +86,15 @@ __device__ __forceinline__ u32x2 to_codes(const float (&f)[kWide], const CodeSca
     }
     return o;
 }
+// Codes with those past the first `valid` zero, as behind a row's end also in a block of NaN.
+__device__ __forceinline__ u32x2 first_codes(u32x2 codes, int valid) {
+    if (valid < kWide) {
+        const uint64_t keep = valid > 0 ? (1ull << 8 * valid) - 1 : 0;
+        codes[0] &= (uint32_t)keep;
+        codes[1] &= (uint32_t)(keep >> 32);
+    }
+    return codes;
+}
 __device__ __forceinline__ uint32_t magnitude(float v) {
     return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
 }

@@ -46,12 +46,12 @@ __device__ __forceinline__ S sum_all(S v, S *between) {
 }
 
 // Eight columns from c of a row of blocks: the block's scale by its first lane, the codes by all,
-// zeros past the width up to `blocks` whole blocks.  All 16 lanes of a block take part.
-__device__ __forceinline__ void write_codes(const BlockRowsArgs &q, int64_t row, int c, int blocks,
+// zeros past the width up to whole blocks.  All 16 lanes of a block take part.
+__device__ __forceinline__ void write_codes(const BlockRowsArgs &q, int64_t row, int c, int cols,
                                             const float (&f)[kWide]) {
     const CodeScale s = code_scale(largest_of_block(largest8(f)));
-    if (c >= blocks * kBlock) return;
-    *reinterpret_cast<u32x2 *>(q.q + row * q.ld + c) = to_codes(f, s);
+    if (c >= blocks_of(cols) * kBlock) return;
+    *reinterpret_cast<u32x2 *>(q.q + row * q.ld + c) = first_codes(to_codes(f, s), cols - c);
     if ((c & (kBlock - 1)) == 0) q.scale[(c / kBlock) * q.lds + row] = s.scale;
 }
 
@@ -175,7 +175,7 @@ rms_norm_kernel(NormArgs a) {
             if (valid > 0)
                 store8(static_cast<uint16_t *>(a.y) + row * a.ldy + c, narrow<BF>(f), valid);
         } else {
-            write_codes(a.q, row, c, blocks_of(a.cols), f);
+            write_codes(a.q, row, c, a.cols, f);
         }
     }
 }
@@ -374,7 +374,8 @@ block_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t n, in
     v = __builtin_bit_cast(float, big);
     big = larger(big, __builtin_bit_cast(uint32_t, lane_xor<4>(v)));
     const CodeScale s = code_scale(big);
-    const u32x2 lo = to_codes(f[0], s), hi = to_codes(f[1], s);
+    const u32x2 lo = first_codes(to_codes(f[0], s), cols - c);
+    const u32x2 hi = first_codes(to_codes(f[1], s), cols - c - kWide);
     *reinterpret_cast<u32x4 *>(q.q + row * q.ld + c) = u32x4{lo[0], lo[1], hi[0], hi[1]};
     if ((c & (kBlock - 1)) == 0) q.scale[(c / kBlock) * q.lds + row] = s.scale;
 }
@@ -412,7 +413,8 @@ block_quantize_weight_kernel(const void *__restrict__ w, int64_t ldw, int rows, 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t row = r0 + 16 * i;
-        if (row < rows) *reinterpret_cast<u32x2 *>(q + row * ldq + c) = to_codes(f[i], s);
+        if (row < rows)
+            *reinterpret_cast<u32x2 *>(q + row * ldq + c) = first_codes(to_codes(f[i], s), valid);
     }
 }
 
