@@ -191,3 +191,26 @@ def test_codes_behind_a_row_are_zero_also_after_a_nan(ctx, cols):
         assert (codes[:, cols:] == 0).all()
         assert (codes[1, cols - 1] & 0x7F) == 0x7F
         assert torch.isnan(got.scale[-1 if got.scale.shape[0] == 1 else 1, -1])
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("which", list(RANGES))
+@pytest.mark.parametrize("n,m,k", [(60, 130, 300), (1500, 260, 300), (4000, 520, 600)])
+def test_scales_far_apart_by_group_in_tiles(T, ctx, n, m, k, which, back):
+    E = 3
+    xq, xs, wq, ws = case(which, n, E * 640, k, n + k)
+    wq = wq.view(torch.uint8).view(E, 640, k)[:, :m].contiguous()
+    ws = ws.view(E, 5, blocks(k))[:, :blocks(m)].contiguous()
+    if back:
+        wq, ws = wq.transpose(1, 2).contiguous(), ws.transpose(1, 2).contiguous()
+    offsets = [1, n // 3, n // 3, n - 2]
+    y = ctx.block_grouped_linear(T.BlockRows(xq.cuda(), xs.cuda()),
+                                 T.BlockWeight(wq.view(E4M3).cuda(), ws.cuda()),
+                                 torch.tensor(offsets, dtype=torch.int32).cuda(),
+                                 transpose=back).cpu()
+    x = from_blocks(xq, xs)
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        w = from_blocks(wq[e].view(E4M3), ws[e], 128)
+        assert torch.equal(y[a:b], rounded(x[a:b] @ (w if back else w.t())))
+    assert (y[:1] == 0).all() and (y[n - 2:] == 0).all()
