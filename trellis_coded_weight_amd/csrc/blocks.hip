@@ -27,10 +27,10 @@ using i32x8 = int __attribute__((ext_vector_type(8)));
 struct Operand {
     u32x4 a, b;                                  // pieces g and 4 + g
 };
-// A scale as mantissa * 2^(exponent - 127), for a block's factor, the product of its two scales,
-// that is no normal number though what it meets may bring it back into range: the instruction
-// takes the exponents and the mantissas' product is the factor.  NaN and infinity give NaN; zero and subnormal scales
-// have the least exponent.
+// A scale as mantissa * 2^(exponent - 127), for where a block's factor, the product of its two
+// scales, is out of range though what it meets may bring it back: the instruction takes the
+// exponents, and the mantissas' product is the factor.  NaN and infinity give NaN; zero and
+// subnormal scales have the least exponent.
 struct Scale {
     float mantissa;
     int exponent;
@@ -324,7 +324,6 @@ block_gemm_kernel(const uint8_t *__restrict__ w, const float *__restrict__ w_sca
     }
     read_a(0, 0, a[0]);
     int place = 0, before = RING - 1;
-    float largest = 0.0f;                                 // of the factors' magnitudes
     for (int s0 = 0; s0 < steps; s0 += 63) {              // a step takes the next one's scale
         if (s0)
             w64 = kLift * w_there(s0, *reinterpret_cast<const float *>(
@@ -351,9 +350,6 @@ block_gemm_kernel(const uint8_t *__restrict__ w, const float *__restrict__ w_sca
                         scale_add(TM - 1, j, f_last[j]);
                     else
                         scale_add(i - 1, j, f[j]);
-                    if (i == TM / 2 && j % 2 == 0)
-                        largest = fmaxf(fmaxf(largest, fabsf(f[j])),
-                                        fabsf(f[j + 1 < TN ? j + 1 : j]));
                     if (i + 1 == TM) {
                         f_last[j] = f[j];
                         f[j] = read_scale(j, after);
@@ -377,24 +373,29 @@ block_gemm_kernel(const uint8_t *__restrict__ w, const float *__restrict__ w_sca
     for (int j = 0; j < TN; ++j) scale_add(TM - 1, j, f_last[j]);
     // Factors and sums are held over 2^-24 (kLift): a factor that is subnormal then, the product of
     // two scales below 2^-150, is off by at most 2^-174, and what it meets, less than 2^25, by less
-    // than any result shows.  Where one or a sum is past the largest number, this wave's sums once
-    // more, by the scales' exponents and from memory; not for rows that are NaN by their scales.
-    // 4,096 rows, 12288 x 4096, against factors without any of this: 0.5 % more; the exponents
-    // carried through the loop 4 %, a second loop that takes them from the first such factor on 1 %
-    // (and of 1,000 to 2,000 rows, 4096 x 4096: 2, 8 and 8 to 11 %).
-    uint32_t past = !(largest <= FLT_MAX) ? (1u << TN) - 1 : 0;   // by rows of 16
+    // than any result shows.  An infinite factor leaves infinity or NaN, whatever it meets.  Where a
+    // sum is past the largest number, this wave's sums once more, by the scales' exponents and from
+    // memory; not for rows that are NaN by their scales.
+    // 4,096 rows, 12288 x 4096, against factors without any of this, in turn on one card: 0.5 % more
+    // (163.3 us for 162.5); the exponents carried through the loop 4 %, a second loop that takes
+    // them from the first such factor on 1 % (both 8 to 11 % of 1,000 to 2,000 rows, 4096 x 4096).
+    uint32_t past = 0;                                    // by rows of 16
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-        float zero = 0.0f;                                // or NaN
+        float sum = 0.0f;                                 // finite if all are (and below 2^64)
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                zero = __builtin_fmaf(acc[i][j][c], 0.0f, zero);
-                acc[i][j][c] *= 1.0f / kLift;
-            }
-        past |= zero != 0.0f ? 1u << j : 0;
+            for (int c = 0; c < 4; c += 2)
+                sum = __builtin_fmaf(acc[i][j][c], acc[i][j][c + 1], sum);
+        past |= !(fabsf(sum) <= FLT_MAX) ? 1u << j : 0;
     }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[i][j][c] *= 1.0f / kLift;
     if (__builtin_amdgcn_ballot_w64(past != 0)) {
         const uint8_t *xs_rows = x + row0 * p.ldx;
         bool bad = false;
