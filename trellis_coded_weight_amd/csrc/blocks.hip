@@ -12,8 +12,9 @@
 // The unit aligns the products of eight neighbouring k's to the largest and keeps 13 bits below its
 // leading one (measured: 2^16 + 2^s is exact from s = 3 on within such an eight, and to 24 bits
 // across them); the rest is binary32.  With the loss of that emulated, 4,096 normally distributed
-// terms are off by 2e-5 (root mean square), rounding the result to binary16 takes 1.9e-4 and to
-// bfloat16 1.7e-3.  It is the price of the 8-bit rate: codes widened to bfloat16 run at half of it.
+// terms are off by 2e-5 (root mean square; 3.7e-5 where some channels are 12 times the others, 1e-4
+// where 200 times), rounding the result to binary16 takes 2.1e-4 and to bfloat16 1.7e-3.  It is the
+// price of the 8-bit rate: codes widened to bfloat16 run at half of it.
 #include "blocks.h"
 
 #include <algorithm>
@@ -119,10 +120,11 @@ struct GemmArgs {
 // wave's 32 lanes read at a time into different banks.
 // WK: sets of waves with rings of their own that take the contraction's blocks by turns, for calls
 // of few tiles; their sums are added in order.
-// 4,096 rows, 12288 x 4096: 166 to 182 us by the card, 2.27 to 2.48 PFLOP/s; 176 on one where the
-// library's product with one scale for each operand took 173 to 175.  Counted before the loads were
-// spread (188 us): matrix units busy 54 % of the kernel's cycles, vector instructions issued on 47 %
-// of a unit's busy ones, shared memory active on 27 %.
+// 4,096 rows, 12288 x 4096: 166 to 185 us by the card, 2.23 to 2.48 PFLOP/s; 176 on one where the
+// library's product with one scale for each operand took 173 to 175.  Matrix units are busy 66 % of
+// a compute unit's busy cycles (59 % of the kernel's), vector instructions issued on 53 %, shared
+// memory active on 31 %; turned, 2,000 rows, 4096 x 4096: 49, 48 and 30 %; 128 x 64 tiles, 333 rows:
+// 30, 36 and 28 %, with waves waiting for 38 % of theirs.
 // 24 rows, 4096 x 12288: 11.6 us, 4.3 TB/s (32 x 32 tiles, four sets).
 template <int BM>
 __device__ __forceinline__ int turned_slot(int row) {

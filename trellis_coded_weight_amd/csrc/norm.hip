@@ -106,7 +106,8 @@ __device__ __forceinline__ float times(float v, const Rsqrt &r) {
 // binary32's range the row is summed again in binary64.  Roundings: s to its stored type, y once
 // to its type, or its quotient by the block's scale to binary32 and then e4m3.
 // 8,200 x 4,096, bfloat16, residual and blocks: 43 us, 5.4 TB/s where a large copy reaches 4.88;
-// 1 x 4,096: 2.9 us, the rest of a call's 14.5 is the host's.
+// 1 x 4,096: 2.9 us, the rest of a call's 14.5 is the host's.  1,000 x 20,000 into 16 bits (V = 0):
+// 41 (33 the floor).
 template <int T, int V, bool BF, bool G32>
 __global__ void __launch_bounds__(T < 256 ? 256 : T)
 rms_norm_kernel(NormArgs a) {
@@ -186,9 +187,10 @@ rms_norm_kernel(NormArgs a) {
 // gain's gradient of its columns stays in registers until the rows are done.  The parts are
 // added in order by a second kernel, so no result depends on scheduling.  V = 0: columns too many
 // for registers; dgain goes through the part in memory.  The next row's loads go out before this
-// one's sums, whose barrier they would else wait behind: 2,000 x 4,096 with ds: 17.6 us,
-// then 3.8 for the parts, 19.4 a call (13.4 the floor); 25.8 and 5.0 with this row's loads behind
-// the last one's sums, 256 lanes a row and one workgroup a compute unit.  8,200 rows: 58.5 (55).
+// one's sums, whose barrier they would else wait behind: 2,000 x 4,096 with ds: 19.4 us
+// a call (13.4 the floor); by the profiler's clock 17.7, then 4.0 for the parts, and 25.8 and 5.0
+// with this row's loads behind the last one's sums, 256 lanes a row and one workgroup a compute
+// unit.  8,200 rows: 59.3 (55).  1,000 x 20,000 (V = 0): 107 (33).
 template <int T, int V, bool BF, bool G32>
 __global__ void __launch_bounds__(T)
 rms_norm_backward_kernel(NormBackwardArgs a) {
