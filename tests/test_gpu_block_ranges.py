@@ -29,6 +29,8 @@ RANGES = {
     "least": ([-126, -120, -110, -100], -22, 2.0 ** 8),        # as those of rows of tiny values
     "large": ([68, 69, 70, -100], 60, 2.0 ** -9),              # infinite
     "high": ([50, 49, 0], 50, 2.0 ** 3),                       # sums above 2^104
+    "huge": ([-110, -105, -126], 110, 1.0),                    # one scale large, the other small
+    "tiny": ([110, 112, 0], -110, 2.0 ** 3),
     "subnormal": ([-130, -135, -127, -126], 20, 2.0 ** 3),     # scales below the normal range
     "zero": ([None, 0, None, 40], 60, 2.0 ** -9),             # scales of zero
 }
