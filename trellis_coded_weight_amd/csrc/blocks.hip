@@ -384,7 +384,7 @@ block_gemm_kernel(const uint8_t *__restrict__ w, const float *__restrict__ w_sca
     uint32_t past = 0;                                    // by rows of 16
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-        float sum = 0.0f;                                 // finite if all are (and below 2^64)
+        float sum = 0.0f;                                 // finite if all are, and below 2^63
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
